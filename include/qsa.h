@@ -410,6 +410,126 @@ QSA_API int qsa_sparse_attention_noalloc(const qsa_cache_t* cache, const void* q
                                  const int32_t* count, int32_t k, float scale, int32_t chunk_units, void* out,
                                  float* lse, int32_t* dev_status, void* stream);
 
+/*
+ * The calls below serve layers that attend to everything they hold (dense
+ * layers next to sparse ones, or a cache kept to a budget instead of being
+ * selected from): rotary positions for the rows that go into the cache, the
+ * attention of one token over the whole cache, and eviction from it.  The pages
+ * have no counterpart to them.
+ *
+ * qsa_rope -- rotary positions with one to three axes (time, height, width for
+ * images and video), applied to up to QSA_ROPE_MAX_TENSORS tensors of the same
+ * n tokens (say q, k, the indexer's q and k) in one launch.
+ * Pair i < rot_dim / 2 of every head turns by pos[axis[i]][token] * freq[i]
+ * radians (the angle reduced in fp64):
+ *   y0 = x0 cos - x1 sin;  y1 = x1 cos + x0 sin
+ * in fp32, rounded once to BF16.  The pair is dims (i, i + rot_dim / 2), or
+ * (2i, 2i + 1) when `adjacent`.  Dims rot_dim .. head_dim - 1 are copied.
+ *   plan    host memory, read during the call: rot_dim a multiple of 16, 16 ..
+ *           2 * QSA_ROPE_MAX_PAIRS; num_axes 1 .. QSA_ROPE_MAX_AXES; axis[i] <
+ *           num_axes; freq[i] finite
+ *   tensors host memory: bf16 rows [n][heads][head_dim], heads and dims dense,
+ *           tokens in_stride / out_stride elements apart (multiples of 8, at
+ *           least heads * head_dim; not read when n == 1); 16-byte aligned;
+ *           head_dim a multiple of 16, rot_dim .. 256.  out may be in itself
+ *           (same stride: then only the rotated dims are touched); any other
+ *           overlap of an output with an input or output is refused.  Column
+ *           slices of one buffer (a fused projection) do not overlap.
+ *   pos     int32 [num_axes][pos_stride], pos_stride >= n; any value
+ * When an indexer call follows, qsa_append_kv has to stand between (rope,
+ * append, index): the indexer reads q_idx before it waits for the kernel before
+ * it (see the conventions above).  n = 0 is a no-op.
+ */
+#define QSA_ROPE_MAX_PAIRS 128
+#define QSA_ROPE_MAX_AXES 3
+#define QSA_ROPE_MAX_TENSORS 4
+typedef struct {
+  int32_t rot_dim;
+  int32_t num_axes;
+  int32_t adjacent;
+  uint8_t axis[QSA_ROPE_MAX_PAIRS];
+  double freq[QSA_ROPE_MAX_PAIRS];
+} qsa_rope_plan_t;
+typedef struct {
+  const void* in;
+  void* out;
+  int32_t heads;
+  int32_t head_dim;
+  int64_t in_stride;
+  int64_t out_stride;
+} qsa_rope_tensor_t;
+QSA_API int qsa_rope(const qsa_rope_plan_t* plan, const qsa_rope_tensor_t* tensors, int32_t num_tensors,
+             const int32_t* pos, int64_t pos_stride, int32_t n, void* stream);
+
+/*
+ * qsa_dense_decode -- attention of one token per query over all the tokens its
+ * sequence holds, 0 .. q_pos[q], split over the cache's length and joined:
+ *   z_t = scale * q[q][h] . K[t][g];  lse = log sum_t exp(z_t);
+ *   out = BF16(sum_t exp(z_t - lse) V[t][g])
+ * and, when mass_out is given, the attention weight each micro-block of each
+ * queried sequence received, added into a running total:
+ *   mass_out[s][b] = decay * mass_in[s][b]
+ *                  + sum_{queries q of s} sum_h sum_{t in block b} exp(z_t - lse)
+ * for every block b that a query of s sees (the open block too); the rest of
+ * mass_out is left as it was.  mass_out may be mass_in.
+ *   q bf16 [nq][hq][256]; out bf16 [nq][hq][256]; lse fp32 [nq][hq]
+ *   mass_in, mass_out fp32 [max_seqs][mass_ld] (both or neither), mass_ld >=
+ *   max_pages_per_seq * 16
+ *   workspace  256-byte aligned, at least qsa_dense_decode_workspace_bytes (its
+ *              contents need no preparation); calls that share one must not
+ *              overlap on the GPU, captured graphs included
+ * A query with q_seq < 0 (padding) or q_pos == -1 (no tokens) gets out = 0 and
+ * lse = -inf; so does, flagged, one whose sequence or position is out of range.
+ * The 64 tokens of a page-table miss are left out and flagged; a query left
+ * with no token gets out = 0 and lse = -inf.  Rows behind q_pos are never read
+ * into a result, whatever they hold.  Several queries of one sequence are
+ * allowed.  Splits depend on the lengths and the SM count alone: the same call
+ * gives the same bits.
+ * Requirements: hq % Hkv == 0, hq / Hkv <= 16, scale > 0; BF16 or FP8 K/V (for
+ * FP8 each q row is scaled by a power of two into FP16's range).
+ */
+QSA_API int64_t qsa_dense_decode_workspace_bytes(const qsa_cache_t* cache, int32_t nq, int32_t hq, int32_t with_mass);
+QSA_API int qsa_dense_decode(const qsa_cache_t* cache, const void* q, int32_t nq, int32_t hq, const int32_t* q_seq,
+                     const int32_t* q_pos, float scale, void* out, float* lse, const float* mass_in,
+                     float* mass_out, int64_t mass_ld, float decay, void* workspace, int64_t workspace_bytes,
+                     int32_t* dev_status, void* stream);
+
+/*
+ * qsa_evict -- cut sequences of the cache group down to `budget` complete
+ * micro-blocks, by accumulated attention weight.  A sequence of seq_len[i]
+ * tokens has nb = seq_len[i] / 4 complete blocks.  With nb > budget it keeps its
+ * first `sink` blocks, its last `recent`, and of those between the budget -
+ * sink - recent of largest mass_in (ties, -0 and +0 included: lower index; NaN
+ * below every number); otherwise all.  Kept blocks close ranks in order from
+ * block 0, the open block follows them, K/V runs and kc rows alike; the mass
+ * row moves along (mass_out[s], freed entries up to the old end set to 0;
+ * mass_out may be mass_in).  kc_partial stays as it is.  Keys keep the rotary
+ * positions they were stored with; later tokens are appended at new_len.
+ *   dst_table int32 [max_seqs][max_pages_per_seq] pages the kept blocks go to,
+ *             or NULL: in place (block_table).  Row s, page P must be block
+ *             table's own page at (s, P), or a page that holds nothing any
+ *             sequence still needs, and the rows of one call's sequences must
+ *             not share a page that is written.  Pages that the first `sink`
+ *             blocks fill are not written in place, so a shared prefix inside
+ *             them stays shared.  The caller then puts the rows into its block
+ *             table and frees pages ceil(new_len / 64) and up.
+ *   seq_ids, seq_len int32 [n]; keep int32 [n][budget] kept complete blocks,
+ *   ascending, then -1; keep_count, new_len int32 [n] (new_len may be seq_len)
+ *   workspace  256-byte aligned, at least qsa_evict_workspace_bytes; calls that
+ *              share one must not overlap on the GPU, captured graphs included
+ * An entry with seq_ids[i] < 0 is skipped; one out of range, one listed before
+ * (QSA_DEV_BAD_SEQ) or with a length out of range (QSA_DEV_BAD_POS) is refused:
+ * nothing of it moves, keep_count = 0, new_len = seq_len.  A block whose page
+ * is a table miss is lost (QSA_DEV_BAD_PAGE).  Requirements: 1 <= budget <=
+ * max_pages_per_seq * 16, sink + recent <= budget, mass_ld >=
+ * max_pages_per_seq * 16.
+ */
+QSA_API int64_t qsa_evict_workspace_bytes(const qsa_cache_t* cache, int32_t n, int32_t budget);
+QSA_API int qsa_evict(const qsa_cache_t* cache, const int32_t* dst_table, const int32_t* seq_ids, const int32_t* seq_len,
+              int32_t n, const float* mass_in, float* mass_out, int64_t mass_ld, int32_t budget, int32_t sink,
+              int32_t recent, int32_t* keep, int32_t* keep_count, int32_t* new_len, void* workspace,
+              int64_t workspace_bytes, int32_t* dev_status, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,977 @@
+// qsa_dense_decode: softmax attention of one token over every token its
+// sequence holds in the paged cache, split over the cache's length and joined;
+// on request the attention weight that each micro-block received is added into
+// a running total (the total qsa_evict selects by).
+//
+//   z_t = scale q . k_t,  lse = log sum_t exp(z_t),  o = sum_t exp(z_t - lse) v_t
+//   mass_out[s][b] = decay mass_in[s][b] + sum_{q of s} sum_h sum_{t in b} exp(z_t - lse)
+//
+// What bounds it: the K/V bytes, each read once (2 x 256 elements per token and
+// KV head).  At 16 Q heads per KV head that is 16 flop per BF16 byte, far below
+// the card's balance, so the matrix work runs on mma.sync with the 16 rows the
+// group fills; a tcgen05 tile would have 128 rows, K and V rows interleaved in
+// its operand, and an instruction floor that alone exceeds the copy time.
+//
+// Split.  A tile is 16 tokens of one (query, KV head): 4 micro-blocks, one
+// contiguous run of the page (16 KiB BF16, 8 KiB e4m3).  The tiles of all pairs,
+// query-major, form one list that the CTAs (one per SM) share evenly, so ragged
+// lengths leave no SM idle; the lengths are read on the device (no host copy of
+// q_pos).  A pair inside one CTA is written to out / lse at once; of the others
+// a CTA holds at most two pieces (its first and its last), so the partials need
+// 2 CTAs x 16 rows of workspace whatever the batch, and a second small kernel
+// joins them and adds up the weights.
+//
+// CTA = 8 consumer warps + 1 copy warp.  The copy warp resolves 32 tiles' pages
+// at once, one batch ahead, and one lane moves each tile with bulk copies into
+// an 11-stage ring (176 KiB in flight).  Each consumer warp takes whole tiles:
+// S = Q K^T, a running maximum and sum, O += P V over all 256 dims, with no
+// exchange between warps until the pair's piece ends.
+#include "qsa_common.cuh"
+
+namespace {
+
+using namespace qsa;
+
+constexpr int kWarps = 8;                       // consumer warps
+constexpr int kConsumerThreads = kWarps * 32;
+constexpr int kThreads = kConsumerThreads + 32;  // + the copy warp
+constexpr int kTile = 16;                        // tokens of a tile
+constexpr int kTileRuns = kTile / kRatio;        // 4 micro-blocks
+constexpr int kTilesPerPage = kPage / kTile;
+constexpr int kMaxCtas = 256;                    // partial slots reserved: 2 per CTA
+constexpr int kMinTiles = 8;                     // tiles a CTA takes at least: one per consumer warp
+constexpr int kQStride = kHeadDim * 2 + 16;      // Q rows 528 B apart: conflict-free 16-byte fragment reads
+constexpr int kQBytes = 16 * kQStride;
+constexpr int kCombBytes = kWarps * 16 * 64 * 4;  // one 64-dim slice of every warp's O
+constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s
+constexpr int kBarConsumers = 1;
+// The running maximum a warp subtracts may lag the true one by this much (base
+// 2), so that O is seldom rescaled: exp2 stays below 2^8, harmless in fp32 sums
+// and in the BF16 / FP16 weights, whose precision is relative.
+constexpr float kLag = 8.f;
+
+// BF16: runs lie in shared memory as in the cache (128-byte swizzled rows).
+// e4m3: rows are plain, so runs are placed 32 B apart to spread the banks.
+template <bool F8>
+struct Lay {
+  static constexpr int kRunBytes = 2 * kRatio * kHeadDim * (F8 ? 1 : 2);
+  static constexpr int kRunStride = kRunBytes + (F8 ? 32 : 0);
+  static constexpr int kStageBytes = kTileRuns * kRunStride;
+  static constexpr int kStages = F8 ? 22 : 11;
+  static constexpr int kOffQ = kStages * kStageBytes;
+  static constexpr int kOffComb = kOffQ + kQBytes;
+  static constexpr int kOffML = kOffComb + kCombBytes;          // [warp][16 rows] (m, l)
+  static constexpr int kOffScale = kOffML + kWarps * 16 * 8;    // logit scale of each row
+  static constexpr int kOffValid = kOffScale + 16 * 4;          // tokens in each stage
+  static constexpr int kOffPlan = (kOffValid + kStages * 4 + 15) & ~15;
+  static constexpr int kOffBar = kOffPlan + 64;
+  static constexpr int kOffAbort = kOffBar + 2 * kStages * 8;
+  static constexpr int kSmem = kOffAbort + 16;
+  static_assert(kSmem <= 232448, "shared memory budget");
+};
+
+struct DenseArgs {
+  const uint8_t* kv;
+  const int32_t* bt;
+  int32_t num_pages, max_seqs, mpps, hkv;
+  const __nv_bfloat16* q;
+  int32_t nq, hq, G;
+  const int32_t* q_seq;
+  const int32_t* q_pos;
+  float scale_log2;
+  int64_t* pre;     // [nq + 1] tiles before each query; pre[nq] = all
+  float* part_lse;  // [2 CTAs][G], base 2
+  float* part_o;    // [2 CTAs][G][256], normalised
+  __nv_bfloat16* out;
+  float* lse;
+  float* bsum;  // [nq][hq][max tiles][4] sums of exp2(z - bmax) per micro-block, or null
+  float* bmax;  // [nq][hq][max tiles]
+  int32_t ctas;
+  int32_t* st;
+};
+
+// Tokens query q attends to; 0 for a padding row (q_seq < 0), an empty context
+// (q_pos == -1) and, flagged, for a sequence or position out of range.
+__device__ __forceinline__ int query_len(const DenseArgs& a, int q, bool report) {
+  const int seq = a.q_seq[q], p = a.q_pos[q];
+  if (seq < 0 || p == -1) return 0;
+  if (seq >= a.max_seqs) {
+    if (report) flag(a.st, QSA_DEV_BAD_SEQ);
+    return 0;
+  }
+  if (p < 0 || (int64_t)p >= (int64_t)a.mpps * kPage) {
+    if (report) flag(a.st, QSA_DEV_BAD_POS);
+    return 0;
+  }
+  return p + 1;
+}
+
+__device__ __forceinline__ int tiles_of(int len) { return (len + kTile - 1) / kTile; }
+
+// CTAs that share T tiles, and the first tile of CTA c's share.
+__host__ __device__ __forceinline__ int ctas_used(int64_t T, int ctas) {
+  const int64_t want = (T + kMinTiles - 1) / kMinTiles;
+  return want < ctas ? (want < 1 ? 1 : (int)want) : ctas;
+}
+__host__ __device__ __forceinline__ int64_t share_begin(int64_t T, int n, int c) { return T * c / n; }
+// The CTA whose share holds tile t: the largest c with share_begin(c) <= t.
+__host__ __device__ __forceinline__ int share_of(int64_t T, int n, int64_t t) {
+  int c = (int)(((t + 1) * n - 1) / T);
+  return c;
+}
+
+// A CTA's position in the tile list.
+struct Walk {
+  int q, g;       // pair
+  int len;        // tokens of the query
+  int seq;
+  int t0, t1;     // tiles of the pair in this CTA
+  int64_t begin;  // global index of the pair's first tile
+};
+
+// The piece at or after global tile x (x inside query q's tiles, which begin at qbegin).
+__device__ __forceinline__ void load_piece(const DenseArgs& a, Walk& w, int64_t x, int64_t x1) {
+  const int nt = tiles_of(w.len);
+  const int64_t qbegin = w.begin;  // on entry: the query's first tile
+  w.g = (int)((x - qbegin) / nt);
+  w.begin = qbegin + (int64_t)w.g * nt;
+  w.t0 = (int)(x - w.begin);
+  w.t1 = (int)min((int64_t)nt, x1 - w.begin);
+}
+
+// Step to the next piece; false at the end of the share.
+__device__ __forceinline__ bool next_piece(const DenseArgs& a, Walk& w, int64_t x1) {
+  const int nt = tiles_of(w.len);
+  const int64_t x = w.begin + w.t1;
+  if (x >= x1) return false;
+  if (w.g + 1 < a.hkv) {
+    ++w.g;
+    w.begin += nt;
+  } else {
+    do {
+      ++w.q;
+      w.len = query_len(a, w.q, false);
+    } while (w.len == 0);
+    w.seq = a.q_seq[w.q];
+    w.g = 0;
+    w.begin = x;
+  }
+  w.t0 = 0;
+  w.t1 = (int)min((int64_t)tiles_of(w.len), x1 - w.begin);
+  return true;
+}
+
+// Bounded wait; false (and the abort flag) when the limit passed.
+__device__ __forceinline__ bool wait_bar(const DenseArgs& a, uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = global_timer_ns();
+  for (uint32_t it = 0;; ++it) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((it & 255u) == 255u) {
+      if (*abort_flag) return false;
+      if (global_timer_ns() - t0 > kWaitLimitNs) {
+        flag(a.st, QSA_DEV_TIMEOUT);
+        *abort_flag = 1;
+        return false;
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------------------ copy warp
+
+template <bool F8>
+__device__ void copy_warp(const DenseArgs& a, uint8_t* smem, Walk w, int64_t x1) {
+  using LY = Lay<F8>;
+  const int lane = threadIdx.x & 31;
+  const uint32_t ring = smem_u32(smem);
+  const uint32_t full = smem_u32(smem + LY::kOffBar), empty = full + LY::kStages * 8;
+  int* valid = reinterpret_cast<int*>(smem + LY::kOffValid);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + LY::kOffAbort);
+  const uint64_t policy = l2_policy_evict_first();
+  int64_t T = 0;
+  bool more = true, stop = false;
+  while (more && !stop) {
+    // pages of 32 tiles at a time, the next batch's loads issued before this batch's copies
+    int tb = w.t0;
+    auto lookup = [&](int t) {
+      int page = -1;
+      if (t < w.t1) page = __ldg(a.bt + (int64_t)w.seq * a.mpps + t / kTilesPerPage);
+      return page;
+    };
+    int page = lookup(tb + lane);
+    while (tb < w.t1 && !stop) {
+      const int page_next = lookup(tb + 32 + lane);
+      const int n = min(32, w.t1 - tb);
+      const bool bad = lane < n && (page < 0 || page >= a.num_pages);
+      if (bad) flag(a.st, QSA_DEV_BAD_PAGE);
+      for (int i = 0; i < n; ++i, ++T) {
+        const int pg = __shfl_sync(0xffffffffu, bad ? -1 : page, i);
+        const int stage = (int)(T % LY::kStages);
+        int ok = 1;
+        if (lane == 0) {
+          if (T >= LY::kStages)
+            ok = wait_bar(a, empty + stage * 8, (uint32_t)((T / LY::kStages - 1) & 1), abort_flag);
+          if (ok) {
+            const int t = tb + i;
+            const int tok = min(kTile, w.len - t * kTile);
+            valid[stage] = pg < 0 ? 0 : tok;
+            if (pg < 0) {
+              mbar_arrive(full + stage * 8);
+            } else {
+              const int runs = (tok + kRatio - 1) / kRatio;  // whole micro-blocks that hold a token
+              const uint8_t* src = a.kv + (((size_t)pg * a.hkv + w.g) * kBlocksPerPage +
+                                           (size_t)(t % kTilesPerPage) * kTileRuns) * LY::kRunBytes;
+              const uint32_t dst = ring + stage * LY::kStageBytes;
+              mbar_arrive_expect_tx(full + stage * 8, runs * LY::kRunBytes);
+              if constexpr (F8) {
+                for (int r = 0; r < runs; ++r)
+                  bulk_g2s(dst + r * LY::kRunStride, src + r * LY::kRunBytes, LY::kRunBytes, full + stage * 8, policy);
+              } else {
+                bulk_g2s(dst, src, runs * LY::kRunBytes, full + stage * 8, policy);
+              }
+            }
+          }
+        }
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        if (!ok) {
+          stop = true;
+          break;
+        }
+      }
+      page = page_next;
+      tb += 32;
+    }
+    if (!stop) more = next_piece(a, w, x1);
+  }
+  // never leave the CTA with copies in flight
+  if (lane == 0) {
+    for (int64_t t = max((int64_t)0, T - LY::kStages); t < T; ++t) {
+      const uint64_t s0 = global_timer_ns();
+      while (!mbar_try_wait(full + (int)(t % LY::kStages) * 8, (uint32_t)((t / LY::kStages) & 1)))
+        if (global_timer_ns() - s0 > kWaitLimitNs) break;
+    }
+  }
+  __syncwarp();
+}
+
+// ------------------------------------------------------------------ consumers
+
+// Which token of the tile a lane's logits and V rows belong to.  Columns n = 2tq + e
+// of S's n-tile j (lane tq of each quad holds e = 0, 1):
+//   BF16: micro-block 2j + e, row tq ^ e.  K's column n then reads row (n >> 1) ^ (n & 1):
+//         neighbouring columns read rows of different parity, whose swizzled chunks
+//         fall into different banks; V's four quad lanes read four different rows.
+//   e4m3: micro-block (tq + 2e) & 3, row 2j + e: the quad's lanes read four different
+//         runs, 32 B apart in bank space.
+template <bool F8>
+__device__ __forceinline__ int tile_run(int j, int tq, int e) {
+  return F8 ? ((tq + 2 * e) & 3) : 2 * j + e;
+}
+template <bool F8>
+__device__ __forceinline__ int tile_row(int j, int tq, int e) {
+  return F8 ? 2 * j + e : (tq ^ e);
+}
+
+template <bool F8>
+__device__ void consumers(const DenseArgs& a, uint8_t* smem, Walk w, int64_t T_all, int64_t x0, int64_t x1) {
+  using LY = Lay<F8>;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int gq = lane >> 2, tq = lane & 3;
+  const uint32_t ring = smem_u32(smem), qb = smem_u32(smem + LY::kOffQ);
+  const uint32_t full = smem_u32(smem + LY::kOffBar), empty = full + LY::kStages * 8;
+  const volatile int* valid = reinterpret_cast<const volatile int*>(smem + LY::kOffValid);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + LY::kOffAbort);
+  float* comb = reinterpret_cast<float*>(smem + LY::kOffComb);
+  float2* ml = reinterpret_cast<float2*>(smem + LY::kOffML);
+  float* row_scale = reinterpret_cast<float*>(smem + LY::kOffScale);
+  const int G = a.G;
+  const int64_t max_tiles = (int64_t)a.mpps * kTilesPerPage;
+
+  // K: column n = gq of n-tile j, V: this lane's tokens (j, e)
+  const int ke = gq & 1, kt = gq >> 1;
+  uint32_t k_off[2], v_off[2][2];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int kr = tile_row<F8>(j, kt, ke);
+    k_off[j] = tile_run<F8>(j, kt, ke) * LY::kRunStride + kr * (F8 ? 256 : 128);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int r = tile_row<F8>(j, tq, e);
+      // BF16: V row 4 + r of the run, chunk (gq >> 1) + 4 (gq & 1) of each 64-dim atom; e4m3: 16-dim chunk gq
+      v_off[j][e] = tile_run<F8>(j, tq, e) * LY::kRunStride +
+                    (F8 ? 1024 + r * 256 + gq * 16
+                        : (4 + r) * 128 + ((((gq >> 1) + 4 * (gq & 1)) ^ (4 + r)) << 4));
+    }
+  }
+  const int kr0 = tile_row<F8>(0, kt, ke);  // BF16: the row, for the chunk swizzle
+
+  int64_t T_base = 0;
+  for (;;) {
+    const int n_tiles = w.t1 - w.t0;
+    // ---- Q rows of the group (rows beyond it are zero).  e4m3 K/V takes FP16 operands:
+    // each row is scaled by a power of two into FP16's range (exact down to 2^-38 of its
+    // largest element) and its logit scale takes the factor back.
+#pragma unroll
+    for (int it = 0; it < 2; ++it) {
+      const int row = warp + 8 * it;
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (row < G) v = ldg_nc(a.q + ((size_t)w.q * a.hq + (size_t)w.g * G + row) * kHeadDim + lane * 8);
+      float sc = a.scale_log2;
+      if constexpr (F8) {
+        uint32_t x[4] = {v.x, v.y, v.z, v.w};
+        uint32_t mx = 0;  // largest magnitude, as ordered bits
+#pragma unroll
+        for (int e = 0; e < 4; ++e) mx = max(mx, max(x[e] & 0x7fffu, (x[e] >> 16) & 0x7fffu));
+        mx = __reduce_max_sync(0xffffffffu, mx);
+        const int ex = (int)(mx >> 7);  // biased exponent
+        const int up = (ex == 0 || ex == 255) ? 0 : max(-100, min(100, 127 + 13 - ex));
+        const float f = __uint_as_float((uint32_t)(127 + up) << 23);
+        sc *= __uint_as_float((uint32_t)(127 - up) << 23);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const __half2 h = __floats2half2_rn(__uint_as_float(x[e] << 16) * f, __uint_as_float(x[e] & 0xffff0000u) * f);
+          x[e] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+        v = make_uint4(x[0], x[1], x[2], x[3]);
+      }
+      sts128(qb + row * kQStride + lane * 16, v);
+      if (lane == 0) row_scale[row] = sc;
+    }
+    named_bar_sync(kBarConsumers, kConsumerThreads);
+    const float sc0 = row_scale[gq], sc1 = row_scale[gq + 8];
+
+    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+    float o[32][4];
+#pragma unroll
+    for (int nt = 0; nt < 32; ++nt) o[nt][0] = o[nt][1] = o[nt][2] = o[nt][3] = 0.f;
+
+    for (int ti = warp; ti < n_tiles; ti += kWarps) {
+      const int64_t T = T_base + ti;
+      const int stage = (int)(T % LY::kStages);
+      const bool got = !*abort_flag && wait_bar(a, full + stage * 8, (uint32_t)((T / LY::kStages) & 1), abort_flag);
+      __syncwarp();
+      if (!__all_sync(0xffffffffu, got)) break;
+      const int nv = valid[stage];
+      const uint32_t kb = ring + stage * LY::kStageBytes;
+
+      // ---- S = Q K^T, two n-tiles of 8 tokens
+      float s[2][4];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.f;
+      if constexpr (F8) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {  // 64 dims: lane tq holds dims 64i + 16tq .. + 15
+          const uint32_t qo = (4 * i + tq) * 32;
+          const uint4 qa0 = lds128(qb + gq * kQStride + qo), qa1 = lds128(qb + gq * kQStride + qo + 16);
+          const uint4 qc0 = lds128(qb + (gq + 8) * kQStride + qo), qc1 = lds128(qb + (gq + 8) * kQStride + qo + 16);
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const uint4 kk = lds128(kb + k_off[j] + (4 * i + tq) * 16);
+            const uint4 k0 = e4m3x8_to_f16x8(make_uint2(kk.x, kk.y)), k1 = e4m3x8_to_f16x8(make_uint2(kk.z, kk.w));
+            mma_f16_16816(s[j], qa0.x, qc0.x, qa0.y, qc0.y, k0.x, k0.y);
+            mma_f16_16816(s[j], qa0.z, qc0.z, qa0.w, qc0.w, k0.z, k0.w);
+            mma_f16_16816(s[j], qa1.x, qc1.x, qa1.y, qc1.y, k1.x, k1.y);
+            mma_f16_16816(s[j], qa1.z, qc1.z, qa1.w, qc1.w, k1.z, k1.w);
+          }
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {  // 32 dims of atom i / 2: lane tq holds chunk 2tq + i % 2
+          const int ch = 2 * tq + (i & 1);
+          const uint4 qa = lds128(qb + gq * kQStride + (8 * (i >> 1) + ch) * 16);
+          const uint4 qc = lds128(qb + (gq + 8) * kQStride + (8 * (i >> 1) + ch) * 16);
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const uint4 kk = lds128(kb + k_off[j] + (i >> 1) * 1024 + ((ch ^ kr0) << 4));
+            mma_bf16_16816(s[j], qa.x, qc.x, qa.y, qc.y, kk.x, kk.y);
+            mma_bf16_16816(s[j], qa.z, qc.z, qa.w, qc.w, kk.z, kk.w);
+          }
+        }
+      }
+      // ---- mask, running maximum and sum (base 2)
+      bool ok[2][2];
+      float r0 = -INFINITY, r1 = -INFINITY;
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          ok[j][e] = tile_run<F8>(j, tq, e) * kRatio + tile_row<F8>(j, tq, e) < nv;
+          s[j][e] = ok[j][e] ? s[j][e] * sc0 : -INFINITY;
+          s[j][2 + e] = ok[j][e] ? s[j][2 + e] * sc1 : -INFINITY;
+          r0 = fmaxf(r0, s[j][e]);
+          r1 = fmaxf(r1, s[j][2 + e]);
+        }
+      r0 = fmaxf(r0, __shfl_xor_sync(0xffffffffu, r0, 1));
+      r1 = fmaxf(r1, __shfl_xor_sync(0xffffffffu, r1, 1));
+      r0 = fmaxf(r0, __shfl_xor_sync(0xffffffffu, r0, 2));
+      r1 = fmaxf(r1, __shfl_xor_sync(0xffffffffu, r1, 2));
+      const bool up0 = r0 > m0 + kLag, up1 = r1 > m1 + kLag;  // -inf + 8 = -inf: the first logit always moves it
+      if (__any_sync(0xffffffffu, up0 || up1)) {
+        const float n0 = up0 ? r0 : m0, n1 = up1 ? r1 : m1;
+        const float al0 = up0 ? exp2f(m0 - n0) : 1.f, al1 = up1 ? exp2f(m1 - n1) : 1.f;
+        m0 = n0;
+        m1 = n1;
+        l0 *= al0;
+        l1 *= al1;
+#pragma unroll
+        for (int nt = 0; nt < 32; ++nt) {
+          o[nt][0] *= al0;
+          o[nt][1] *= al0;
+          o[nt][2] *= al1;
+          o[nt][3] *= al1;
+        }
+      }
+      // rows that have seen no token yet keep every logit at -inf
+      const float sub0 = m0 == -INFINITY ? 0.f : m0, sub1 = m1 == -INFINITY ? 0.f : m1;
+      float p[2][4];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        p[j][0] = exp2f(s[j][0] - sub0);
+        p[j][1] = exp2f(s[j][1] - sub0);
+        p[j][2] = exp2f(s[j][2] - sub1);
+        p[j][3] = exp2f(s[j][3] - sub1);
+      }
+      l0 += (p[0][0] + p[0][1]) + (p[1][0] + p[1][1]);
+      l1 += (p[0][2] + p[0][3]) + (p[1][2] + p[1][3]);
+
+      // ---- weight of each micro-block: sums over its 4 tokens, one per quad lane
+      if (a.bsum) {
+        float b0, b1;
+        if constexpr (F8) {  // lane tq has rows 0, 2 of run tq and rows 1, 3 of run tq ^ 2
+          b0 = p[0][0] + p[1][0] + __shfl_xor_sync(0xffffffffu, p[0][1] + p[1][1], 2);
+          b1 = p[0][2] + p[1][2] + __shfl_xor_sync(0xffffffffu, p[0][3] + p[1][3], 2);
+        } else {  // run 2j + e over the quad: halve the runs a lane carries twice
+          const bool hi = tq & 2, odd = tq & 1;
+          const float a0 = (hi ? p[1][0] : p[0][0]) + __shfl_xor_sync(0xffffffffu, hi ? p[0][0] : p[1][0], 2);
+          const float a1 = (hi ? p[1][1] : p[0][1]) + __shfl_xor_sync(0xffffffffu, hi ? p[0][1] : p[1][1], 2);
+          const float c0 = (hi ? p[1][2] : p[0][2]) + __shfl_xor_sync(0xffffffffu, hi ? p[0][2] : p[1][2], 2);
+          const float c1 = (hi ? p[1][3] : p[0][3]) + __shfl_xor_sync(0xffffffffu, hi ? p[0][3] : p[1][3], 2);
+          b0 = (odd ? a1 : a0) + __shfl_xor_sync(0xffffffffu, odd ? a0 : a1, 1);
+          b1 = (odd ? c1 : c0) + __shfl_xor_sync(0xffffffffu, odd ? c0 : c1, 1);
+        }
+        const int64_t base = ((int64_t)w.q * a.hq + (int64_t)w.g * G) * max_tiles + w.t0 + ti;
+        if (gq < G) {
+          const int64_t at = base + gq * max_tiles;
+          a.bsum[at * 4 + tq] = b0;
+          if (tq == 0) a.bmax[at] = m0;
+        }
+        if (gq + 8 < G) {
+          const int64_t at = base + (gq + 8) * max_tiles;
+          a.bsum[at * 4 + tq] = b1;
+          if (tq == 0) a.bmax[at] = m1;
+        }
+      }
+
+      // ---- O += P V.  BF16 V: the weights enter as a BF16 hi + lo pair (about 17
+      // significant bits; 8 alone would show in short contexts).  e4m3 V: FP16 weights,
+      // 11 bits against the cache's 4.
+      uint32_t pa[4], pl[4];
+      if constexpr (F8) {
+        pa[0] = pack_f16_sat(p[0][0], p[0][1]);
+        pa[1] = pack_f16_sat(p[0][2], p[0][3]);
+        pa[2] = pack_f16_sat(p[1][0], p[1][1]);
+        pa[3] = pack_f16_sat(p[1][2], p[1][3]);
+      } else {
+        split_bf16(p[0][0], p[0][1], pa[0], pl[0]);
+        split_bf16(p[0][2], p[0][3], pa[1], pl[1]);
+        split_bf16(p[1][0], p[1][1], pa[2], pl[2]);
+        split_bf16(p[1][2], p[1][3], pa[3], pl[3]);
+      }
+      const bool whole = nv == kTile;
+      constexpr int kSlices = F8 ? 2 : 4;  // e4m3: 128 dims per 16-byte read of the 8 column groups; BF16: 64
+#pragma unroll
+      for (int c = 0; c < kSlices; ++c) {
+        uint4 x[2][2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            x[j][e] = lds128(kb + v_off[j][e] + c * (F8 ? 128 : 1024));
+            if (!whole && !ok[j][e]) x[j][e] = make_uint4(0, 0, 0, 0);  // rows behind the end may hold anything
+          }
+        const uint32_t x00[4] = {x[0][0].x, x[0][0].y, x[0][0].z, x[0][0].w};
+        const uint32_t x01[4] = {x[0][1].x, x[0][1].y, x[0][1].z, x[0][1].w};
+        const uint32_t x10[4] = {x[1][0].x, x[1][0].y, x[1][0].z, x[1][0].w};
+        const uint32_t x11[4] = {x[1][1].x, x[1][1].y, x[1][1].z, x[1][1].w};
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          if constexpr (F8) {  // 4 dims: the two tokens' bytes are paired, then widened
+            const uint2 t0 = e4m3x4_to_f16x4(__byte_perm(x00[r], x01[r], 0x5140));
+            const uint2 t1 = e4m3x4_to_f16x4(__byte_perm(x00[r], x01[r], 0x7362));
+            const uint2 u0 = e4m3x4_to_f16x4(__byte_perm(x10[r], x11[r], 0x5140));
+            const uint2 u1 = e4m3x4_to_f16x4(__byte_perm(x10[r], x11[r], 0x7362));
+            mma_f16_16816(o[c * 16 + 4 * r + 0], pa[0], pa[1], pa[2], pa[3], t0.x, u0.x);
+            mma_f16_16816(o[c * 16 + 4 * r + 1], pa[0], pa[1], pa[2], pa[3], t0.y, u0.y);
+            mma_f16_16816(o[c * 16 + 4 * r + 2], pa[0], pa[1], pa[2], pa[3], t1.x, u1.x);
+            mma_f16_16816(o[c * 16 + 4 * r + 3], pa[0], pa[1], pa[2], pa[3], t1.y, u1.y);
+          } else {
+            const uint32_t lo0 = __byte_perm(x00[r], x01[r], 0x5410), hi0 = __byte_perm(x00[r], x01[r], 0x7632);
+            const uint32_t lo1 = __byte_perm(x10[r], x11[r], 0x5410), hi1 = __byte_perm(x10[r], x11[r], 0x7632);
+            mma_bf16_16816(o[c * 8 + 2 * r], pa[0], pa[1], pa[2], pa[3], lo0, lo1);
+            mma_bf16_16816(o[c * 8 + 2 * r + 1], pa[0], pa[1], pa[2], pa[3], hi0, hi1);
+            mma_bf16_16816(o[c * 8 + 2 * r], pl[0], pl[1], pl[2], pl[3], lo0, lo1);
+            mma_bf16_16816(o[c * 8 + 2 * r + 1], pl[0], pl[1], pl[2], pl[3], hi0, hi1);
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(empty + stage * 8);
+    }
+    T_base += n_tiles;
+
+    // ---- join the warps' (m, l, O)
+    l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
+    l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
+    l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
+    l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
+    if (tq == 0) {
+      ml[warp * 16 + gq] = make_float2(m0, l0);
+      ml[warp * 16 + gq + 8] = make_float2(m1, l1);
+    }
+    named_bar_sync(kBarConsumers, kConsumerThreads);
+    const int nw = min(kWarps, n_tiles);  // warps that had a tile
+    float fac[2], lse2[2];
+#pragma unroll
+    for (int hr = 0; hr < 2; ++hr) {
+      const int row = gq + 8 * hr;
+      float M = -INFINITY, L = 0.f;
+      for (int v = 0; v < nw; ++v) M = fmaxf(M, ml[v * 16 + row].x);
+      fac[hr] = 0.f;
+      lse2[hr] = -INFINITY;
+      if (M != -INFINITY) {
+        for (int v = 0; v < nw; ++v) L += ml[v * 16 + row].y * exp2f(ml[v * 16 + row].x - M);
+        fac[hr] = exp2f((hr ? m1 : m0) - M) / L;
+        lse2[hr] = M + log2f(L);
+      }
+    }
+    // whole pair here: straight to out; else to this CTA's first or last partial slot
+    const int nt_pair = tiles_of(w.len);
+    const bool direct = w.t0 == 0 && w.t1 == nt_pair;
+    const int slot = 2 * blockIdx.x + (w.begin > x0 ? 1 : 0);
+    if (warp == 0 && tq == 0) {
+#pragma unroll
+      for (int hr = 0; hr < 2; ++hr) {
+        const int row = gq + 8 * hr;
+        if (row < G) {
+          if (direct)
+            a.lse[(size_t)w.q * a.hq + (size_t)w.g * G + row] = lse2[hr] * 0.69314718055994530942f;
+          else
+            a.part_lse[(size_t)slot * G + row] = lse2[hr];
+        }
+      }
+    }
+    // 64 dims at a time: every warp's slice to shared memory, then one float4 per thread
+#pragma unroll
+    for (int sl = 0; sl < 4; ++sl) {
+      if (warp < nw) {
+        float* dst = comb + warp * 16 * 64;
+#pragma unroll
+        for (int hr = 0; hr < 2; ++hr)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              // BF16: n-tile 8sl + i holds, in column 2tq + e, dim 64sl + 32e + 8tq + i;
+              // e4m3: n-tile 16 (sl >> 1) + i, column 2tq + e, dim 128 (sl >> 1) + 32tq + 16e + i:
+              // slice sl then takes i = 8 (sl & 1) .. + 7 of every column
+              const int i0 = F8 ? 16 * (sl >> 1) + 8 * (sl & 1) + 4 * k : 8 * sl + 4 * k;
+              const int cc = 2 * hr + e;
+              const int col = (F8 ? 16 * tq + 8 * e : 32 * e + 8 * tq) + 4 * k;
+              *reinterpret_cast<float4*>(dst + (gq + 8 * hr) * 64 + col) =
+                  make_float4(o[i0][cc] * fac[hr], o[i0 + 1][cc] * fac[hr], o[i0 + 2][cc] * fac[hr],
+                              o[i0 + 3][cc] * fac[hr]);
+            }
+      }
+      named_bar_sync(kBarConsumers, kConsumerThreads);
+      const int row = tid >> 4, col = (tid & 15) * 4;
+      if (row < G) {
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int v = 0; v < nw; ++v) {
+          const float4 y = *reinterpret_cast<const float4*>(comb + (v * 16 + row) * 64 + col);
+          acc.x += y.x;
+          acc.y += y.y;
+          acc.z += y.z;
+          acc.w += y.w;
+        }
+        const int dim = F8 ? 128 * (sl >> 1) + 16 * (col >> 3) + 8 * (sl & 1) + (col & 7) : 64 * sl + col;
+        if (direct) {
+          uint2 v2;
+          v2.x = pack_bf16(acc.x, acc.y);
+          v2.y = pack_bf16(acc.z, acc.w);
+          *reinterpret_cast<uint2*>(a.out + ((size_t)w.q * a.hq + (size_t)w.g * G + row) * kHeadDim + dim) = v2;
+        } else {
+          *reinterpret_cast<float4*>(a.part_o + ((size_t)slot * G + row) * kHeadDim + dim) = acc;
+        }
+      }
+      named_bar_sync(kBarConsumers, kConsumerThreads);
+    }
+    if (!next_piece(a, w, x1)) break;
+  }
+}
+
+template <bool F8>
+__global__ void __launch_bounds__(kThreads, 1) dense_decode_kernel(DenseArgs a) {
+  using LY = Lay<F8>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  pdl_launch_dependents();
+  int64_t* plan = reinterpret_cast<int64_t*>(smem + LY::kOffPlan);
+  // warp 0 sets the pipeline up, the others wait for the previous kernel meanwhile
+  if (tid == 0) {
+    const uint32_t bars = smem_u32(smem + LY::kOffBar);
+    for (int i = 0; i < 2 * LY::kStages; ++i) mbar_init(bars + i * 8, 1);
+    fence_mbar_init();
+    *reinterpret_cast<volatile int*>(smem + LY::kOffAbort) = 0;
+  }
+  pdl_wait_previous();
+  // ---- the share of this CTA: tiles of every query, summed by one warp
+  if (warp == 0) {
+    int64_t total = 0;
+    for (int b = 0; b < a.nq; b += 32) {
+      const int q = b + lane;
+      int64_t n = q < a.nq ? (int64_t)tiles_of(query_len(a, q, blockIdx.x == 0)) * a.hkv : 0;
+      int64_t inc = n;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, inc, d);
+        if (lane >= d) inc += y;
+      }
+      if (blockIdx.x == 0 && q < a.nq) a.pre[q] = total + inc - n;
+      total += __shfl_sync(0xffffffffu, inc, 31);
+    }
+    if (blockIdx.x == 0 && lane == 0) a.pre[a.nq] = total;
+    const int used = ctas_used(total, a.ctas);
+    int64_t x0 = 0, x1 = 0;
+    if (total > 0 && (int)blockIdx.x < used) {
+      x0 = share_begin(total, used, blockIdx.x);
+      x1 = share_begin(total, used, blockIdx.x + 1);
+    }
+    // the query that holds tile x0
+    int64_t before = 0;
+    for (int b = 0; b < a.nq && x0 < x1; b += 32) {
+      const int q = b + lane;
+      const int len = q < a.nq ? query_len(a, q, false) : 0;
+      const int64_t n = (int64_t)tiles_of(len) * a.hkv;
+      int64_t inc = n;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, inc, d);
+        if (lane >= d) inc += y;
+      }
+      const int64_t first = before + inc - n;
+      if (n > 0 && first <= x0 && x0 < first + n) {
+        plan[2] = q;
+        plan[3] = first;
+        plan[4] = len;
+        plan[5] = a.q_seq[q];
+      }
+      before += __shfl_sync(0xffffffffu, inc, 31);
+      if (before > x0) break;
+    }
+    if (lane == 0) {
+      plan[0] = x0;
+      plan[1] = x1;
+      plan[6] = total;
+    }
+  }
+  __syncthreads();
+  const int64_t x0 = plan[0], x1 = plan[1];
+  if (x0 >= x1) return;
+  Walk w;
+  w.q = (int)plan[2];
+  w.begin = plan[3];
+  w.len = (int)plan[4];
+  w.seq = (int)plan[5];
+  load_piece(a, w, x0, x1);
+  if (warp < kWarps)
+    consumers<F8>(a, smem, w, plan[6], x0, x1);
+  else
+    copy_warp<F8>(a, smem, w, x1);
+}
+
+// ------------------------------------------------------------------ join + weights
+
+constexpr int kJoinThreads = 256;
+
+struct JoinArgs {
+  DenseArgs d;
+  const float* mass_in;
+  float* mass_out;
+  int64_t mass_ld;
+  float decay;
+  int32_t mass_blocks;  // CTAs per query for the weights
+};
+
+// CTAs of pair (q, g): shares first .. last, and the partial slot of share c.
+struct Pieces {
+  int64_t begin;
+  int64_t T;
+  int n, first, last;
+};
+
+__device__ __forceinline__ Pieces pieces_of(const DenseArgs& a, int q, int g) {
+  Pieces r;
+  const int64_t b0 = a.pre[q], b1 = a.pre[q + 1];
+  r.T = a.pre[a.nq];
+  const int64_t nt = (b1 - b0) / a.hkv;
+  r.begin = b0 + nt * g;
+  if (nt == 0) {
+    r.n = 0;
+    r.first = 0;
+    r.last = -1;
+    return r;
+  }
+  r.n = ctas_used(r.T, a.ctas);
+  r.first = share_of(r.T, r.n, r.begin);
+  r.last = share_of(r.T, r.n, r.begin + nt - 1);
+  return r;
+}
+
+__device__ __forceinline__ int slot_of(const Pieces& p, int c) {
+  return 2 * c + (p.begin > share_begin(p.T, p.n, c) ? 1 : 0);
+}
+
+// Base-2 lse of (q, h), by one warp: the joined pieces' or, for a pair that one
+// CTA held, the one already in lse.
+__device__ __forceinline__ float joined_lse2(const DenseArgs& a, int q, int h) {
+  const int lane = threadIdx.x & 31;
+  const Pieces p = pieces_of(a, q, h / a.G);
+  if (p.last < p.first) return -INFINITY;
+  if (p.first == p.last) return a.lse[(size_t)q * a.hq + h] * 1.44269504088896340736f;
+  const int row = h % a.G;
+  float M = -INFINITY;
+  for (int c = p.first + lane; c <= p.last; c += 32) M = fmaxf(M, a.part_lse[(size_t)slot_of(p, c) * a.G + row]);
+#pragma unroll
+  for (int d = 16; d; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+  if (M == -INFINITY) return -INFINITY;
+  float L = 0.f;
+  for (int c = p.first + lane; c <= p.last; c += 32) L += exp2f(a.part_lse[(size_t)slot_of(p, c) * a.G + row] - M);
+#pragma unroll
+  for (int d = 16; d; d >>= 1) L += __shfl_xor_sync(0xffffffffu, L, d);
+  return M + log2f(L);
+}
+
+// Blocks 0 .. nq*hq-1: one (query, head) each; the pieces are spread over 4
+// groups of 64 threads (4 dims each) and summed in a fixed order.  The blocks
+// after them: 256 tiles (1,024 micro-blocks) of one query's sequence each.
+__global__ void __launch_bounds__(kJoinThreads) dense_join_kernel(JoinArgs ja) {
+  const DenseArgs& a = ja.d;
+  pdl_launch_dependents();
+  pdl_wait_previous();
+  const int tid = threadIdx.x;
+  __shared__ float4 acc_s[4][64];
+  __shared__ float lse_s[kMaxCtas];
+  const int64_t n_join = (int64_t)a.nq * a.hq;
+  if (blockIdx.x < n_join) {
+    const int q = (int)(blockIdx.x / a.hq), h = (int)(blockIdx.x % a.hq);
+    const Pieces p = pieces_of(a, q, h / a.G);
+    if (p.last >= p.first && p.first == p.last) return;  // written by its CTA
+    const int grp = tid >> 6, c4 = tid & 63;
+    uint2 o = make_uint2(0, 0);
+    float lse = -INFINITY;
+    if (p.last > p.first) {
+      const int n = p.last - p.first + 1, row = h % a.G;
+      for (int i = tid; i < n; i += kJoinThreads) lse_s[i] = a.part_lse[(size_t)slot_of(p, p.first + i) * a.G + row];
+      __syncthreads();
+      float M = -INFINITY;
+      for (int i = 0; i < n; ++i) M = fmaxf(M, lse_s[i]);
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      float L = 0.f;
+      if (M != -INFINITY) {
+        for (int i = 0; i < n; ++i) L += exp2f(lse_s[i] - M);
+#pragma unroll 4
+        for (int i = grp; i < n; i += 4) {
+          const float e = exp2f(lse_s[i] - M);  // 0 for an empty piece, whose row is zero
+          const float4 x = reinterpret_cast<const float4*>(
+              a.part_o + ((size_t)slot_of(p, p.first + i) * a.G + row) * kHeadDim)[c4];
+          acc.x += e * x.x;
+          acc.y += e * x.y;
+          acc.z += e * x.z;
+          acc.w += e * x.w;
+        }
+      }
+      acc_s[grp][c4] = acc;
+      __syncthreads();
+      if (grp == 0 && M != -INFINITY) {
+        const float inv = 1.f / L;
+        float4 r = acc_s[0][c4];
+#pragma unroll
+        for (int k = 1; k < 4; ++k) {
+          r.x += acc_s[k][c4].x;
+          r.y += acc_s[k][c4].y;
+          r.z += acc_s[k][c4].z;
+          r.w += acc_s[k][c4].w;
+        }
+        o.x = pack_bf16(r.x * inv, r.y * inv);
+        o.y = pack_bf16(r.z * inv, r.w * inv);
+        lse = (M + log2f(L)) * 0.69314718055994530942f;
+      }
+    }
+    if (grp == 0) {
+      reinterpret_cast<uint2*>(a.out + (size_t)blockIdx.x * kHeadDim)[c4] = o;
+      if (c4 == 0) a.lse[blockIdx.x] = lse;
+    }
+    return;
+  }
+  // ---- weights.  The first query of a sequence adds up all of the sequence's
+  // queries in order, so the total does not depend on which block runs first.
+  const int64_t wb = blockIdx.x - n_join;
+  const int q0 = (int)(wb / ja.mass_blocks);
+  const int seq = a.q_seq[q0];
+  if (query_len(a, q0, false) == 0) return;
+  for (int q = 0; q < q0; ++q)
+    if (a.q_seq[q] == seq && query_len(a, q, false) > 0) return;
+  const int tile = (int)(wb % ja.mass_blocks) * kJoinThreads + tid;
+  const int64_t max_tiles = (int64_t)a.mpps * kTilesPerPage;
+  float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+  int longest = 0;
+  for (int q = q0; q < a.nq; ++q) {
+    const int len = query_len(a, q, false);
+    if (len == 0 || a.q_seq[q] != seq) continue;
+    longest = max(longest, len);
+    for (int h0 = 0; h0 < a.hq; h0 += kMaxCtas) {
+      __syncthreads();
+      for (int h = h0 + (tid >> 5); h < min(a.hq, h0 + kMaxCtas); h += kJoinThreads / 32) {
+        const float v = joined_lse2(a, q, h);
+        if ((tid & 31) == 0) lse_s[h - h0] = v;
+      }
+      __syncthreads();
+      if (tile < tiles_of(len)) {
+        for (int h = h0; h < min(a.hq, h0 + kMaxCtas); ++h) {
+          const int64_t at = ((int64_t)q * a.hq + h) * max_tiles + tile;
+          const float l2 = lse_s[h - h0], bm = a.bmax[at];
+          if (l2 == -INFINITY || bm == -INFINITY) continue;  // no token seen
+          const float f = exp2f(bm - l2);
+          const float4 b = reinterpret_cast<const float4*>(a.bsum)[at];
+          sum.x += f * b.x;
+          sum.y += f * b.y;
+          sum.z += f * b.z;
+          sum.w += f * b.w;
+        }
+      }
+    }
+  }
+  const int blocks = (longest + kRatio - 1) / kRatio;
+  const float v[4] = {sum.x, sum.y, sum.z, sum.w};
+  const int64_t row = (int64_t)seq * ja.mass_ld;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int b = tile * kTileRuns + k;
+    if (b < blocks) ja.mass_out[row + b] = ja.decay * ja.mass_in[row + b] + v[k];
+  }
+}
+
+int64_t align256(int64_t n) { return (n + 255) / 256 * 256; }
+
+struct WorkspaceMap {
+  int64_t pre, part_lse, part_o, bsum, bmax, total;
+};
+
+WorkspaceMap workspace_map(const qsa_cache_t& c, int32_t nq, int32_t hq, bool with_mass) {
+  const int64_t G = hq / c.num_kv_heads;
+  WorkspaceMap m;
+  m.pre = 0;
+  m.part_lse = align256((int64_t)(nq + 1) * 8);
+  m.part_o = m.part_lse + align256(2 * kMaxCtas * G * 4);
+  m.bsum = m.part_o + align256(2 * kMaxCtas * G * kHeadDim * 4);
+  const int64_t tiles = with_mass ? (int64_t)nq * hq * c.max_pages_per_seq * kTilesPerPage : 0;
+  m.bmax = m.bsum + align256(tiles * 16);
+  m.total = m.bmax + align256(tiles * 4);
+  return m;
+}
+
+int check_shape(const qsa_cache_t* cache, int32_t nq, int32_t hq) {
+  if (!cache || nq < 0 || hq < 1) return QSA_ERR_INVALID_ARG;
+  const qsa_cache_t& c = *cache;
+  if (c.num_pages < 1 || c.max_seqs < 1 || c.max_pages_per_seq < 1 || c.num_kv_heads < 1) return QSA_ERR_INVALID_ARG;
+  if (hq % c.num_kv_heads != 0) return QSA_ERR_INVALID_ARG;
+  if (hq / c.num_kv_heads > QSA_MAX_GROUP) return QSA_ERR_UNSUPPORTED;
+  if (c.max_pages_per_seq > 0x7fffffff / kPage) return QSA_ERR_UNSUPPORTED;  // positions are int32
+  return QSA_OK;
+}
+
+template <bool F8>
+int launch_dense(const DenseArgs& a, cudaStream_t s) {
+  // per device, once: the attribute belongs to the device's copy of the kernel
+  if (cudaFuncSetAttribute(dense_decode_kernel<F8>, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<F8>::kSmem) !=
+      cudaSuccess) {
+    (void)cudaGetLastError();
+    return QSA_ERR_CUDA;
+  }
+  return qsa_host::launch(dense_decode_kernel<F8>, dim3((unsigned)a.ctas), dim3(kThreads), (size_t)Lay<F8>::kSmem, s,
+                          a);
+}
+
+}  // namespace
+
+extern "C" int64_t qsa_dense_decode_workspace_bytes(const qsa_cache_t* cache, int32_t nq, int32_t hq,
+                                                    int32_t with_mass) {
+  const int rc = check_shape(cache, nq, hq);
+  if (rc != QSA_OK) return rc;
+  return workspace_map(*cache, nq, hq, with_mass != 0).total;
+}
+
+extern "C" int qsa_dense_decode(const qsa_cache_t* cache, const void* q, int32_t nq, int32_t hq, const int32_t* q_seq,
+                                const int32_t* q_pos, float scale, void* out, float* lse, const float* mass_in,
+                                float* mass_out, int64_t mass_ld, float decay, void* workspace,
+                                int64_t workspace_bytes, int32_t* dev_status, void* stream) {
+  const int rc = check_shape(cache, nq, hq);
+  if (rc != QSA_OK) return rc;
+  const qsa_cache_t& c = *cache;
+  if (!(scale > 0.f) || (mass_in == nullptr) != (mass_out == nullptr)) return QSA_ERR_INVALID_ARG;
+  if (c.kv_dtype != QSA_KV_BF16 && c.kv_dtype != QSA_KV_FP8_E4M3) return QSA_ERR_UNSUPPORTED;
+  if (nq == 0) return QSA_OK;
+  if (!c.kv_pages || !c.block_table || !q || !q_seq || !q_pos || !out || !lse || !workspace) return QSA_ERR_INVALID_ARG;
+  auto misaligned = [](const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) != 0; };
+  if (misaligned(c.kv_pages, 16) || misaligned(q, 16) || misaligned(out, 8) || misaligned(workspace, 256))
+    return QSA_ERR_INVALID_ARG;
+  const bool mass = mass_in != nullptr;
+  if (mass && mass_ld < (int64_t)c.max_pages_per_seq * kBlocksPerPage) return QSA_ERR_INVALID_ARG;
+  const WorkspaceMap m = workspace_map(c, nq, hq, mass);
+  if (workspace_bytes < m.total) return QSA_ERR_INVALID_ARG;
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return QSA_ERR_CUDA;
+  }
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  DenseArgs a;
+  a.kv = static_cast<const uint8_t*>(c.kv_pages);
+  a.bt = c.block_table;
+  a.num_pages = c.num_pages;
+  a.max_seqs = c.max_seqs;
+  a.mpps = c.max_pages_per_seq;
+  a.hkv = c.num_kv_heads;
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.nq = nq;
+  a.hq = hq;
+  a.G = hq / c.num_kv_heads;
+  a.q_seq = q_seq;
+  a.q_pos = q_pos;
+  a.scale_log2 = scale * 1.44269504088896340736f;
+  a.pre = reinterpret_cast<int64_t*>(ws + m.pre);
+  a.part_lse = reinterpret_cast<float*>(ws + m.part_lse);
+  a.part_o = reinterpret_cast<float*>(ws + m.part_o);
+  a.out = static_cast<__nv_bfloat16*>(out);
+  a.lse = lse;
+  a.bsum = mass ? reinterpret_cast<float*>(ws + m.bsum) : nullptr;
+  a.bmax = mass ? reinterpret_cast<float*>(ws + m.bmax) : nullptr;
+  a.ctas = sms < kMaxCtas ? sms : kMaxCtas;
+  a.st = dev_status;
+  JoinArgs j;
+  j.d = a;
+  j.mass_in = mass_in;
+  j.mass_out = mass_out;
+  j.mass_ld = mass_ld;
+  j.decay = decay;
+  const int64_t tiles = (int64_t)c.max_pages_per_seq * kTilesPerPage;
+  j.mass_blocks = (int32_t)((tiles + kJoinThreads - 1) / kJoinThreads);
+  const int64_t grid = (int64_t)nq * hq + (mass ? (int64_t)nq * j.mass_blocks : 0);
+  if (grid > 0x7fffffff) return QSA_ERR_UNSUPPORTED;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const int r = c.kv_dtype == QSA_KV_FP8_E4M3 ? launch_dense<true>(a, s) : launch_dense<false>(a, s);
+  if (r != QSA_OK) return r;
+  return qsa_host::launch(dense_join_kernel, dim3((unsigned)grid), dim3(kJoinThreads), 0, s, j);
+}

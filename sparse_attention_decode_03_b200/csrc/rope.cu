@@ -1,0 +1,178 @@
+// qsa_rope: rotary positions with one to three axes (time, height, width),
+// applied to up to four tensors of the same tokens in one launch: the main
+// queries and keys, and the indexer's, before qsa_append_kv and the attention.
+//
+// Pair i of a head (dims i and i + R/2, or 2i and 2i + 1) turns by the angle
+// pos[axis(i)] * freq(i):
+//   y0 = x0 cos - x1 sin,  y1 = x1 cos + x0 sin   (fp32, one rounding to BF16)
+// Dims R and above are copied.  The angle is reduced to one turn in 64 bits: a
+// position of a quarter-million tokens times a frequency near 1 has lost about
+// 2^-7 rad in fp32.  sin and cos of the reduced turn are taken in fp32.
+//
+// What bounds it: the bytes of the rows for a prompt chunk, launch latency for a
+// decode step.  A CTA takes kTokens tokens; it computes their R/2 angles once
+// (shared by every head), then its warps take the rows: 16 bytes per lane, a
+// half-split pair's partner chunk by shuffle.  Rows of 128 dims go two to a warp.
+#include "qsa_common.cuh"
+
+namespace {
+
+using namespace qsa;
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kTokens = 2;  // tokens of a CTA
+constexpr int kMaxPairs = QSA_ROPE_MAX_PAIRS;
+
+struct RopeArgs {
+  qsa_rope_plan_t plan;
+  qsa_rope_tensor_t t[QSA_ROPE_MAX_TENSORS];
+  int32_t num_tensors;
+  int32_t items;  // warp-sized pieces of one token's rows
+  const int32_t* pos;
+  int64_t pos_stride;
+  int32_t n;
+};
+
+__global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeArgs a) {
+  __shared__ float2 cs[kTokens][kMaxPairs];  // cos, sin
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int half = a.plan.rot_dim / 2;
+  const int64_t tok0 = (int64_t)blockIdx.x * kTokens;
+  const int ntok = (int)min((int64_t)kTokens, a.n - tok0);
+  pdl_wait_previous();
+  for (int k = tid; k < ntok * half; k += kThreads) {
+    const int i = k % half, t = k / half;
+    const int p = a.pos[a.plan.axis[i] * a.pos_stride + tok0 + t];
+    double turn = (double)p * a.plan.freq[i] * 0.15915494309189533577;  // 1 / 2 pi
+    turn -= rint(turn);
+    float s, c;
+    sincospif(2.f * (float)turn, &s, &c);
+    cs[t][i] = make_float2(c, s);
+  }
+  __syncthreads();
+  const int total = ntok * a.items;
+  for (int k = warp; k < total; k += kWarps) {
+    const int t = k / a.items;
+    int item = k % a.items, ti = 0;
+    // the tensor and row of this piece: 256-dim rows take a warp, rows of up to 128 half of one
+    int rows_per = 1, cnt = 0;
+    for (;; ++ti) {
+      rows_per = a.t[ti].head_dim <= 128 ? 2 : 1;
+      cnt = (a.t[ti].heads + rows_per - 1) / rows_per;
+      if (item < cnt) break;
+      item -= cnt;
+    }
+    const qsa_rope_tensor_t& x = a.t[ti];
+    const int lanes = 32 / rows_per;
+    const int c = lane % lanes, head = item * rows_per + lane / lanes;
+    const int rot_chunks = a.plan.rot_dim / 8;
+    const bool in_place = x.in == x.out;
+    const bool live = head < x.heads && c * 8 < x.head_dim && !(in_place && c >= rot_chunks);
+    uint4 v = make_uint4(0, 0, 0, 0);
+    const int64_t tok = tok0 + t;
+    if (live)
+      v = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(x.in) + tok * x.in_stride +
+                                          (int64_t)head * x.head_dim + c * 8);
+    uint32_t w[4] = {v.x, v.y, v.z, v.w}, r[4];
+    if (a.plan.adjacent) {
+      if (c < rot_chunks) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 k2 = cs[t][c * 4 + e];
+          const float x0 = __uint_as_float(w[e] << 16), x1 = __uint_as_float(w[e] & 0xffff0000u);
+          r[e] = pack_bf16(x0 * k2.x - x1 * k2.y, x1 * k2.x + x0 * k2.y);
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) r[e] = w[e];
+      }
+    } else {
+      const int hc = rot_chunks / 2;  // chunks of a half
+      const bool low = c < hc;
+      const int from = lane + (low ? hc : -hc);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t o = __shfl_sync(0xffffffffu, w[e], from & 31);
+        r[e] = w[e];
+        if (c < rot_chunks) {
+          const int i = (low ? c : c - hc) * 8 + 2 * e;
+          const float2 k0 = cs[t][i], k1 = cs[t][i + 1];
+          const float s0 = low ? -k0.y : k0.y, s1 = low ? -k1.y : k1.y;
+          r[e] = pack_bf16(__uint_as_float(w[e] << 16) * k0.x + __uint_as_float(o << 16) * s0,
+                           __uint_as_float(w[e] & 0xffff0000u) * k1.x + __uint_as_float(o & 0xffff0000u) * s1);
+        }
+      }
+    }
+    if (live)
+      *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(x.out) + tok * x.out_stride +
+                                (int64_t)head * x.head_dim + c * 8) = make_uint4(r[0], r[1], r[2], r[3]);
+  }
+}
+
+// n rows of `row` elements, `stride` apart.
+struct Rows {
+  uintptr_t at;
+  int64_t stride, row;
+};
+
+// Whether two sets of n rows share an element.  Rows of one stride may
+// interleave (column slices of one buffer); of different strides, sets whose
+// byte ranges cross count as overlapping.
+bool rows_overlap(const Rows& x, const Rows& y, int32_t n) {
+  const uintptr_t xe = x.at + 2 * (uintptr_t)((n - 1) * x.stride + x.row);
+  const uintptr_t ye = y.at + 2 * (uintptr_t)((n - 1) * y.stride + y.row);
+  if (xe <= y.at || ye <= x.at) return false;
+  if (n == 1 || x.stride != y.stride) return true;
+  const int64_t s = 2 * x.stride, d = (int64_t)(y.at - x.at);
+  const int64_t r = ((d % s) + s) % s;  // y's column offset from x's rows, in bytes
+  return r < 2 * x.row || r + 2 * y.row > s;
+}
+
+}  // namespace
+
+extern "C" int qsa_rope(const qsa_rope_plan_t* plan, const qsa_rope_tensor_t* tensors, int32_t num_tensors,
+                        const int32_t* pos, int64_t pos_stride, int32_t n, void* stream) {
+  if (!plan || !tensors || num_tensors < 1 || num_tensors > QSA_ROPE_MAX_TENSORS || n < 0) return QSA_ERR_INVALID_ARG;
+  if (plan->rot_dim < 16 || plan->rot_dim % 16 || plan->rot_dim > 2 * QSA_ROPE_MAX_PAIRS) return QSA_ERR_INVALID_ARG;
+  if (plan->num_axes < 1 || plan->num_axes > QSA_ROPE_MAX_AXES) return QSA_ERR_INVALID_ARG;
+  for (int i = 0; i < plan->rot_dim / 2; ++i)
+    if (plan->axis[i] >= plan->num_axes || !(plan->freq[i] - plan->freq[i] == 0.0)) return QSA_ERR_INVALID_ARG;
+  if (n == 0) return QSA_OK;
+  if (!pos || (plan->num_axes > 1 && pos_stride < n)) return QSA_ERR_INVALID_ARG;
+  RopeArgs a;
+  a.plan = *plan;
+  a.num_tensors = num_tensors;
+  a.items = 0;
+  a.pos = pos;
+  a.pos_stride = pos_stride;
+  a.n = n;
+  for (int k = 0; k < num_tensors; ++k) {
+    const qsa_rope_tensor_t& t = tensors[k];
+    if (!t.in || !t.out || t.heads < 1) return QSA_ERR_INVALID_ARG;
+    if (t.head_dim < plan->rot_dim || t.head_dim % 16 || t.head_dim > QSA_HEAD_DIM) return QSA_ERR_INVALID_ARG;
+    const int64_t row = (int64_t)t.heads * t.head_dim;
+    if (row > (1 << 24)) return QSA_ERR_UNSUPPORTED;
+    if (n > 1 && (t.in_stride < row || t.out_stride < row)) return QSA_ERR_INVALID_ARG;
+    if ((reinterpret_cast<uintptr_t>(t.in) & 15u) || (reinterpret_cast<uintptr_t>(t.out) & 15u) ||
+        (n > 1 && ((t.in_stride & 7) || (t.out_stride & 7))))
+      return QSA_ERR_INVALID_ARG;
+    a.t[k] = t;
+    a.items += t.head_dim <= 128 ? (t.heads + 1) / 2 : t.heads;
+  }
+  // an output may be its own input; any other overlap would read rotated rows
+  for (int j = 0; j < num_tensors; ++j) {
+    const int64_t row = (int64_t)tensors[j].heads * tensors[j].head_dim;
+    const Rows o{reinterpret_cast<uintptr_t>(tensors[j].out), tensors[j].out_stride, row};
+    for (int k = 0; k < num_tensors; ++k) {
+      const int64_t row_k = (int64_t)tensors[k].heads * tensors[k].head_dim;
+      const Rows ik{reinterpret_cast<uintptr_t>(tensors[k].in), tensors[k].in_stride, row_k};
+      const Rows ok{reinterpret_cast<uintptr_t>(tensors[k].out), tensors[k].out_stride, row_k};
+      const bool in_place = j == k && ik.at == o.at && (n == 1 || ik.stride == o.stride);
+      if (!in_place && rows_overlap(o, ik, n)) return QSA_ERR_INVALID_ARG;
+      if (j < k && rows_overlap(o, ok, n)) return QSA_ERR_INVALID_ARG;
+    }
+  }
+  const unsigned grid = (unsigned)(((int64_t)n + kTokens - 1) / kTokens);
+  return qsa_host::launch(rope_kernel, dim3(grid), dim3(kThreads), 0, static_cast<cudaStream_t>(stream), a);
+}

@@ -45,6 +45,19 @@ class qsa_cache_t(ctypes.Structure):
                 ("num_kv_heads", ctypes.c_int32), ("kv_dtype", ctypes.c_int32)]
 
 
+ROPE_MAX_PAIRS, ROPE_MAX_AXES, ROPE_MAX_TENSORS = 128, 3, 4
+
+
+class qsa_rope_plan_t(ctypes.Structure):
+    _fields_ = [("rot_dim", ctypes.c_int32), ("num_axes", ctypes.c_int32), ("adjacent", ctypes.c_int32),
+                ("axis", ctypes.c_uint8 * ROPE_MAX_PAIRS), ("freq", ctypes.c_double * ROPE_MAX_PAIRS)]
+
+
+class qsa_rope_tensor_t(ctypes.Structure):
+    _fields_ = [("in_", ctypes.c_void_p), ("out", ctypes.c_void_p), ("heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("in_stride", ctypes.c_int64), ("out_stride", ctypes.c_int64)]
+
+
 KV_BF16 = 0
 KV_FP8_E4M3 = 1
 _KV_TORCH = {KV_BF16: torch.bfloat16, KV_FP8_E4M3: torch.float8_e4m3fn}
@@ -73,6 +86,12 @@ def _load() -> ctypes.CDLL:
         "qsa_dcp_localize_tokens": (ctypes.c_int, [P, P, I32, I32, I32, I32, P, P, P]),
         "qsa_dcp_localize_selection": (ctypes.c_int, [P, P, P, I32, I32, I32, I32, I32, P, P, P, P, P]),
         "qsa_sparse_attention_noalloc": (ctypes.c_int, [PC, P, I32, I32, P, P, P, P, I32, F, I32, P, P, P, P]),
+        "qsa_rope": (ctypes.c_int, [ctypes.POINTER(qsa_rope_plan_t), ctypes.POINTER(qsa_rope_tensor_t), I32, P, I64,
+                                    I32, P]),
+        "qsa_dense_decode_workspace_bytes": (I64, [PC, I32, I32, I32]),
+        "qsa_dense_decode": (ctypes.c_int, [PC, P, I32, I32, P, P, F, P, P, P, P, I64, F, P, I64, P, P]),
+        "qsa_evict_workspace_bytes": (I64, [PC, I32, I32]),
+        "qsa_evict": (ctypes.c_int, [PC, P, P, P, I32, P, P, I64, I32, I32, I32, P, P, P, P, I64, P, P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -746,6 +765,283 @@ class StepPipeline:
         """Host (out, lse) of step i: valid once its download has completed."""
         _, out, lse = self.hosts[i % 2]
         return out, lse
+
+
+# ----------------------------------------------------------------------------
+# layers that attend to everything they hold: rotary positions, dense decode,
+# eviction.  Every call has a bind_* form that checks its arguments once.
+
+
+class LaunchCall:
+    """A bound C entry point (see :class:`BoundCall`) that takes its stream when
+    it is called: the one it was bound to, or the caller's current stream.  It
+    runs on its tensors' device whichever device is current.  The tensors must
+    stay alive and unchanged in shape while the call is used."""
+
+    def __init__(self, name: str, args: tuple, keep: tuple, device: torch.device, stream=None):
+        self.name = name
+        self.fn = getattr(LIB, name)
+        self.args = args
+        self._keep = keep
+        self.device = device.index if device.index is not None else torch.cuda.current_device()
+        self.stream = stream
+
+    def __call__(self):
+        if torch.cuda.current_device() != self.device:
+            with torch.cuda.device(self.device):
+                return self()
+        s = self.stream if self.stream is not None else torch.cuda.current_stream(self.device)
+        rc = self.fn(*self.args, ctypes.c_void_p(s.cuda_stream))
+        if rc != QSA_OK:
+            raise QSAError(self.name, rc)
+
+
+def _same_device(device, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} is on {t.device}, expected {device}")
+
+
+def _status(dev_status):
+    return None if dev_status is None else _req(dev_status, "dev_status", torch.int32, (1,))
+
+
+def _workspace_ptr(workspace, need: int, name: str = "workspace"):
+    _req(workspace, name, torch.uint8, (None,))
+    if workspace.numel() < need:
+        raise ValueError(f"{name}: {workspace.numel()} bytes, needs {need}")
+    return _ptr(workspace)
+
+
+class RopePlan:
+    """What qsa_rope rotates and how fast.  `sections` holds the number of pairs
+    of each axis (time, height, width; one axis for plain text); rot_dim is
+    twice their sum.  Pair i turns by base ** (-2 i / rot_dim) per position, or
+    by freqs[i] where given.  `cycled` deals the pairs to the axes in turn
+    (0, 1, 2, 0, 1, 2, ...) as long as axes 1 and 2 have pairs left, the rest to
+    axis 0; otherwise the sections follow one another.  `adjacent` pairs dims
+    (2i, 2i + 1) instead of (i, i + rot_dim / 2)."""
+
+    def __init__(self, rot_dim: int, sections=None, base: float = 1.0e4, cycled: bool = False,
+                 adjacent: bool = False, freqs=None):
+        half = int(rot_dim) // 2
+        if rot_dim < 16 or rot_dim % 16 or half > ROPE_MAX_PAIRS:
+            raise ValueError(f"rot_dim must be a multiple of 16 in [16, {2 * ROPE_MAX_PAIRS}], got {rot_dim}")
+        sections = (half,) if sections is None else tuple(int(x) for x in sections)
+        if not 1 <= len(sections) <= ROPE_MAX_AXES or any(x < 0 for x in sections) or sum(sections) != half:
+            raise ValueError(f"sections {sections} must be 1 to {ROPE_MAX_AXES} counts that add up to rot_dim / 2 = "
+                             f"{half}")
+        if cycled:
+            k = len(sections)
+            axis = [i % k if i % k and i < k * sections[i % k] else 0 for i in range(half)]
+            if [axis.count(a) for a in range(k)] != list(sections):
+                raise ValueError(f"sections {sections} cannot be dealt in turn over {half} pairs")
+        else:
+            axis = [a for a, x in enumerate(sections) for _ in range(x)]
+        if freqs is None:
+            freqs = [float(base) ** (-2.0 * i / rot_dim) for i in range(half)]
+        freqs = [float(f) for f in freqs]
+        if len(freqs) != half or not all(math.isfinite(f) for f in freqs):
+            raise ValueError(f"freqs must be {half} finite numbers")
+        self.rot_dim, self.num_axes, self.adjacent = int(rot_dim), len(sections), bool(adjacent)
+        self.axis, self.freqs = axis, freqs
+        self._struct = qsa_rope_plan_t(self.rot_dim, self.num_axes, int(self.adjacent),
+                                       (ctypes.c_uint8 * ROPE_MAX_PAIRS)(*axis),
+                                       (ctypes.c_double * ROPE_MAX_PAIRS)(*freqs))
+
+    def struct(self) -> qsa_rope_plan_t:
+        return self._struct
+
+
+def _rope_rows(t, name: str, n: int):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name}: expected {torch.bfloat16}, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dim() != 3 or t.shape[0] != n:
+        raise ValueError(f"{name}: expected shape ({n}, heads, head_dim), got {tuple(t.shape)}")
+    if t.numel() and ((t.shape[2] > 1 and t.stride(2) != 1) or (t.shape[1] > 1 and t.stride(1) != t.shape[2])):
+        raise ValueError(f"{name}: heads and dims must be dense (only the token stride is free)")
+    return t
+
+
+def bind_rope(plan: RopePlan, pos, inputs, outputs=None, stream=None) -> LaunchCall:
+    """qsa_rope with its arguments checked once; see :func:`qsa_rope`."""
+    _req(pos, "pos", torch.int32, (plan.num_axes, None))
+    n = int(pos.shape[1])
+    inputs = list(inputs)
+    outputs = inputs if outputs is None else list(outputs)
+    if not 1 <= len(inputs) <= ROPE_MAX_TENSORS or len(outputs) != len(inputs):
+        raise ValueError(f"1 to {ROPE_MAX_TENSORS} inputs and as many outputs")
+    arr = (qsa_rope_tensor_t * len(inputs))()
+    for k, (x, y) in enumerate(zip(inputs, outputs)):
+        _rope_rows(x, f"inputs[{k}]", n)
+        _rope_rows(y, f"outputs[{k}]", n)
+        if x.shape != y.shape:
+            raise ValueError(f"outputs[{k}]: expected shape {tuple(x.shape)}, got {tuple(y.shape)}")
+        _same_device(pos.device, **{f"inputs[{k}]": x, f"outputs[{k}]": y})
+        arr[k] = qsa_rope_tensor_t(x.data_ptr(), y.data_ptr(), int(x.shape[1]), int(x.shape[2]), x.stride(0),
+                                   y.stride(0))
+    st = plan.struct()
+    return LaunchCall("qsa_rope", (ctypes.byref(st), arr, len(inputs), _ptr(pos), n, n),
+                      (plan, st, arr, pos, inputs, outputs), pos.device, stream)
+
+
+def qsa_rope(plan: RopePlan, pos, inputs, outputs=None, stream=None):
+    """Rotate bf16 tensors [n][heads][head_dim] (q, k, the indexer's, ...) by the
+    positions pos int32 [axes][n]; in place unless `outputs` are given.  Only the
+    token stride is free, so slices of a fused projection can be passed.  Returns
+    the outputs."""
+    outputs = list(inputs) if outputs is None else list(outputs)
+    bind_rope(plan, pos, inputs, outputs, stream)()
+    return outputs
+
+
+def dense_decode_workspace_bytes(cache: PagedCache, nq: int, hq: int, with_mass: bool = False) -> int:
+    r = LIB.qsa_dense_decode_workspace_bytes(ctypes.byref(cache.struct()), int(nq), int(hq), int(with_mass))
+    _check("qsa_dense_decode_workspace_bytes", r if r < 0 else QSA_OK)
+    return r
+
+
+def _mass_args(cache: PagedCache, mass_in, mass_out):
+    ld = cache.max_pages_per_seq * BLOCKS_PER_PAGE
+    for t, nm in ((mass_in, "mass_in"), (mass_out, "mass_out")):
+        _req(t, nm, torch.float32, (cache.max_seqs, None))
+        if t.shape[1] < ld:
+            raise ValueError(f"{nm}: {t.shape[1]} blocks per sequence, needs {ld}")
+    if mass_in.shape != mass_out.shape:
+        raise ValueError("mass_in and mass_out must have the same shape")
+    return int(mass_in.shape[1])
+
+
+def bind_dense_decode(cache: PagedCache, q, q_seq, q_pos, scale: float, out, lse, workspace, mass_in=None,
+                      mass_out=None, decay: float = 1.0, dev_status=None, stream=None) -> LaunchCall:
+    """qsa_dense_decode with its arguments checked once; see :func:`qsa_dense_decode`."""
+    nq = int(q_seq.shape[0])
+    hq = int(q.shape[1]) if q.dim() == 3 else -1
+    _req(q, "q", torch.bfloat16, (nq, hq, HEAD_DIM))
+    _req(q_seq, "q_seq", torch.int32, (nq,))
+    _req(q_pos, "q_pos", torch.int32, (nq,))
+    _req(out, "out", torch.bfloat16, (nq, hq, HEAD_DIM))
+    _req(lse, "lse", torch.float32, (nq, hq))
+    ld = 0
+    if mass_in is not None or mass_out is not None:
+        ld = _mass_args(cache, mass_in, mass_out)
+    _status(dev_status)
+    ws = _workspace_ptr(workspace, dense_decode_workspace_bytes(cache, nq, hq, ld > 0))
+    _same_device(q.device, q_seq=q_seq, q_pos=q_pos, out=out, lse=lse, workspace=workspace, mass_in=mass_in,
+                 mass_out=mass_out, dev_status=dev_status, kv_pages=cache.kv_pages)
+    st = cache.struct()
+    return LaunchCall("qsa_dense_decode",
+                      (ctypes.byref(st), _ptr(q), nq, hq, _ptr(q_seq), _ptr(q_pos), float(scale), _ptr(out),
+                       _ptr(lse), _ptr(mass_in), _ptr(mass_out), ld, float(decay), ws, int(workspace.numel()),
+                       _ptr(dev_status)),
+                      (cache, st, q, q_seq, q_pos, out, lse, mass_in, mass_out, workspace, dev_status), q.device,
+                      stream)
+
+
+def qsa_dense_decode(cache: PagedCache, q, q_seq, q_pos, scale: float, out, lse, workspace, mass_in=None,
+                     mass_out=None, decay: float = 1.0, dev_status=None, stream=None):
+    """Attention of one token per query over all the tokens its sequence holds
+    (positions 0 .. q_pos); with mass_in / mass_out (fp32 [max_seqs][blocks]) also
+    the attention weight of every micro-block, added into a running total.
+    `workspace`: uint8, dense_decode_workspace_bytes(...) of them."""
+    bind_dense_decode(cache, q, q_seq, q_pos, scale, out, lse, workspace, mass_in, mass_out, decay, dev_status,
+                      stream)()
+
+
+def evict_workspace_bytes(cache: PagedCache, n: int, budget: int) -> int:
+    r = LIB.qsa_evict_workspace_bytes(ctypes.byref(cache.struct()), int(n), int(budget))
+    _check("qsa_evict_workspace_bytes", r if r < 0 else QSA_OK)
+    return r
+
+
+def bind_evict(cache: PagedCache, seq_ids, seq_len, mass_in, mass_out, budget: int, sink: int, recent: int, keep,
+               keep_count, new_len, workspace, dst_table=None, dev_status=None, stream=None) -> LaunchCall:
+    """qsa_evict with its arguments checked once; see :func:`qsa_evict`."""
+    n = int(seq_ids.shape[0])
+    for t, nm in ((seq_ids, "seq_ids"), (seq_len, "seq_len"), (keep_count, "keep_count"), (new_len, "new_len")):
+        _req(t, nm, torch.int32, (n,))
+    _req(keep, "keep", torch.int32, (n, int(budget)))
+    ld = _mass_args(cache, mass_in, mass_out)
+    if dst_table is not None:
+        _req(dst_table, "dst_table", torch.int32, (cache.max_seqs, cache.max_pages_per_seq))
+    _status(dev_status)
+    ws = _workspace_ptr(workspace, evict_workspace_bytes(cache, n, budget))
+    _same_device(seq_ids.device, seq_len=seq_len, mass_in=mass_in, mass_out=mass_out, keep=keep,
+                 keep_count=keep_count, new_len=new_len, workspace=workspace, dst_table=dst_table,
+                 dev_status=dev_status, block_table=cache.block_table)
+    st = cache.struct()
+    return LaunchCall("qsa_evict",
+                      (ctypes.byref(st), _ptr(dst_table), _ptr(seq_ids), _ptr(seq_len), n, _ptr(mass_in),
+                       _ptr(mass_out), ld, int(budget), int(sink), int(recent), _ptr(keep), _ptr(keep_count),
+                       _ptr(new_len), ws, int(workspace.numel()), _ptr(dev_status)),
+                      (cache, st, seq_ids, seq_len, mass_in, mass_out, keep, keep_count, new_len, workspace,
+                       dst_table, dev_status), seq_ids.device, stream)
+
+
+def qsa_evict(cache: PagedCache, seq_ids, seq_len, mass_in, mass_out, budget: int, sink: int, recent: int, keep,
+              keep_count, new_len, workspace, dst_table=None, dev_status=None, stream=None):
+    """Cut sequences down to `budget` complete micro-blocks by accumulated
+    attention weight: the first `sink`, the last `recent` and the heaviest
+    between them, moved together in order (in place, or into the pages of
+    dst_table).  Fills keep [n][budget], keep_count and new_len."""
+    bind_evict(cache, seq_ids, seq_len, mass_in, mass_out, budget, sink, recent, keep, keep_count, new_len,
+               workspace, dst_table, dev_status, stream)()
+
+
+class DenseDecoder:
+    """Outputs and workspace of qsa_dense_decode for up to `max_nq` queries.  With
+    ``track=True`` it also holds `mass`, the running attention weight of every
+    micro-block (``decay`` of the old total is kept at each step), and
+    :meth:`evict` cuts sequences to a budget by it."""
+
+    def __init__(self, cache: PagedCache, hq: int, max_nq: int, scale: float = 1.0 / 16.0, track: bool = False,
+                 decay: float = 1.0):
+        dev = cache.device
+        self.cache, self.hq, self.max_nq, self.scale, self.decay = cache, hq, max_nq, float(scale), float(decay)
+        self.out = torch.empty((max_nq, hq, HEAD_DIM), dtype=torch.bfloat16, device=dev)
+        self.lse = torch.empty((max_nq, hq), dtype=torch.float32, device=dev)
+        self.mass = (torch.zeros((cache.max_seqs, cache.max_pages_per_seq * BLOCKS_PER_PAGE), dtype=torch.float32,
+                                 device=dev) if track else None)
+        self.workspace = torch.empty(dense_decode_workspace_bytes(cache, max_nq, hq, track), dtype=torch.uint8,
+                                     device=dev)
+        self.dev_status = torch.zeros((1,), dtype=torch.int32, device=dev)
+
+    def bind(self, q, q_seq, q_pos, stream=None) -> list:
+        """The pre-bound launch of a step's attention, for a StepGraph."""
+        nq = int(q_seq.shape[0])
+        if nq > self.max_nq:
+            raise ValueError(f"{nq} queries, at most {self.max_nq}")
+        return [bind_dense_decode(self.cache, q, q_seq, q_pos, self.scale, self.out[:nq], self.lse[:nq],
+                                  self.workspace, self.mass, self.mass, self.decay, self.dev_status, stream)]
+
+    def run(self, q, q_seq, q_pos, stream=None):
+        """out [nq][hq][256] and lse [nq][hq] of the queries (views of this object's buffers)."""
+        self.bind(q, q_seq, q_pos, stream)[0]()
+        nq = int(q_seq.shape[0])
+        return self.out[:nq], self.lse[:nq]
+
+    def evict(self, seq_ids, seq_len, budget: int, sink: int = 0, recent: int = 0, dst_table=None, stream=None):
+        """Cut the listed sequences (seq_len tokens each) to `budget` complete
+        micro-blocks by `mass`.  Returns (new_len, keep, keep_count), device
+        tensors; the caller appends at new_len and frees the pages behind it."""
+        if self.mass is None:
+            raise ValueError("evict needs track=True")
+        n, dev = int(seq_ids.shape[0]), self.cache.device
+        keep = torch.empty((n, int(budget)), dtype=torch.int32, device=dev)
+        count = torch.empty((n,), dtype=torch.int32, device=dev)
+        new_len = torch.empty((n,), dtype=torch.int32, device=dev)
+        ws = torch.empty(evict_workspace_bytes(self.cache, n, budget), dtype=torch.uint8, device=dev)
+        if stream is not None:  # allocated on the current stream, used on this one
+            for t in (keep, count, new_len, ws):
+                t.record_stream(stream)
+            stream.wait_stream(torch.cuda.current_stream(dev))
+        qsa_evict(self.cache, seq_ids, seq_len, self.mass, self.mass, budget, sink, recent, keep, count, new_len, ws,
+                  dst_table, self.dev_status, stream)
+        return new_len, keep, count
 
 
 def splits_bound(k: int, chunk_units: int) -> int:
