@@ -21,29 +21,31 @@
 // 2 CTAs x 16 rows of workspace whatever the batch, and a second small kernel
 // joins them and adds up the weights.
 //
-// CTA = 8 consumer warps + 1 copy warp.  The copy warp resolves 32 tiles' pages
-// at once, one batch ahead, and one lane moves each tile with bulk copies into
-// an 11-stage ring (176 KiB in flight).  Each consumer warp takes whole tiles:
-// S = Q K^T, a running maximum and sum, O += P V over all 256 dims, with no
-// exchange between warps until the pair's piece ends.
+// CTA = 6 (BF16) or 7 (e4m3) consumer warps + 1 copy warp: with 8 warps or
+// fewer a thread may hold 255 registers, and the 16 x 256 accumulator takes 128.
+// The copy warp resolves 32 tiles' pages at once, one batch ahead, and a lane
+// each moves a tile with bulk copies into a ring of 12 or 21 tiles; it also
+// brings the Q rows of the next pair.  Tile T goes to consumer warp T % warps,
+// which computes S = Q K^T, a running maximum and sum, and O += P V over all 256
+// dims, with no exchange between warps until the pair's piece ends.
 #include "qsa_common.cuh"
 
 namespace {
 
 using namespace qsa;
 
-constexpr int kWarps = 8;                       // consumer warps
-constexpr int kConsumerThreads = kWarps * 32;
-constexpr int kThreads = kConsumerThreads + 32;  // + the copy warp
 constexpr int kTile = 16;                        // tokens of a tile
 constexpr int kTileRuns = kTile / kRatio;        // 4 micro-blocks
 constexpr int kTilesPerPage = kPage / kTile;
 constexpr int kMaxCtas = 256;                    // partial slots reserved: 2 per CTA
-constexpr int kMinTiles = 8;                     // tiles a CTA takes at least: one per consumer warp
+constexpr int kMinTiles = 6;                     // tiles a CTA takes at least: about one per consumer warp
 constexpr int kQStride = kHeadDim * 2 + 16;      // Q rows 528 B apart: conflict-free 16-byte fragment reads
 constexpr int kQBytes = 16 * kQStride;
-constexpr int kCombBytes = kWarps * 16 * 64 * 4;  // one 64-dim slice of every warp's O
+constexpr int kSlice = 32;                       // dims of O that the warps join at once
+constexpr int kSlices = kHeadDim / kSlice;
+constexpr int kCombRow = kSlice + 4;             // floats; the skew spreads the rows over the banks
 constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s
+constexpr int kTab = 64;  // queries whose length a CTA keeps in shared memory
 constexpr int kBarConsumers = 1;
 // The running maximum a warp subtracts may lag the true one by this much (base
 // 2), so that O is seldom rescaled: exp2 stays below 2^8, harmless in fp32 sums
@@ -54,20 +56,31 @@ constexpr float kLag = 8.f;
 // e4m3: rows are plain, so runs are placed 32 B apart to spread the banks.
 template <bool F8>
 struct Lay {
+  static constexpr int kWarps = F8 ? 7 : 6;  // consumer warps
+  static constexpr int kConsumerThreads = kWarps * 32;
+  static constexpr int kThreads = kConsumerThreads + 32;
   static constexpr int kRunBytes = 2 * kRatio * kHeadDim * (F8 ? 1 : 2);
   static constexpr int kRunStride = kRunBytes + (F8 ? 32 : 0);
   static constexpr int kStageBytes = kTileRuns * kRunStride;
-  static constexpr int kStages = F8 ? 22 : 11;
-  static constexpr int kOffQ = kStages * kStageBytes;
-  static constexpr int kOffComb = kOffQ + kQBytes;
-  static constexpr int kOffML = kOffComb + kCombBytes;          // [warp][16 rows] (m, l)
-  static constexpr int kOffScale = kOffML + kWarps * 16 * 8;    // logit scale of each row
+  static constexpr int kStages = F8 ? 21 : 12;
+  // Tile T and tile T + kStages, which reuses its stage, belong to one warp: it has
+  // seen the stage's last phase end before it waits for the next.  A parity wait
+  // cannot tell a phase from the one two before, so another warp could run ahead.
+  static_assert(kStages % kWarps == 0, "a stage has one consumer");
+  static constexpr int kCombWarp = 16 * kCombRow;               // floats of one warp's slice
+  static constexpr int kOffQ = kStages * kStageBytes;           // two pieces' Q rows
+  static constexpr int kOffComb = kOffQ + 2 * kQBytes;
+  static constexpr int kOffML = kOffComb + kWarps * kCombWarp * 4;  // [warp][16 rows] (m, l)
+  static constexpr int kOffScale = kOffML + kWarps * 16 * 8;    // e4m3: logit scale of each row
   static constexpr int kOffValid = kOffScale + 16 * 4;          // tokens in each stage
   static constexpr int kOffPlan = (kOffValid + kStages * 4 + 15) & ~15;
-  static constexpr int kOffBar = kOffPlan + 64;
-  static constexpr int kOffAbort = kOffBar + 2 * kStages * 8;
+  static constexpr int kOffTab = kOffPlan + 16 * 8;             // (len, seq) of queries q0 ..
+  static constexpr int kOffBar = kOffTab + kTab * 8;            // full, empty, Q full [2], Q empty [2]
+  static constexpr int kOffAbort = kOffBar + (2 * kStages + 4) * 8;
   static constexpr int kSmem = kOffAbort + 16;
+  static constexpr int kIssue = F8 ? 7 : 3;  // copy-warp lanes that wait and issue together, a tile each
   static_assert(kSmem <= 232448, "shared memory budget");
+  static_assert(kWarps * kSlices * kCombWarp * 4 <= kOffQ, "a whole O of every warp fits the ring");
 };
 
 struct DenseArgs {
@@ -127,6 +140,8 @@ struct Walk {
   int seq;
   int t0, t1;     // tiles of the pair in this CTA
   int64_t begin;  // global index of the pair's first tile
+  int q0;         // the share's first query, whose table entry comes first
+  const int2* tab;
 };
 
 // The piece at or after global tile x (x inside query q's tiles, which begin at qbegin).
@@ -150,9 +165,11 @@ __device__ __forceinline__ bool next_piece(const DenseArgs& a, Walk& w, int64_t 
   } else {
     do {
       ++w.q;
-      w.len = query_len(a, w.q, false);
+      const int k = w.q - w.q0;
+      const int2 e = k < kTab ? w.tab[k] : make_int2(query_len(a, w.q, false), a.q_seq[w.q]);
+      w.len = e.x;
+      w.seq = e.y;
     } while (w.len == 0);
-    w.seq = a.q_seq[w.q];
     w.g = 0;
     w.begin = x;
   }
@@ -188,69 +205,94 @@ __device__ void copy_warp(const DenseArgs& a, uint8_t* smem, Walk w, int64_t x1)
   const uint32_t full = smem_u32(smem + LY::kOffBar), empty = full + LY::kStages * 8;
   int* valid = reinterpret_cast<int*>(smem + LY::kOffValid);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + LY::kOffAbort);
-  const uint64_t policy = l2_policy_evict_first();
-  int64_t T = 0;
+  const uint64_t policy = l2_policy_evict_first(), policy_q = l2_policy_evict_normal();
+  uint32_t T = 0, n_issued = 0;  // tiles taken up, tiles whose copies were issued
+  uint32_t piece = 0;            // pieces whose Q rows were issued
+  const uint32_t q_full = empty + LY::kStages * 8, q_empty = q_full + 16;
   bool more = true, stop = false;
   while (more && !stop) {
-    // pages of 32 tiles at a time, the next batch's loads issued before this batch's copies
-    int tb = w.t0;
+    {  // Q rows of the group, 512 bytes each
+      const uint32_t b = piece & 1u;
+      if (piece >= 2 && !wait_bar(a, q_empty + b * 8, ((piece >> 1) - 1) & 1u, abort_flag)) stop = true;
+      if (__any_sync(0xffffffffu, stop)) {
+        stop = true;
+        break;
+      }
+      if (lane == 0) mbar_arrive_expect_tx(q_full + b * 8, a.G * kHeadDim * 2);
+      __syncwarp();
+      if (lane < a.G)
+        bulk_g2s(smem_u32(smem + LY::kOffQ) + b * kQBytes + lane * kQStride,
+                 a.q + ((size_t)w.q * a.hq + (size_t)w.g * a.G + lane) * kHeadDim, kHeadDim * 2, q_full + b * 8,
+                 policy_q);
+      ++piece;
+    }
+    // lane = tile: pages of 32 tiles at a time, the next batch's loads issued before this batch's copies
     auto lookup = [&](int t) {
       int page = -1;
       if (t < w.t1) page = __ldg(a.bt + (int64_t)w.seq * a.mpps + t / kTilesPerPage);
       return page;
     };
-    int page = lookup(tb + lane);
-    while (tb < w.t1 && !stop) {
+    int page = lookup(w.t0 + lane);
+    for (int tb = w.t0; tb < w.t1 && !stop; tb += 32) {
       const int page_next = lookup(tb + 32 + lane);
-      const int n = min(32, w.t1 - tb);
-      const bool bad = lane < n && (page < 0 || page >= a.num_pages);
-      if (bad) flag(a.st, QSA_DEV_BAD_PAGE);
-      for (int i = 0; i < n; ++i, ++T) {
-        const int pg = __shfl_sync(0xffffffffu, bad ? -1 : page, i);
-        const int stage = (int)(T % LY::kStages);
-        int ok = 1;
-        if (lane == 0) {
-          if (T >= LY::kStages)
-            ok = wait_bar(a, empty + stage * 8, (uint32_t)((T / LY::kStages - 1) & 1), abort_flag);
-          if (ok) {
-            const int t = tb + i;
-            const int tok = min(kTile, w.len - t * kTile);
-            valid[stage] = pg < 0 ? 0 : tok;
-            if (pg < 0) {
-              mbar_arrive(full + stage * 8);
-            } else {
-              const int runs = (tok + kRatio - 1) / kRatio;  // whole micro-blocks that hold a token
-              const uint8_t* src = a.kv + (((size_t)pg * a.hkv + w.g) * kBlocksPerPage +
-                                           (size_t)(t % kTilesPerPage) * kTileRuns) * LY::kRunBytes;
-              const uint32_t dst = ring + stage * LY::kStageBytes;
-              mbar_arrive_expect_tx(full + stage * 8, runs * LY::kRunBytes);
-              if constexpr (F8) {
-                for (int r = 0; r < runs; ++r)
-                  bulk_g2s(dst + r * LY::kRunStride, src + r * LY::kRunBytes, LY::kRunBytes, full + stage * 8, policy);
-              } else {
-                bulk_g2s(dst, src, runs * LY::kRunBytes, full + stage * 8, policy);
-              }
-            }
-          }
-        }
-        ok = __shfl_sync(0xffffffffu, ok, 0);
-        if (!ok) {
+      const int n = min(32, w.t1 - tb), t = tb + lane;
+      const bool bad = page < 0 || page >= a.num_pages;
+      if (lane < n && bad) flag(a.st, QSA_DEV_BAD_PAGE);
+      const int tok = min(kTile, w.len - t * kTile);
+      const int runs = (tok + kRatio - 1) / kRatio;  // whole micro-blocks that hold a token
+      const uint8_t* src = a.kv + (((size_t)page * a.hkv + w.g) * kBlocksPerPage +
+                                   (size_t)(t % kTilesPerPage) * kTileRuns) * LY::kRunBytes;
+      const uint32_t mine = T + lane;
+      const int stage = (int)(mine % LY::kStages);
+      const uint32_t bar = full + stage * 8, dst = ring + stage * LY::kStageBytes;
+      for (int i0 = 0; i0 < n; i0 += LY::kIssue) {
+        const bool on = lane >= i0 && lane < min(n, i0 + LY::kIssue);
+        bool ok = true;
+        if (on && mine >= LY::kStages)
+          ok = wait_bar(a, empty + stage * 8, (mine / LY::kStages - 1) & 1u, abort_flag);
+        if (!__all_sync(0xffffffffu, ok)) {  // the tiles before these have been issued, these have not
+          n_issued = T + i0;
           stop = true;
           break;
         }
+        if (on) {
+          valid[stage] = bad ? 0 : tok;
+          if (bad) {
+            mbar_arrive(bar);
+          } else {
+            mbar_arrive_expect_tx(bar, runs * LY::kRunBytes);
+            if constexpr (F8) {
+#pragma unroll
+              for (int r = 0; r < kTileRuns; ++r)
+                if (r < runs) bulk_g2s(dst + r * LY::kRunStride, src + r * LY::kRunBytes, LY::kRunBytes, bar, policy);
+            } else {
+              bulk_g2s(dst, src, runs * LY::kRunBytes, bar, policy);
+            }
+          }
+        }
       }
+      if (!stop) n_issued = T + n;
+      T += n;
       page = page_next;
-      tb += 32;
     }
     if (!stop) more = next_piece(a, w, x1);
   }
-  // never leave the CTA with copies in flight
-  if (lane == 0) {
-    for (int64_t t = max((int64_t)0, T - LY::kStages); t < T; ++t) {
-      const uint64_t s0 = global_timer_ns();
-      while (!mbar_try_wait(full + (int)(t % LY::kStages) * 8, (uint32_t)((t / LY::kStages) & 1)))
-        if (global_timer_ns() - s0 > kWaitLimitNs) break;
-    }
+  // never leave the CTA with copies in flight: each lane waits for one stage's last copy
+  const uint32_t left = min(n_issued, (uint32_t)LY::kStages), left_q = min(piece, 2u);
+  uint32_t bar = 0, parity = 0;
+  if (lane < (int)left) {
+    const uint32_t t = n_issued - 1 - lane;
+    bar = full + (t % LY::kStages) * 8;
+    parity = (t / LY::kStages) & 1u;
+  } else if (lane >= 30 && lane - 30 < (int)left_q) {
+    const uint32_t t = piece - 1 - (lane - 30);
+    bar = q_full + (t & 1u) * 8;
+    parity = (t >> 1) & 1u;
+  }
+  if (bar) {
+    const uint64_t s0 = global_timer_ns();
+    while (!mbar_try_wait(bar, parity))
+      if (global_timer_ns() - s0 > kWaitLimitNs) break;
   }
   __syncwarp();
 }
@@ -274,17 +316,19 @@ __device__ __forceinline__ int tile_row(int j, int tq, int e) {
 }
 
 template <bool F8>
-__device__ void consumers(const DenseArgs& a, uint8_t* smem, Walk w, int64_t T_all, int64_t x0, int64_t x1) {
+__device__ void consumers(const DenseArgs& a, uint8_t* smem, Walk w, int64_t x0, int64_t x1) {
   using LY = Lay<F8>;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int gq = lane >> 2, tq = lane & 3;
-  const uint32_t ring = smem_u32(smem), qb = smem_u32(smem + LY::kOffQ);
+  const uint32_t ring = smem_u32(smem);
   const uint32_t full = smem_u32(smem + LY::kOffBar), empty = full + LY::kStages * 8;
+  const uint32_t q_full = empty + LY::kStages * 8, q_empty = q_full + 16;
   const volatile int* valid = reinterpret_cast<const volatile int*>(smem + LY::kOffValid);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + LY::kOffAbort);
   float* comb = reinterpret_cast<float*>(smem + LY::kOffComb);
   float2* ml = reinterpret_cast<float2*>(smem + LY::kOffML);
   float* row_scale = reinterpret_cast<float*>(smem + LY::kOffScale);
+  constexpr int kWarps = LY::kWarps, kConsumerThreads = LY::kConsumerThreads;
   const int G = a.G;
   const int64_t max_tiles = (int64_t)a.mpps * kTilesPerPage;
 
@@ -306,19 +350,22 @@ __device__ void consumers(const DenseArgs& a, uint8_t* smem, Walk w, int64_t T_a
   }
   const int kr0 = tile_row<F8>(0, kt, ke);  // BF16: the row, for the chunk swizzle
 
-  int64_t T_base = 0;
-  for (;;) {
+  uint32_t T_base = 0;
+  for (uint32_t piece = 0;; ++piece) {
     const int n_tiles = w.t1 - w.t0;
-    // ---- Q rows of the group (rows beyond it are zero).  e4m3 K/V takes FP16 operands:
-    // each row is scaled by a power of two into FP16's range (exact down to 2^-38 of its
-    // largest element) and its logit scale takes the factor back.
+    // ---- Q rows of the group (rows beyond it are zero, written once at the start)
+    const uint32_t qb = smem_u32(smem + LY::kOffQ) + (piece & 1u) * kQBytes;
+    if (!*abort_flag) wait_bar(a, q_full + (piece & 1u) * 8, (piece >> 1) & 1u, abort_flag);
+    __syncwarp();
+    float sc0 = a.scale_log2, sc1 = a.scale_log2;
+    if constexpr (F8) {
+      // FP16 operands: each row is scaled by a power of two into FP16's range (exact down
+      // to 2^-38 of its largest element) and its logit scale takes the factor back
 #pragma unroll
-    for (int it = 0; it < 2; ++it) {
-      const int row = warp + 8 * it;
-      uint4 v = make_uint4(0, 0, 0, 0);
-      if (row < G) v = ldg_nc(a.q + ((size_t)w.q * a.hq + (size_t)w.g * G + row) * kHeadDim + lane * 8);
-      float sc = a.scale_log2;
-      if constexpr (F8) {
+      for (int it = 0; it < 3; ++it) {
+        const int row = warp + kWarps * it;
+        if (row >= 16) break;
+        const uint4 v = lds128(qb + row * kQStride + lane * 16);
         uint32_t x[4] = {v.x, v.y, v.z, v.w};
         uint32_t mx = 0;  // largest magnitude, as ordered bits
 #pragma unroll
@@ -327,29 +374,30 @@ __device__ void consumers(const DenseArgs& a, uint8_t* smem, Walk w, int64_t T_a
         const int ex = (int)(mx >> 7);  // biased exponent
         const int up = (ex == 0 || ex == 255) ? 0 : max(-100, min(100, 127 + 13 - ex));
         const float f = __uint_as_float((uint32_t)(127 + up) << 23);
-        sc *= __uint_as_float((uint32_t)(127 - up) << 23);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const __half2 h = __floats2half2_rn(__uint_as_float(x[e] << 16) * f, __uint_as_float(x[e] & 0xffff0000u) * f);
           x[e] = *reinterpret_cast<const uint32_t*>(&h);
         }
-        v = make_uint4(x[0], x[1], x[2], x[3]);
+        sts128(qb + row * kQStride + lane * 16, make_uint4(x[0], x[1], x[2], x[3]));
+        if (lane == 0) row_scale[row] = a.scale_log2 * __uint_as_float((uint32_t)(127 - up) << 23);
       }
-      sts128(qb + row * kQStride + lane * 16, v);
-      if (lane == 0) row_scale[row] = sc;
+      fence_proxy_async();  // these writes come before the copy of the piece after next
+      named_bar_sync(kBarConsumers, kConsumerThreads);
+      sc0 = row_scale[gq];
+      sc1 = row_scale[gq + 8];
     }
-    named_bar_sync(kBarConsumers, kConsumerThreads);
-    const float sc0 = row_scale[gq], sc1 = row_scale[gq + 8];
 
     float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
     float o[32][4];
 #pragma unroll
     for (int nt = 0; nt < 32; ++nt) o[nt][0] = o[nt][1] = o[nt][2] = o[nt][3] = 0.f;
 
-    for (int ti = warp; ti < n_tiles; ti += kWarps) {
-      const int64_t T = T_base + ti;
+    const int rank = (int)((warp + kWarps - T_base % kWarps) % kWarps);  // this warp's first tile of the piece
+    for (int ti = rank; ti < n_tiles; ti += kWarps) {
+      const uint32_t T = T_base + ti;
       const int stage = (int)(T % LY::kStages);
-      const bool got = !*abort_flag && wait_bar(a, full + stage * 8, (uint32_t)((T / LY::kStages) & 1), abort_flag);
+      const bool got = !*abort_flag && wait_bar(a, full + stage * 8, (T / LY::kStages) & 1u, abort_flag);
       __syncwarp();
       if (!__all_sync(0xffffffffu, got)) break;
       const int nv = valid[stage];
@@ -519,6 +567,8 @@ __device__ void consumers(const DenseArgs& a, uint8_t* smem, Walk w, int64_t T_a
       if (lane == 0) mbar_arrive(empty + stage * 8);
     }
     T_base += n_tiles;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(q_empty + (piece & 1u) * 8);
 
     // ---- join the warps' (m, l, O)
     l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
@@ -526,11 +576,11 @@ __device__ void consumers(const DenseArgs& a, uint8_t* smem, Walk w, int64_t T_a
     l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
     l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
     if (tq == 0) {
-      ml[warp * 16 + gq] = make_float2(m0, l0);
-      ml[warp * 16 + gq + 8] = make_float2(m1, l1);
+      ml[rank * 16 + gq] = make_float2(m0, l0);
+      ml[rank * 16 + gq + 8] = make_float2(m1, l1);
     }
     named_bar_sync(kBarConsumers, kConsumerThreads);
-    const int nw = min(kWarps, n_tiles);  // warps that had a tile
+    const int nw = min(kWarps, n_tiles);  // warps that had a tile: ranks 0 .. nw - 1
     float fac[2], lse2[2];
 #pragma unroll
     for (int hr = 0; hr < 2; ++hr) {
@@ -561,131 +611,154 @@ __device__ void consumers(const DenseArgs& a, uint8_t* smem, Walk w, int64_t T_a
         }
       }
     }
-    // 64 dims at a time: every warp's slice to shared memory, then one float4 per thread
+    // O: slices of 32 dims go through shared memory, every warp's to its own place, and a
+    // thread adds up one float4 of them.  After the share's last piece the ring is free and
+    // takes all the slices at once; before, one slice at a time.
+    const bool last = w.begin + w.t1 >= x1;
+    auto add_up = [&](const float* base, int sl, int item) {
+      const int row = item >> 3, col = (item & 7) * 4;
+      if (row >= G) return;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int v = 0; v < nw; ++v) {
+        const float4 y = *reinterpret_cast<const float4*>(base + v * LY::kCombWarp + row * kCombRow + col);
+        acc.x += y.x;
+        acc.y += y.y;
+        acc.z += y.z;
+        acc.w += y.w;
+      }
+      const int dim = F8 ? 128 * (sl >> 2) + 32 * (col >> 3) + 16 * ((sl >> 1) & 1) + 8 * (sl & 1) + (col & 7)
+                         : kSlice * sl + col;
+      if (direct) {
+        uint2 v2;
+        v2.x = pack_bf16(acc.x, acc.y);
+        v2.y = pack_bf16(acc.z, acc.w);
+        *reinterpret_cast<uint2*>(a.out + ((size_t)w.q * a.hq + (size_t)w.g * G + row) * kHeadDim + dim) = v2;
+      } else {
+        *reinterpret_cast<float4*>(a.part_o + ((size_t)slot * G + row) * kHeadDim + dim) = acc;
+      }
+    };
+    float* const whole = reinterpret_cast<float*>(smem);
 #pragma unroll
-    for (int sl = 0; sl < 4; ++sl) {
-      if (warp < nw) {
-        float* dst = comb + warp * 16 * 64;
+    for (int sl = 0; sl < kSlices; ++sl) {
+      float* base = last ? whole + sl * kWarps * LY::kCombWarp : comb;
+      if (rank < nw) {
+        // BF16: n-tile 8 (sl >> 1) + i holds, in column 2tq + e, dim 64 (sl >> 1) + 32e + 8tq + i:
+        //       slice sl takes e = sl & 1.
+        // e4m3: n-tile 16c + i, column 2tq + e, dim 128c + 32tq + 16e + i: slice sl takes
+        //       c = sl >> 2, e = (sl >> 1) & 1 and i = 8 (sl & 1) .. + 7.
+        const int e = F8 ? (sl >> 1) & 1 : sl & 1;
+        const int i0 = F8 ? 16 * (sl >> 2) + 8 * (sl & 1) : 8 * (sl >> 1);
 #pragma unroll
         for (int hr = 0; hr < 2; ++hr)
 #pragma unroll
-          for (int e = 0; e < 2; ++e)
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              // BF16: n-tile 8sl + i holds, in column 2tq + e, dim 64sl + 32e + 8tq + i;
-              // e4m3: n-tile 16 (sl >> 1) + i, column 2tq + e, dim 128 (sl >> 1) + 32tq + 16e + i:
-              // slice sl then takes i = 8 (sl & 1) .. + 7 of every column
-              const int i0 = F8 ? 16 * (sl >> 1) + 8 * (sl & 1) + 4 * k : 8 * sl + 4 * k;
-              const int cc = 2 * hr + e;
-              const int col = (F8 ? 16 * tq + 8 * e : 32 * e + 8 * tq) + 4 * k;
-              *reinterpret_cast<float4*>(dst + (gq + 8 * hr) * 64 + col) =
-                  make_float4(o[i0][cc] * fac[hr], o[i0 + 1][cc] * fac[hr], o[i0 + 2][cc] * fac[hr],
-                              o[i0 + 3][cc] * fac[hr]);
-            }
+          for (int k = 0; k < 2; ++k)
+            *reinterpret_cast<float4*>(base + rank * LY::kCombWarp + (gq + 8 * hr) * kCombRow + 8 * tq + 4 * k) =
+                make_float4(o[i0 + 4 * k][2 * hr + e] * fac[hr], o[i0 + 4 * k + 1][2 * hr + e] * fac[hr],
+                            o[i0 + 4 * k + 2][2 * hr + e] * fac[hr], o[i0 + 4 * k + 3][2 * hr + e] * fac[hr]);
       }
-      named_bar_sync(kBarConsumers, kConsumerThreads);
-      const int row = tid >> 4, col = (tid & 15) * 4;
-      if (row < G) {
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int v = 0; v < nw; ++v) {
-          const float4 y = *reinterpret_cast<const float4*>(comb + (v * 16 + row) * 64 + col);
-          acc.x += y.x;
-          acc.y += y.y;
-          acc.z += y.z;
-          acc.w += y.w;
-        }
-        const int dim = F8 ? 128 * (sl >> 1) + 16 * (col >> 3) + 8 * (sl & 1) + (col & 7) : 64 * sl + col;
-        if (direct) {
-          uint2 v2;
-          v2.x = pack_bf16(acc.x, acc.y);
-          v2.y = pack_bf16(acc.z, acc.w);
-          *reinterpret_cast<uint2*>(a.out + ((size_t)w.q * a.hq + (size_t)w.g * G + row) * kHeadDim + dim) = v2;
-        } else {
-          *reinterpret_cast<float4*>(a.part_o + ((size_t)slot * G + row) * kHeadDim + dim) = acc;
-        }
+      if (!last) {
+        named_bar_sync(kBarConsumers, kConsumerThreads);
+        if (tid < 128) add_up(comb, sl, tid);
+        named_bar_sync(kBarConsumers, kConsumerThreads);
       }
-      named_bar_sync(kBarConsumers, kConsumerThreads);
     }
-    if (!next_piece(a, w, x1)) break;
+    if (last) {
+      named_bar_sync(kBarConsumers, kConsumerThreads);
+      for (int i = tid; i < kSlices * 128; i += kConsumerThreads)
+        add_up(whole + (i >> 7) * kWarps * LY::kCombWarp, i >> 7, i & 127);
+      break;
+    }
+    next_piece(a, w, x1);
   }
 }
 
 template <bool F8>
-__global__ void __launch_bounds__(kThreads, 1) dense_decode_kernel(DenseArgs a) {
+__global__ void __launch_bounds__(Lay<F8>::kThreads, 1) dense_decode_kernel(DenseArgs a) {
   using LY = Lay<F8>;
+  constexpr int kThreads = LY::kThreads, kWarps = LY::kWarps;
   extern __shared__ __align__(1024) uint8_t smem[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_launch_dependents();
-  int64_t* plan = reinterpret_cast<int64_t*>(smem + LY::kOffPlan);
-  // warp 0 sets the pipeline up, the others wait for the previous kernel meanwhile
+  int64_t* plan = reinterpret_cast<int64_t*>(smem + LY::kOffPlan);  // [0..3] share, [4..] warp sums
+  int2* tab = reinterpret_cast<int2*>(smem + LY::kOffTab);
   if (tid == 0) {
     const uint32_t bars = smem_u32(smem + LY::kOffBar);
-    for (int i = 0; i < 2 * LY::kStages; ++i) mbar_init(bars + i * 8, 1);
+    for (int i = 0; i < 2 * LY::kStages + 2; ++i) mbar_init(bars + i * 8, 1);
+    for (int i = 0; i < 2; ++i) mbar_init(bars + (2 * LY::kStages + 2 + i) * 8, LY::kWarps);
     fence_mbar_init();
     *reinterpret_cast<volatile int*>(smem + LY::kOffAbort) = 0;
   }
+  // Q rows beyond the group stay zero
+  for (int i = tid; i < 2 * (16 - a.G) * 32; i += kThreads) {
+    const int row = a.G + (i >> 5) % (16 - a.G), b = (i >> 5) / (16 - a.G);
+    sts128(smem_u32(smem + LY::kOffQ) + b * kQBytes + row * kQStride + (i & 31) * 16, make_uint4(0, 0, 0, 0));
+  }
   pdl_wait_previous();
-  // ---- the share of this CTA: tiles of every query, summed by one warp
-  if (warp == 0) {
-    int64_t total = 0;
-    for (int b = 0; b < a.nq; b += 32) {
-      const int q = b + lane;
-      int64_t n = q < a.nq ? (int64_t)tiles_of(query_len(a, q, blockIdx.x == 0)) * a.hkv : 0;
-      int64_t inc = n;
+  // ---- the share of this CTA.  A thread per query, kThreads of them a round; with
+  // one round (the usual batch) the lengths are loaded once and kept.
+  const bool one_round = a.nq <= kThreads;
+  int64_t total = 0, first = 0;
+  int len = 0;
+  auto scan_round = [&](int base, bool report) {  // tiles before query base + tid; total moves on
+    const int q = base + tid;
+    len = q < a.nq ? query_len(a, q, report) : 0;
+    const int64_t n = (int64_t)tiles_of(len) * a.hkv;
+    int64_t inc = n;
 #pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const int64_t y = __shfl_up_sync(0xffffffffu, inc, d);
-        if (lane >= d) inc += y;
-      }
-      if (blockIdx.x == 0 && q < a.nq) a.pre[q] = total + inc - n;
-      total += __shfl_sync(0xffffffffu, inc, 31);
+    for (int d = 1; d < 32; d <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, inc, d);
+      if (lane >= d) inc += y;
     }
-    if (blockIdx.x == 0 && lane == 0) a.pre[a.nq] = total;
-    const int used = ctas_used(total, a.ctas);
-    int64_t x0 = 0, x1 = 0;
-    if (total > 0 && (int)blockIdx.x < used) {
-      x0 = share_begin(total, used, blockIdx.x);
-      x1 = share_begin(total, used, blockIdx.x + 1);
+    if (lane == 31) plan[4 + warp] = inc;
+    __syncthreads();
+    first = total + inc - n;
+    for (int v = 0; v < kThreads / 32; ++v) {
+      const int64_t x = plan[4 + v];
+      if (v < warp) first += x;
+      total += x;
     }
-    // the query that holds tile x0
-    int64_t before = 0;
-    for (int b = 0; b < a.nq && x0 < x1; b += 32) {
-      const int q = b + lane;
-      const int len = q < a.nq ? query_len(a, q, false) : 0;
-      const int64_t n = (int64_t)tiles_of(len) * a.hkv;
-      int64_t inc = n;
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const int64_t y = __shfl_up_sync(0xffffffffu, inc, d);
-        if (lane >= d) inc += y;
-      }
-      const int64_t first = before + inc - n;
-      if (n > 0 && first <= x0 && x0 < first + n) {
-        plan[2] = q;
-        plan[3] = first;
-        plan[4] = len;
-        plan[5] = a.q_seq[q];
-      }
-      before += __shfl_sync(0xffffffffu, inc, 31);
-      if (before > x0) break;
+    __syncthreads();
+  };
+  for (int b = 0; b < a.nq; b += kThreads) {
+    scan_round(b, blockIdx.x == 0);
+    if (blockIdx.x == 0 && b + tid < a.nq) a.pre[b + tid] = first;
+  }
+  if (blockIdx.x == 0 && tid == 0) a.pre[a.nq] = total;
+  if (total == 0) return;
+  const int used = ctas_used(total, a.ctas);
+  if ((int)blockIdx.x >= used) return;
+  const int64_t x0 = share_begin(total, used, blockIdx.x), x1 = share_begin(total, used, blockIdx.x + 1);
+  auto find_first = [&](int base) {  // the query that holds tile x0
+    if (len > 0 && first <= x0 && x0 < first + (int64_t)tiles_of(len) * a.hkv) {
+      plan[0] = base + tid;
+      plan[1] = first;
     }
-    if (lane == 0) {
-      plan[0] = x0;
-      plan[1] = x1;
-      plan[6] = total;
+  };
+  if (one_round) {
+    find_first(0);
+  } else {
+    total = 0;
+    for (int b = 0; b < a.nq; b += kThreads) {
+      scan_round(b, false);
+      find_first(b);
     }
   }
   __syncthreads();
-  const int64_t x0 = plan[0], x1 = plan[1];
-  if (x0 >= x1) return;
   Walk w;
-  w.q = (int)plan[2];
-  w.begin = plan[3];
-  w.len = (int)plan[4];
-  w.seq = (int)plan[5];
+  w.q0 = w.q = (int)plan[0];
+  w.begin = plan[1];
+  w.tab = tab;
+  if (one_round) {
+    if (tid >= w.q0 && tid < min(a.nq, w.q0 + kTab)) tab[tid - w.q0] = make_int2(len, len ? a.q_seq[tid] : -1);
+  } else if (tid < kTab && w.q0 + tid < a.nq) {
+    tab[tid] = make_int2(query_len(a, w.q0 + tid, false), a.q_seq[w.q0 + tid]);
+  }
+  __syncthreads();
+  w.len = tab[0].x;
+  w.seq = tab[0].y;
   load_piece(a, w, x0, x1);
   if (warp < kWarps)
-    consumers<F8>(a, smem, w, plan[6], x0, x1);
+    consumers<F8>(a, smem, w, x0, x1);
   else
     copy_warp<F8>(a, smem, w, x1);
 }
@@ -899,7 +972,7 @@ int launch_dense(const DenseArgs& a, cudaStream_t s) {
     (void)cudaGetLastError();
     return QSA_ERR_CUDA;
   }
-  return qsa_host::launch(dense_decode_kernel<F8>, dim3((unsigned)a.ctas), dim3(kThreads), (size_t)Lay<F8>::kSmem, s,
+  return qsa_host::launch(dense_decode_kernel<F8>, dim3((unsigned)a.ctas), dim3(Lay<F8>::kThreads), (size_t)Lay<F8>::kSmem, s,
                           a);
 }
 

@@ -263,6 +263,15 @@ QSA_DEVINL uint64_t l2_policy_evict_first() {
   return p;
 }
 
+QSA_DEVINL uint64_t l2_policy_evict_normal() {
+  uint64_t p;
+  asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
+  return p;
+}
+
+// Orders this thread's shared-memory accesses before async copies that follow.
+QSA_DEVINL void fence_proxy_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
 // Programmatic dependent launch.  Every library kernel is launched so that the
 // next kernel on the stream may start while it runs: a kernel first lets its
 // dependents be scheduled, then waits until the previous kernel on the stream

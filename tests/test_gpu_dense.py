@@ -228,6 +228,15 @@ def check_dense(grp, q, q_seq, q_pos, scale=1 / 16, track=False, decay=1.0, mass
     return out, lse
 
 
+def check_bits(grp, q, q_seq, q_pos):
+    nq, hq = q.shape[:2]
+    dec = qsa.DenseDecoder(grp.cache, hq, nq)
+    o, l = dec.run(q.cuda(), i32(q_seq), i32(q_pos))
+    torch.cuda.synchronize()
+    assert int(dec.dev_status.item()) == 0
+    return o, l
+
+
 HEADS = [(16, 2), (24, 2), (12, 1), (6, 1), (3, 1), (4, 4), (16, 1), (9, 3)]
 
 
@@ -253,6 +262,18 @@ def test_dense_decode_one_sequence(n, fp8):
     grp = Group([n], 2, fp8, seed=n, lean=4.0)
     mass0 = torch.rand((1, grp.cache.max_pages_per_seq * 16), generator=gen(n))
     check_dense(grp, queries(1, 24, n, 2.0), [0], [n - 1], track=True, mass0=mass0)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("lens", [[60000, 1, 50011, 40], [131072 + 7] + [100] * 90])
+def test_dense_decode_long_shares(lens, fp8):
+    """Hundreds of tiles per CTA: the ring is reused many times, a share holds several pairs."""
+    grp = Group(lens, 2, fp8, seed=len(lens), lean=4.0)
+    q_seq = list(range(len(lens)))
+    a = check_dense(grp, queries(len(lens), 6, 1), q_seq, [n - 1 for n in lens])
+    for _ in range(20):                                       # the same bits, whatever order the copies land in
+        b = check_bits(grp, queries(len(lens), 6, 1), q_seq, [n - 1 for n in lens])
+        assert torch.equal(bits(a[0]), bits(b[0])) and torch.equal(bits(a[1]), bits(b[1]))
 
 
 @pytest.mark.parametrize("fp8", [False, True])
