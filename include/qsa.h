@@ -485,7 +485,8 @@ QSA_API int qsa_rope(const qsa_rope_plan_t* plan, const qsa_rope_tensor_t* tenso
  * into a result, whatever they hold.  Several queries of one sequence are
  * allowed.  Splits depend on the lengths and the SM count alone: the same call
  * gives the same bits.
- * Requirements: hq % Hkv == 0, hq / Hkv <= 16, scale > 0; BF16 or FP8 K/V (for
+ * Requirements: hq % Hkv == 0, hq / Hkv <= 16, scale > 0, nq * Hkv *
+ * (max_pages_per_seq * 4 + 8) < 2^31; BF16 or FP8 K/V (for
  * FP8 each q row is scaled by a power of two into FP16's range).
  */
 QSA_API int64_t qsa_dense_decode_workspace_bytes(const qsa_cache_t* cache, int32_t nq, int32_t hq, int32_t with_mass);

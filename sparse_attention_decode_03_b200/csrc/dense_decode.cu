@@ -38,7 +38,8 @@ constexpr int kTile = 16;                        // tokens of a tile
 constexpr int kTileRuns = kTile / kRatio;        // 4 micro-blocks
 constexpr int kTilesPerPage = kPage / kTile;
 constexpr int kMaxCtas = 256;                    // partial slots reserved: 2 per CTA
-constexpr int kMinTiles = 6;                     // tiles a CTA takes at least: about one per consumer warp
+constexpr int kPieceCost = 8;                    // what a pair costs a CTA beside its tiles, in tiles
+constexpr int kMinPlaces = 8;                    // places a CTA takes at least
 constexpr int kQStride = kHeadDim * 2 + 16;      // Q rows 528 B apart: conflict-free 16-byte fragment reads
 constexpr int kQBytes = 16 * kQStride;
 constexpr int kSlice = 32;                       // dims of O that the warps join at once
@@ -92,7 +93,7 @@ struct DenseArgs {
   const int32_t* q_seq;
   const int32_t* q_pos;
   float scale_log2;
-  int64_t* pre;     // [nq + 1] tiles before each query; pre[nq] = all
+  int2* span;       // [nq][hkv] first and last CTA that hold tiles of the pair; last < first: none
   float* part_lse;  // [2 CTAs][G], base 2
   float* part_o;    // [2 CTAs][G][256], normalised
   __nv_bfloat16* out;
@@ -121,61 +122,61 @@ __device__ __forceinline__ int query_len(const DenseArgs& a, int q, bool report)
 
 __device__ __forceinline__ int tiles_of(int len) { return (len + kTile - 1) / kTile; }
 
-// CTAs that share T tiles, and the first tile of CTA c's share.
-__host__ __device__ __forceinline__ int ctas_used(int64_t T, int ctas) {
-  const int64_t want = (T + kMinTiles - 1) / kMinTiles;
-  return want < ctas ? (want < 1 ? 1 : (int)want) : ctas;
+// The list that the CTAs share out: every pair takes kPieceCost places (what
+// joining its warps costs beside a tile), then one per tile.
+struct Shares {
+  int n, base, rem;  // CTAs; the first `rem` take base + 1 places, the others base
+};
+__device__ __forceinline__ Shares make_shares(int total, int ctas) {
+  Shares s;
+  s.n = min(ctas, max(1, (total + kMinPlaces - 1) / kMinPlaces));
+  s.base = total / s.n;
+  s.rem = total - s.base * s.n;
+  return s;
 }
-__host__ __device__ __forceinline__ int64_t share_begin(int64_t T, int n, int c) { return T * c / n; }
-// The CTA whose share holds tile t: the largest c with share_begin(c) <= t.
-__host__ __device__ __forceinline__ int share_of(int64_t T, int n, int64_t t) {
-  int c = (int)(((t + 1) * n - 1) / T);
-  return c;
+__device__ __forceinline__ int share_begin(const Shares& s, int c) { return c * s.base + min(c, s.rem); }
+__device__ __forceinline__ int share_of(const Shares& s, int x) {  // the CTA that holds place x
+  const int cut = s.rem * (s.base + 1);
+  return x < cut ? x / (s.base + 1) : s.rem + (x - cut) / s.base;
 }
 
-// A CTA's position in the tile list.
+__device__ __forceinline__ int places_of(int len) { return len ? tiles_of(len) + kPieceCost : 0; }
+
+// A CTA's position in the list: a piece of pair (q, g).
 struct Walk {
-  int q, g;       // pair
-  int len;        // tokens of the query
-  int seq;
-  int t0, t1;     // tiles of the pair in this CTA
-  int64_t begin;  // global index of the pair's first tile
-  int q0;         // the share's first query, whose table entry comes first
+  int q, g;
+  int len, seq;  // of the query
+  int t0, t1;    // tiles of the pair in this CTA
+  int begin;     // the pair's first place
+  int q_tab;     // the query of tab[0]
   const int2* tab;
 };
 
-// The piece at or after global tile x (x inside query q's tiles, which begin at qbegin).
-__device__ __forceinline__ void load_piece(const DenseArgs& a, Walk& w, int64_t x, int64_t x1) {
-  const int nt = tiles_of(w.len);
-  const int64_t qbegin = w.begin;  // on entry: the query's first tile
-  w.g = (int)((x - qbegin) / nt);
-  w.begin = qbegin + (int64_t)w.g * nt;
-  w.t0 = (int)(x - w.begin);
-  w.t1 = (int)min((int64_t)nt, x1 - w.begin);
+__device__ __forceinline__ bool set_span(Walk& w, int x0, int x1) {
+  const int lo = w.begin + kPieceCost;
+  w.t0 = max(0, x0 - lo);
+  w.t1 = min(tiles_of(w.len), x1 - lo);
+  return w.t1 > 0;
 }
 
-// Step to the next piece; false at the end of the share.
-__device__ __forceinline__ bool next_piece(const DenseArgs& a, Walk& w, int64_t x1) {
-  const int nt = tiles_of(w.len);
-  const int64_t x = w.begin + w.t1;
-  if (x >= x1) return false;
+// Whether tiles of a pair after this one lie in the share.
+__device__ __forceinline__ bool has_next(const Walk& w, int x1) { return w.begin + places_of(w.len) + kPieceCost < x1; }
+
+__device__ __forceinline__ void next_piece(const DenseArgs& a, Walk& w, int x1) {
+  w.begin += places_of(w.len);
   if (w.g + 1 < a.hkv) {
     ++w.g;
-    w.begin += nt;
   } else {
     do {
       ++w.q;
-      const int k = w.q - w.q0;
+      const int k = w.q - w.q_tab;
       const int2 e = k < kTab ? w.tab[k] : make_int2(query_len(a, w.q, false), a.q_seq[w.q]);
       w.len = e.x;
       w.seq = e.y;
     } while (w.len == 0);
     w.g = 0;
-    w.begin = x;
   }
-  w.t0 = 0;
-  w.t1 = (int)min((int64_t)tiles_of(w.len), x1 - w.begin);
-  return true;
+  set_span(w, 0, x1);
 }
 
 // Bounded wait; false (and the abort flag) when the limit passed.
@@ -198,7 +199,7 @@ __device__ __forceinline__ bool wait_bar(const DenseArgs& a, uint32_t bar, uint3
 // ------------------------------------------------------------------ copy warp
 
 template <bool F8>
-__device__ void copy_warp(const DenseArgs& a, uint8_t* smem, Walk w, int64_t x1) {
+__device__ void copy_warp(const DenseArgs& a, uint8_t* smem, Walk w, int x1) {
   using LY = Lay<F8>;
   const int lane = threadIdx.x & 31;
   const uint32_t ring = smem_u32(smem);
@@ -275,7 +276,10 @@ __device__ void copy_warp(const DenseArgs& a, uint8_t* smem, Walk w, int64_t x1)
       T += n;
       page = page_next;
     }
-    if (!stop) more = next_piece(a, w, x1);
+    if (!stop) {
+      more = has_next(w, x1);
+      if (more) next_piece(a, w, x1);
+    }
   }
   // never leave the CTA with copies in flight: each lane waits for one stage's last copy
   const uint32_t left = min(n_issued, (uint32_t)LY::kStages), left_q = min(piece, 2u);
@@ -299,6 +303,13 @@ __device__ void copy_warp(const DenseArgs& a, uint8_t* smem, Walk w, int64_t x1)
 
 // ------------------------------------------------------------------ consumers
 
+// 2^x, denormal results flushed: below 2^-126 a weight adds nothing to a sum that holds one of 2^-8 or more
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // Which token of the tile a lane's logits and V rows belong to.  Columns n = 2tq + e
 // of S's n-tile j (lane tq of each quad holds e = 0, 1):
 //   BF16: micro-block 2j + e, row tq ^ e.  K's column n then reads row (n >> 1) ^ (n & 1):
@@ -316,7 +327,7 @@ __device__ __forceinline__ int tile_row(int j, int tq, int e) {
 }
 
 template <bool F8>
-__device__ void consumers(const DenseArgs& a, uint8_t* smem, Walk w, int64_t x0, int64_t x1) {
+__device__ void consumers(const DenseArgs& a, uint8_t* smem, Walk w, const Shares& sh, int x1) {
   using LY = Lay<F8>;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int gq = lane >> 2, tq = lane & 3;
@@ -457,7 +468,7 @@ __device__ void consumers(const DenseArgs& a, uint8_t* smem, Walk w, int64_t x0,
       const bool up0 = r0 > m0 + kLag, up1 = r1 > m1 + kLag;  // -inf + 8 = -inf: the first logit always moves it
       if (__any_sync(0xffffffffu, up0 || up1)) {
         const float n0 = up0 ? r0 : m0, n1 = up1 ? r1 : m1;
-        const float al0 = up0 ? exp2f(m0 - n0) : 1.f, al1 = up1 ? exp2f(m1 - n1) : 1.f;
+        const float al0 = up0 ? exp2_fast(m0 - n0) : 1.f, al1 = up1 ? exp2_fast(m1 - n1) : 1.f;
         m0 = n0;
         m1 = n1;
         l0 *= al0;
@@ -475,10 +486,10 @@ __device__ void consumers(const DenseArgs& a, uint8_t* smem, Walk w, int64_t x0,
       float p[2][4];
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        p[j][0] = exp2f(s[j][0] - sub0);
-        p[j][1] = exp2f(s[j][1] - sub0);
-        p[j][2] = exp2f(s[j][2] - sub1);
-        p[j][3] = exp2f(s[j][3] - sub1);
+        p[j][0] = exp2_fast(s[j][0] - sub0);
+        p[j][1] = exp2_fast(s[j][1] - sub0);
+        p[j][2] = exp2_fast(s[j][2] - sub1);
+        p[j][3] = exp2_fast(s[j][3] - sub1);
       }
       l0 += (p[0][0] + p[0][1]) + (p[1][0] + p[1][1]);
       l1 += (p[0][2] + p[0][3]) + (p[1][2] + p[1][3]);
@@ -584,21 +595,24 @@ __device__ void consumers(const DenseArgs& a, uint8_t* smem, Walk w, int64_t x0,
     float fac[2], lse2[2];
 #pragma unroll
     for (int hr = 0; hr < 2; ++hr) {
-      const int row = gq + 8 * hr;
+      float2 e[kWarps];
       float M = -INFINITY, L = 0.f;
-      for (int v = 0; v < nw; ++v) M = fmaxf(M, ml[v * 16 + row].x);
-      fac[hr] = 0.f;
-      lse2[hr] = -INFINITY;
-      if (M != -INFINITY) {
-        for (int v = 0; v < nw; ++v) L += ml[v * 16 + row].y * exp2f(ml[v * 16 + row].x - M);
-        fac[hr] = exp2f((hr ? m1 : m0) - M) / L;
-        lse2[hr] = M + log2f(L);
+#pragma unroll
+      for (int v = 0; v < kWarps; ++v) {
+        e[v] = ml[v * 16 + gq + 8 * hr];
+        M = fmaxf(M, e[v].x);
       }
+      const float sub = M == -INFINITY ? 0.f : M;
+#pragma unroll
+      for (int v = 0; v < kWarps; ++v) L += e[v].y * exp2_fast(e[v].x - sub);
+      fac[hr] = L > 0.f ? exp2_fast((hr ? m1 : m0) - sub) / L : L;  // L = 0: no token; NaN stays NaN
+      lse2[hr] = M + log2f(L);                                      // -inf when L = 0
     }
-    // whole pair here: straight to out; else to this CTA's first or last partial slot
+    // whole pair here: straight to out; else to the partial slot of the pair that this
+    // CTA took over (0) or leaves unfinished (1)
     const int nt_pair = tiles_of(w.len);
     const bool direct = w.t0 == 0 && w.t1 == nt_pair;
-    const int slot = 2 * blockIdx.x + (w.begin > x0 ? 1 : 0);
+    const int slot = 2 * blockIdx.x + (w.t0 == 0 ? 1 : 0);
     if (warp == 0 && tq == 0) {
 #pragma unroll
       for (int hr = 0; hr < 2; ++hr) {
@@ -611,15 +625,21 @@ __device__ void consumers(const DenseArgs& a, uint8_t* smem, Walk w, int64_t x0,
         }
       }
     }
+    if (w.t0 == 0 && tid == 0)
+      a.span[w.q * a.hkv + w.g] =
+          make_int2(blockIdx.x, direct ? blockIdx.x : share_of(sh, w.begin + kPieceCost + nt_pair - 1));
     // O: slices of 32 dims go through shared memory, every warp's to its own place, and a
     // thread adds up one float4 of them.  After the share's last piece the ring is free and
     // takes all the slices at once; before, one slice at a time.
-    const bool last = w.begin + w.t1 >= x1;
+    const bool last = !has_next(w, x1);
+    const size_t out_row = direct ? (size_t)w.q * a.hq + (size_t)w.g * G : (size_t)slot * G;
     auto add_up = [&](const float* base, int sl, int item) {
       const int row = item >> 3, col = (item & 7) * 4;
       if (row >= G) return;
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int v = 0; v < nw; ++v) {
+#pragma unroll
+      for (int v = 0; v < kWarps; ++v) {
+        if (v >= nw) break;
         const float4 y = *reinterpret_cast<const float4*>(base + v * LY::kCombWarp + row * kCombRow + col);
         acc.x += y.x;
         acc.y += y.y;
@@ -628,31 +648,28 @@ __device__ void consumers(const DenseArgs& a, uint8_t* smem, Walk w, int64_t x0,
       }
       const int dim = F8 ? 128 * (sl >> 2) + 32 * (col >> 3) + 16 * ((sl >> 1) & 1) + 8 * (sl & 1) + (col & 7)
                          : kSlice * sl + col;
-      if (direct) {
-        uint2 v2;
-        v2.x = pack_bf16(acc.x, acc.y);
-        v2.y = pack_bf16(acc.z, acc.w);
-        *reinterpret_cast<uint2*>(a.out + ((size_t)w.q * a.hq + (size_t)w.g * G + row) * kHeadDim + dim) = v2;
-      } else {
-        *reinterpret_cast<float4*>(a.part_o + ((size_t)slot * G + row) * kHeadDim + dim) = acc;
-      }
+      const size_t at = (out_row + row) * kHeadDim + dim;
+      if (direct)
+        *reinterpret_cast<uint2*>(a.out + at) = make_uint2(pack_bf16(acc.x, acc.y), pack_bf16(acc.z, acc.w));
+      else
+        *reinterpret_cast<float4*>(a.part_o + at) = acc;
     };
-    float* const whole = reinterpret_cast<float*>(smem);
+    // BF16: n-tile 8 (sl >> 1) + i holds, in column 2tq + e, dim 64 (sl >> 1) + 32e + 8tq + i:
+    //       slice sl takes e = sl & 1.
+    // e4m3: n-tile 16c + i, column 2tq + e, dim 128c + 32tq + 16e + i: slice sl takes
+    //       c = sl >> 2, e = (sl >> 1) & 1 and i = 8 (sl & 1) .. + 7.
+    float* const put_at = (last ? reinterpret_cast<float*>(smem) : comb) + rank * LY::kCombWarp + gq * kCombRow + 8 * tq;
+    const int put_step = last ? kWarps * LY::kCombWarp : 0;
 #pragma unroll
     for (int sl = 0; sl < kSlices; ++sl) {
-      float* base = last ? whole + sl * kWarps * LY::kCombWarp : comb;
       if (rank < nw) {
-        // BF16: n-tile 8 (sl >> 1) + i holds, in column 2tq + e, dim 64 (sl >> 1) + 32e + 8tq + i:
-        //       slice sl takes e = sl & 1.
-        // e4m3: n-tile 16c + i, column 2tq + e, dim 128c + 32tq + 16e + i: slice sl takes
-        //       c = sl >> 2, e = (sl >> 1) & 1 and i = 8 (sl & 1) .. + 7.
         const int e = F8 ? (sl >> 1) & 1 : sl & 1;
         const int i0 = F8 ? 16 * (sl >> 2) + 8 * (sl & 1) : 8 * (sl >> 1);
 #pragma unroll
         for (int hr = 0; hr < 2; ++hr)
 #pragma unroll
           for (int k = 0; k < 2; ++k)
-            *reinterpret_cast<float4*>(base + rank * LY::kCombWarp + (gq + 8 * hr) * kCombRow + 8 * tq + 4 * k) =
+            *reinterpret_cast<float4*>(put_at + sl * put_step + 8 * hr * kCombRow + 4 * k) =
                 make_float4(o[i0 + 4 * k][2 * hr + e] * fac[hr], o[i0 + 4 * k + 1][2 * hr + e] * fac[hr],
                             o[i0 + 4 * k + 2][2 * hr + e] * fac[hr], o[i0 + 4 * k + 3][2 * hr + e] * fac[hr]);
       }
@@ -664,8 +681,9 @@ __device__ void consumers(const DenseArgs& a, uint8_t* smem, Walk w, int64_t x0,
     }
     if (last) {
       named_bar_sync(kBarConsumers, kConsumerThreads);
+#pragma unroll 1
       for (int i = tid; i < kSlices * 128; i += kConsumerThreads)
-        add_up(whole + (i >> 7) * kWarps * LY::kCombWarp, i >> 7, i & 127);
+        add_up(reinterpret_cast<float*>(smem) + (i >> 7) * kWarps * LY::kCombWarp, i >> 7, i & 127);
       break;
     }
     next_piece(a, w, x1);
@@ -679,7 +697,7 @@ __global__ void __launch_bounds__(Lay<F8>::kThreads, 1) dense_decode_kernel(Dens
   extern __shared__ __align__(1024) uint8_t smem[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_launch_dependents();
-  int64_t* plan = reinterpret_cast<int64_t*>(smem + LY::kOffPlan);  // [0..3] share, [4..] warp sums
+  int* plan = reinterpret_cast<int*>(smem + LY::kOffPlan);  // [0], [1] the first query and its place, [4..] warp sums
   int2* tab = reinterpret_cast<int2*>(smem + LY::kOffTab);
   if (tid == 0) {
     const uint32_t bars = smem_u32(smem + LY::kOffBar);
@@ -697,39 +715,41 @@ __global__ void __launch_bounds__(Lay<F8>::kThreads, 1) dense_decode_kernel(Dens
   // ---- the share of this CTA.  A thread per query, kThreads of them a round; with
   // one round (the usual batch) the lengths are loaded once and kept.
   const bool one_round = a.nq <= kThreads;
-  int64_t total = 0, first = 0;
-  int len = 0;
-  auto scan_round = [&](int base, bool report) {  // tiles before query base + tid; total moves on
+  const bool whole_tab = a.nq <= kTab;
+  int total = 0, first = 0, len = 0;
+  auto scan_round = [&](int base, bool report) {  // places before query base + tid; total moves on
     const int q = base + tid;
     len = q < a.nq ? query_len(a, q, report) : 0;
-    const int64_t n = (int64_t)tiles_of(len) * a.hkv;
-    int64_t inc = n;
+    const int n = places_of(len) * a.hkv;
+    int inc = n;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-      const int64_t y = __shfl_up_sync(0xffffffffu, inc, d);
+      const int y = __shfl_up_sync(0xffffffffu, inc, d);
       if (lane >= d) inc += y;
     }
     if (lane == 31) plan[4 + warp] = inc;
+    if (whole_tab && q < a.nq) tab[q] = make_int2(len, a.q_seq[q]);
     __syncthreads();
     first = total + inc - n;
+#pragma unroll
     for (int v = 0; v < kThreads / 32; ++v) {
-      const int64_t x = plan[4 + v];
+      const int x = plan[4 + v];
       if (v < warp) first += x;
       total += x;
     }
-    __syncthreads();
+    if (!one_round) __syncthreads();
   };
   for (int b = 0; b < a.nq; b += kThreads) {
     scan_round(b, blockIdx.x == 0);
-    if (blockIdx.x == 0 && b + tid < a.nq) a.pre[b + tid] = first;
+    if (blockIdx.x == 0 && b + tid < a.nq && len == 0)
+      for (int g = 0; g < a.hkv; ++g) a.span[(b + tid) * a.hkv + g] = make_int2(0, -1);
   }
-  if (blockIdx.x == 0 && tid == 0) a.pre[a.nq] = total;
   if (total == 0) return;
-  const int used = ctas_used(total, a.ctas);
-  if ((int)blockIdx.x >= used) return;
-  const int64_t x0 = share_begin(total, used, blockIdx.x), x1 = share_begin(total, used, blockIdx.x + 1);
-  auto find_first = [&](int base) {  // the query that holds tile x0
-    if (len > 0 && first <= x0 && x0 < first + (int64_t)tiles_of(len) * a.hkv) {
+  const Shares sh = make_shares(total, a.ctas);
+  if ((int)blockIdx.x >= sh.n) return;
+  const int x0 = share_begin(sh, blockIdx.x), x1 = share_begin(sh, blockIdx.x + 1);
+  auto find_first = [&](int base) {  // the query that holds place x0
+    if (len > 0 && first <= x0 && x0 < first + places_of(len) * a.hkv) {
       plan[0] = base + tid;
       plan[1] = first;
     }
@@ -745,20 +765,21 @@ __global__ void __launch_bounds__(Lay<F8>::kThreads, 1) dense_decode_kernel(Dens
   }
   __syncthreads();
   Walk w;
-  w.q0 = w.q = (int)plan[0];
+  w.q = plan[0];
   w.begin = plan[1];
   w.tab = tab;
-  if (one_round) {
-    if (tid >= w.q0 && tid < min(a.nq, w.q0 + kTab)) tab[tid - w.q0] = make_int2(len, len ? a.q_seq[tid] : -1);
-  } else if (tid < kTab && w.q0 + tid < a.nq) {
-    tab[tid] = make_int2(query_len(a, w.q0 + tid, false), a.q_seq[w.q0 + tid]);
+  w.q_tab = whole_tab ? 0 : w.q;
+  if (!whole_tab) {
+    if (tid < kTab && w.q + tid < a.nq) tab[tid] = make_int2(query_len(a, w.q + tid, false), a.q_seq[w.q + tid]);
+    __syncthreads();
   }
-  __syncthreads();
-  w.len = tab[0].x;
-  w.seq = tab[0].y;
-  load_piece(a, w, x0, x1);
+  w.len = tab[w.q - w.q_tab].x;
+  w.seq = tab[w.q - w.q_tab].y;
+  w.g = (x0 - w.begin) / places_of(w.len);
+  w.begin += w.g * places_of(w.len);
+  if (!set_span(w, x0, x1)) return;  // the share ends before the pair's first tile
   if (warp < kWarps)
-    consumers<F8>(a, smem, w, x0, x1);
+    consumers<F8>(a, smem, w, sh, x1);
   else
     copy_warp<F8>(a, smem, w, x1);
 }
@@ -776,50 +797,24 @@ struct JoinArgs {
   int32_t mass_blocks;  // CTAs per query for the weights
 };
 
-// CTAs of pair (q, g): shares first .. last, and the partial slot of share c.
-struct Pieces {
-  int64_t begin;
-  int64_t T;
-  int n, first, last;
-};
-
-__device__ __forceinline__ Pieces pieces_of(const DenseArgs& a, int q, int g) {
-  Pieces r;
-  const int64_t b0 = a.pre[q], b1 = a.pre[q + 1];
-  r.T = a.pre[a.nq];
-  const int64_t nt = (b1 - b0) / a.hkv;
-  r.begin = b0 + nt * g;
-  if (nt == 0) {
-    r.n = 0;
-    r.first = 0;
-    r.last = -1;
-    return r;
-  }
-  r.n = ctas_used(r.T, a.ctas);
-  r.first = share_of(r.T, r.n, r.begin);
-  r.last = share_of(r.T, r.n, r.begin + nt - 1);
-  return r;
-}
-
-__device__ __forceinline__ int slot_of(const Pieces& p, int c) {
-  return 2 * c + (p.begin > share_begin(p.T, p.n, c) ? 1 : 0);
-}
+// The partial slot of CTA c's piece of a pair that spans several CTAs.
+__device__ __forceinline__ int slot_of(const int2& span, int c) { return 2 * c + (c == span.x ? 1 : 0); }
 
 // Base-2 lse of (q, h), by one warp: the joined pieces' or, for a pair that one
 // CTA held, the one already in lse.
 __device__ __forceinline__ float joined_lse2(const DenseArgs& a, int q, int h) {
   const int lane = threadIdx.x & 31;
-  const Pieces p = pieces_of(a, q, h / a.G);
-  if (p.last < p.first) return -INFINITY;
-  if (p.first == p.last) return a.lse[(size_t)q * a.hq + h] * 1.44269504088896340736f;
+  const int2 p = a.span[q * a.hkv + h / a.G];
+  if (p.y < p.x) return -INFINITY;
+  if (p.x == p.y) return a.lse[(size_t)q * a.hq + h] * 1.44269504088896340736f;
   const int row = h % a.G;
   float M = -INFINITY;
-  for (int c = p.first + lane; c <= p.last; c += 32) M = fmaxf(M, a.part_lse[(size_t)slot_of(p, c) * a.G + row]);
+  for (int c = p.x + lane; c <= p.y; c += 32) M = fmaxf(M, a.part_lse[(size_t)slot_of(p, c) * a.G + row]);
 #pragma unroll
   for (int d = 16; d; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
   if (M == -INFINITY) return -INFINITY;
   float L = 0.f;
-  for (int c = p.first + lane; c <= p.last; c += 32) L += exp2f(a.part_lse[(size_t)slot_of(p, c) * a.G + row] - M);
+  for (int c = p.x + lane; c <= p.y; c += 32) L += exp2f(a.part_lse[(size_t)slot_of(p, c) * a.G + row] - M);
 #pragma unroll
   for (int d = 16; d; d >>= 1) L += __shfl_xor_sync(0xffffffffu, L, d);
   return M + log2f(L);
@@ -832,36 +827,62 @@ __global__ void __launch_bounds__(kJoinThreads) dense_join_kernel(JoinArgs ja) {
   const DenseArgs& a = ja.d;
   pdl_launch_dependents();
   pdl_wait_previous();
-  const int tid = threadIdx.x;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   __shared__ float4 acc_s[4][64];
-  __shared__ float lse_s[kMaxCtas];
+  __shared__ float lse_s[kMaxCtas];  // pieces' lse, then their weights (kMaxCtas <= kJoinThreads: one each)
+  __shared__ float red_s[2][kJoinThreads / 32];
+  static_assert(kMaxCtas <= kJoinThreads, "a thread per piece");
   const int64_t n_join = (int64_t)a.nq * a.hq;
   if (blockIdx.x < n_join) {
-    const int q = (int)(blockIdx.x / a.hq), h = (int)(blockIdx.x % a.hq);
-    const Pieces p = pieces_of(a, q, h / a.G);
-    if (p.last >= p.first && p.first == p.last) return;  // written by its CTA
+    const int q = (int)(blockIdx.x / a.hq), h = (int)(blockIdx.x % a.hq), row = h % a.G;
+    const int2 p = a.span[q * a.hkv + h / a.G];
+    if (p.x == p.y) return;  // written by its CTA
     const int grp = tid >> 6, c4 = tid & 63;
     uint2 o = make_uint2(0, 0);
     float lse = -INFINITY;
-    if (p.last > p.first) {
-      const int n = p.last - p.first + 1, row = h % a.G;
-      for (int i = tid; i < n; i += kJoinThreads) lse_s[i] = a.part_lse[(size_t)slot_of(p, p.first + i) * a.G + row];
+    const int n = p.y - p.x + 1;
+    if (n > 1) {
+      // rows: requested before their weights are known
+      const float4* base = reinterpret_cast<const float4*>(a.part_o + (size_t)row * kHeadDim) + c4;
+      const size_t step = (size_t)a.G * (kHeadDim / 4);
+      constexpr int kAhead = 4;
+      float4 x[kAhead];
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k)
+        if (grp + 4 * k < n) x[k] = base[slot_of(p, p.x + grp + 4 * k) * step];
+      float v = tid < n ? a.part_lse[(size_t)slot_of(p, p.x + tid) * a.G + row] : -INFINITY;
+      float M = v;
+#pragma unroll
+      for (int d = 16; d; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+      if (lane == 0) red_s[0][warp] = M;
       __syncthreads();
-      float M = -INFINITY;
-      for (int i = 0; i < n; ++i) M = fmaxf(M, lse_s[i]);
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int k = 0; k < kJoinThreads / 32; ++k) M = fmaxf(M, red_s[0][k]);
+      float e = M == -INFINITY ? 0.f : exp2f(v - M);  // 0 for an empty piece, whose row is zero
+      if (tid < n) lse_s[tid] = e;
+#pragma unroll
+      for (int d = 16; d; d >>= 1) e += __shfl_xor_sync(0xffffffffu, e, d);
+      if (lane == 0) red_s[1][warp] = e;
+      __syncthreads();
       float L = 0.f;
-      if (M != -INFINITY) {
-        for (int i = 0; i < n; ++i) L += exp2f(lse_s[i] - M);
-#pragma unroll 4
-        for (int i = grp; i < n; i += 4) {
-          const float e = exp2f(lse_s[i] - M);  // 0 for an empty piece, whose row is zero
-          const float4 x = reinterpret_cast<const float4*>(
-              a.part_o + ((size_t)slot_of(p, p.first + i) * a.G + row) * kHeadDim)[c4];
-          acc.x += e * x.x;
-          acc.y += e * x.y;
-          acc.z += e * x.z;
-          acc.w += e * x.w;
+#pragma unroll
+      for (int k = 0; k < kJoinThreads / 32; ++k) L += red_s[1][k];
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int i0 = grp; i0 < n; i0 += 4 * kAhead) {
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+          const int i = i0 + 4 * k;
+          if (i >= n) break;
+          const float f = lse_s[i];
+          acc.x += f * x[k].x;
+          acc.y += f * x[k].y;
+          acc.z += f * x[k].z;
+          acc.w += f * x[k].w;
+        }
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+          const int i = i0 + 4 * kAhead + 4 * k;
+          if (i < n) x[k] = base[slot_of(p, p.x + i) * step];
         }
       }
       acc_s[grp][c4] = acc;
@@ -938,14 +959,14 @@ __global__ void __launch_bounds__(kJoinThreads) dense_join_kernel(JoinArgs ja) {
 int64_t align256(int64_t n) { return (n + 255) / 256 * 256; }
 
 struct WorkspaceMap {
-  int64_t pre, part_lse, part_o, bsum, bmax, total;
+  int64_t span, part_lse, part_o, bsum, bmax, total;
 };
 
 WorkspaceMap workspace_map(const qsa_cache_t& c, int32_t nq, int32_t hq, bool with_mass) {
   const int64_t G = hq / c.num_kv_heads;
   WorkspaceMap m;
-  m.pre = 0;
-  m.part_lse = align256((int64_t)(nq + 1) * 8);
+  m.span = 0;
+  m.part_lse = align256((int64_t)nq * c.num_kv_heads * 8);
   m.part_o = m.part_lse + align256(2 * kMaxCtas * G * 4);
   m.bsum = m.part_o + align256(2 * kMaxCtas * G * kHeadDim * 4);
   const int64_t tiles = with_mass ? (int64_t)nq * hq * c.max_pages_per_seq * kTilesPerPage : 0;
@@ -961,6 +982,8 @@ int check_shape(const qsa_cache_t* cache, int32_t nq, int32_t hq) {
   if (hq % c.num_kv_heads != 0) return QSA_ERR_INVALID_ARG;
   if (hq / c.num_kv_heads > QSA_MAX_GROUP) return QSA_ERR_UNSUPPORTED;
   if (c.max_pages_per_seq > 0x7fffffff / kPage) return QSA_ERR_UNSUPPORTED;  // positions are int32
+  if (((int64_t)c.max_pages_per_seq * kTilesPerPage + kPieceCost) * c.num_kv_heads > 0x7fffffff / (nq > 0 ? nq : 1))
+    return QSA_ERR_UNSUPPORTED;  // places are int32
   return QSA_OK;
 }
 
@@ -1024,7 +1047,7 @@ extern "C" int qsa_dense_decode(const qsa_cache_t* cache, const void* q, int32_t
   a.q_seq = q_seq;
   a.q_pos = q_pos;
   a.scale_log2 = scale * 1.44269504088896340736f;
-  a.pre = reinterpret_cast<int64_t*>(ws + m.pre);
+  a.span = reinterpret_cast<int2*>(ws + m.span);
   a.part_lse = reinterpret_cast<float*>(ws + m.part_lse);
   a.part_o = reinterpret_cast<float*>(ws + m.part_o);
   a.out = static_cast<__nv_bfloat16*>(out);

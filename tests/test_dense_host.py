@@ -53,6 +53,9 @@ def test_dense_decode_refuses_bad_arguments_before_any_cuda_call():
     assert call(cache=ctypes.byref(odd)) == -2
     huge = cache_struct(mpps=0x7fffffff // 64 + 1)
     assert call(cache=ctypes.byref(huge)) == -2
+    wide = cache_struct(mpps=0x7fffffff // 64)      # 134 million tiles a pair: 8 pairs are 2^30 places, 16 too many
+    assert L.qsa_dense_decode_workspace_bytes(ctypes.byref(wide), 4, 16, 0) > 0
+    assert L.qsa_dense_decode_workspace_bytes(ctypes.byref(wide), 8, 16, 0) == -2
     assert L.qsa_dense_decode_workspace_bytes(cp, 1, 3, 0) == -1
     assert L.qsa_dense_decode_workspace_bytes(None, 1, 16, 0) == -1
 
@@ -165,51 +168,68 @@ def test_rope_plan():
 # ---------------------------------------------------------------- index arithmetic, restated
 
 
-MIN_TILES = 8
+PIECE_COST, MIN_PLACES = 8, 8
 
 
 def shares(T, ctas):
-    n = max(1, min(ctas, -(-T // MIN_TILES)))
-    return n, [T * c // n for c in range(n + 1)]
+    n = min(ctas, max(1, -(-T // MIN_PLACES)))
+    base, rem = divmod(T, n)
+    return n, [c * base + min(c, rem) for c in range(n + 1)], base, rem
 
 
-def share_of(T, n, t):
-    return ((t + 1) * n - 1) // T
+def share_of(base, rem, x):
+    cut = rem * (base + 1)
+    return x // (base + 1) if x < cut else rem + (x - cut) // base
 
 
 @pytest.mark.parametrize("seed", range(40))
 def test_shares_cover_every_tile_once_and_partials_have_slots_of_their_own(seed):
-    """A CTA leaves at most two unfinished pairs, its first and its last; the join
-    finds every piece of a pair in the slot it was written to."""
+    """Every tile is in one CTA's walk; a CTA leaves at most two unfinished pairs,
+    the one it took over and the one it hands on, each in a slot of its own."""
     rng = random.Random(seed)
     hkv = rng.choice([1, 2, 4])
     lens = [rng.choice([0, 1, 16, 17, rng.randint(0, 50), rng.randint(0, 9000)]) for _ in range(rng.randint(1, 90))]
-    tiles = [-(-n // 16) for n in lens]
-    T = sum(tiles) * hkv
+    pairs, T = [], 0                                   # (first place, tiles)
+    for n in lens:
+        for _ in range(hkv if n else 0):
+            pairs.append((T, -(-n // 16)))
+            T += PIECE_COST + -(-n // 16)
     if T == 0:
         return
     ctas = rng.choice([1, 3, 148, 256])
-    n, start = shares(T, ctas)
+    n, start, base, rem = shares(T, ctas)
     assert start[0] == 0 and start[n] == T and all(a < b for a, b in zip(start, start[1:]))
-    for t in range(0, T, max(1, T // 500)):
-        c = share_of(T, n, t)
-        assert start[c] <= t < start[c + 1]
-    begins, b = [], 0
-    for nt in tiles:
-        for _ in range(hkv):
-            begins.append((b, nt))
-            b += nt
-    written = {}
-    for pair, (b, nt) in enumerate(begins):
-        if nt == 0:
-            continue
-        first, last = share_of(T, n, b), share_of(T, n, b + nt - 1)
-        if first == last:
-            continue
-        for c in range(first, last + 1):
-            slot = 2 * c + (1 if b > start[c] else 0)       # as the writing CTA and the join both name it
-            assert slot not in written, (pair, written[slot])
-            written[slot] = pair
+    for x in range(0, T, max(1, T // 500)):
+        c = share_of(base, rem, x)
+        assert start[c] <= x < start[c + 1]
+    done, slots = {}, {}
+    for c in range(n):                                 # the walk of CTA c
+        x0, x1 = start[c], start[c + 1]
+        k = next(i for i, (b, nt) in enumerate(pairs) if b <= x0 < b + PIECE_COST + nt)
+        b, nt = pairs[k]
+        t0, t1 = max(0, x0 - b - PIECE_COST), min(nt, x1 - b - PIECE_COST)
+        while t1 > 0:
+            for t in range(t0, t1):
+                assert (k, t) not in done
+                done[k, t] = c
+            if t0 == 0:                                # this CTA names the pair's CTAs
+                last = c if t1 == nt else share_of(base, rem, b + PIECE_COST + nt - 1)
+                slots.setdefault(k, {})["span"] = (c, last)
+            if not (t0 == 0 and t1 == nt):
+                s = 2 * c + (1 if t0 == 0 else 0)
+                assert all(s not in v.get("slots", {}) for v in slots.values())
+                slots.setdefault(k, {}).setdefault("slots", {})[s] = c
+            if not b + PIECE_COST + nt + PIECE_COST < x1:
+                break
+            k += 1
+            b, nt = pairs[k]
+            t0, t1 = 0, min(nt, x1 - b - PIECE_COST)
+            assert t1 > 0
+    assert len(done) == sum(nt for _, nt in pairs)
+    for k, v in slots.items():                         # the join looks for each piece where it was put
+        first, last = v["span"]
+        if first != last:
+            assert v["slots"] == {2 * c + (1 if c == first else 0): c for c in range(first, last + 1)}
 
 
 @pytest.mark.parametrize("seed", range(60))
