@@ -12,8 +12,8 @@
 // group fills; a tcgen05 tile would have 128 rows, K and V rows interleaved in
 // its operand, and an instruction floor that alone exceeds the copy time.
 //
-// Split.  A tile is 16 tokens of one (query, KV head): 4 micro-blocks, one
-// contiguous run of the page (16 KiB BF16, 8 KiB e4m3).  The tiles of all pairs,
+// Split.  A tile is 16 tokens (BF16) or 32 (e4m3) of one (query, KV head): 4 or 8
+// micro-blocks, one contiguous 16 KiB of the page.  The tiles of all pairs,
 // query-major, form one list that the CTAs (one per SM) share evenly, so ragged
 // lengths leave no SM idle; the lengths are read on the device (no host copy of
 // q_pos).  A pair inside one CTA is written to out / lse at once; of the others
@@ -21,25 +21,23 @@
 // 2 CTAs x 16 rows of workspace whatever the batch, and a second small kernel
 // joins them and adds up the weights.
 //
-// CTA = 6 (BF16) or 7 (e4m3) consumer warps + 1 copy warp: with 8 warps or
-// fewer a thread may hold 255 registers, and the 16 x 256 accumulator takes 128.
-// The copy warp resolves 32 tiles' pages at once, one batch ahead, and a lane
-// each moves a tile with bulk copies into a ring of 12 or 21 tiles; it also
-// brings the Q rows of the next pair.  Tile T goes to consumer warp T % warps,
-// which computes S = Q K^T, a running maximum and sum, and O += P V over all 256
-// dims, with no exchange between warps until the pair's piece ends.
+// CTA = 6 consumer warps + 1 copy warp: with 8 warps or fewer a thread may hold
+// 255 registers, and the 16 x 256 accumulator takes 128.  The copy warp resolves
+// 32 tiles' pages at once, one batch ahead, and a lane each moves a tile (16
+// tokens BF16, 32 e4m3: 16 KiB) with bulk copies into a ring of 12; it also
+// brings the Q rows of the next pair.  Tile T goes to consumer warp T % 6, which
+// computes S = Q K^T, a running maximum and sum, and O += P V over all 256 dims,
+// with no exchange between warps until the pair's piece ends.
 #include "qsa_common.cuh"
 
 namespace {
 
 using namespace qsa;
 
-constexpr int kTile = 16;                        // tokens of a tile
-constexpr int kTileRuns = kTile / kRatio;        // 4 micro-blocks
-constexpr int kTilesPerPage = kPage / kTile;
+constexpr int kStrip = 16;                       // tokens of one matrix product: 4 micro-blocks
+constexpr int kStripRuns = kStrip / kRatio;
+constexpr int kStripsPerPage = kPage / kStrip;
 constexpr int kMaxCtas = 256;                    // partial slots reserved: 2 per CTA
-constexpr int kPieceCost = 8;                    // what a pair costs a CTA beside its tiles, in tiles
-constexpr int kMinPlaces = 8;                    // places a CTA takes at least
 constexpr int kQStride = kHeadDim * 2 + 16;      // Q rows 528 B apart: conflict-free 16-byte fragment reads
 constexpr int kQBytes = 16 * kQStride;
 constexpr int kSlice = 32;                       // dims of O that the warps join at once
@@ -57,13 +55,19 @@ constexpr float kLag = 8.f;
 // e4m3: rows are plain, so runs are placed 32 B apart to spread the banks.
 template <bool F8>
 struct Lay {
-  static constexpr int kWarps = F8 ? 7 : 6;  // consumer warps
+  static constexpr int kWarps = 6;  // consumer warps
   static constexpr int kConsumerThreads = kWarps * 32;
   static constexpr int kThreads = kConsumerThreads + 32;
   static constexpr int kRunBytes = 2 * kRatio * kHeadDim * (F8 ? 1 : 2);
   static constexpr int kRunStride = kRunBytes + (F8 ? 32 : 0);
+  static constexpr int kStrips = F8 ? 2 : 1;  // of a tile
+  static constexpr int kTile = kStrips * kStrip;
+  static constexpr int kTileRuns = kStrips * kStripRuns;
+  static constexpr int kTilesPerPage = kPage / kTile;
   static constexpr int kStageBytes = kTileRuns * kRunStride;
-  static constexpr int kStages = F8 ? 21 : 12;
+  static constexpr int kStages = 12;
+  static constexpr int kPieceCost = F8 ? 5 : 8;  // what a pair costs a CTA beside its tiles, in tiles
+  static constexpr int kMinPlaces = 8;            // places a CTA takes at least
   // Tile T and tile T + kStages, which reuses its stage, belong to one warp: it has
   // seen the stage's last phase end before it waits for the next.  A parity wait
   // cannot tell a phase from the one two before, so another warp could run ahead.
@@ -79,7 +83,7 @@ struct Lay {
   static constexpr int kOffBar = kOffTab + kTab * 8;            // full, empty, Q full [2], Q empty [2]
   static constexpr int kOffAbort = kOffBar + (2 * kStages + 4) * 8;
   static constexpr int kSmem = kOffAbort + 16;
-  static constexpr int kIssue = F8 ? 7 : 3;  // copy-warp lanes that wait and issue together, a tile each
+  static constexpr int kIssue = 3;  // copy-warp lanes that wait and issue together, a tile each
   static_assert(kSmem <= 232448, "shared memory budget");
   static_assert(kWarps * kSlices * kCombWarp * 4 <= kOffQ, "a whole O of every warp fits the ring");
 };
@@ -120,16 +124,20 @@ __device__ __forceinline__ int query_len(const DenseArgs& a, int q, bool report)
   return p + 1;
 }
 
-__device__ __forceinline__ int tiles_of(int len) { return (len + kTile - 1) / kTile; }
+template <class LY>
+__device__ __forceinline__ int tiles_of(int len) {
+  return (len + LY::kTile - 1) / LY::kTile;
+}
 
 // The list that the CTAs share out: every pair takes kPieceCost places (what
 // joining its warps costs beside a tile), then one per tile.
 struct Shares {
   int n, base, rem;  // CTAs; the first `rem` take base + 1 places, the others base
 };
+template <class LY>
 __device__ __forceinline__ Shares make_shares(int total, int ctas) {
   Shares s;
-  s.n = min(ctas, max(1, (total + kMinPlaces - 1) / kMinPlaces));
+  s.n = min(ctas, max(1, (total + LY::kMinPlaces - 1) / LY::kMinPlaces));
   s.base = total / s.n;
   s.rem = total - s.base * s.n;
   return s;
@@ -140,7 +148,10 @@ __device__ __forceinline__ int share_of(const Shares& s, int x) {  // the CTA th
   return x < cut ? x / (s.base + 1) : s.rem + (x - cut) / s.base;
 }
 
-__device__ __forceinline__ int places_of(int len) { return len ? tiles_of(len) + kPieceCost : 0; }
+template <class LY>
+__device__ __forceinline__ int places_of(int len) {
+  return len ? tiles_of<LY>(len) + LY::kPieceCost : 0;
+}
 
 // A CTA's position in the list: a piece of pair (q, g).
 struct Walk {
@@ -152,18 +163,23 @@ struct Walk {
   const int2* tab;
 };
 
+template <class LY>
 __device__ __forceinline__ bool set_span(Walk& w, int x0, int x1) {
-  const int lo = w.begin + kPieceCost;
+  const int lo = w.begin + LY::kPieceCost;
   w.t0 = max(0, x0 - lo);
-  w.t1 = min(tiles_of(w.len), x1 - lo);
+  w.t1 = min(tiles_of<LY>(w.len), x1 - lo);
   return w.t1 > 0;
 }
 
 // Whether tiles of a pair after this one lie in the share.
-__device__ __forceinline__ bool has_next(const Walk& w, int x1) { return w.begin + places_of(w.len) + kPieceCost < x1; }
+template <class LY>
+__device__ __forceinline__ bool has_next(const Walk& w, int x1) {
+  return w.begin + places_of<LY>(w.len) + LY::kPieceCost < x1;
+}
 
+template <class LY>
 __device__ __forceinline__ void next_piece(const DenseArgs& a, Walk& w, int x1) {
-  w.begin += places_of(w.len);
+  w.begin += places_of<LY>(w.len);
   if (w.g + 1 < a.hkv) {
     ++w.g;
   } else {
@@ -176,7 +192,7 @@ __device__ __forceinline__ void next_piece(const DenseArgs& a, Walk& w, int x1) 
     } while (w.len == 0);
     w.g = 0;
   }
-  set_span(w, 0, x1);
+  set_span<LY>(w, 0, x1);
 }
 
 // Bounded wait; false (and the abort flag) when the limit passed.
@@ -230,7 +246,7 @@ __device__ void copy_warp(const DenseArgs& a, uint8_t* smem, Walk w, int x1) {
     // lane = tile: pages of 32 tiles at a time, the next batch's loads issued before this batch's copies
     auto lookup = [&](int t) {
       int page = -1;
-      if (t < w.t1) page = __ldg(a.bt + (int64_t)w.seq * a.mpps + t / kTilesPerPage);
+      if (t < w.t1) page = __ldg(a.bt + (int64_t)w.seq * a.mpps + t / LY::kTilesPerPage);
       return page;
     };
     int page = lookup(w.t0 + lane);
@@ -239,10 +255,10 @@ __device__ void copy_warp(const DenseArgs& a, uint8_t* smem, Walk w, int x1) {
       const int n = min(32, w.t1 - tb), t = tb + lane;
       const bool bad = page < 0 || page >= a.num_pages;
       if (lane < n && bad) flag(a.st, QSA_DEV_BAD_PAGE);
-      const int tok = min(kTile, w.len - t * kTile);
+      const int tok = min(LY::kTile, w.len - t * LY::kTile);
       const int runs = (tok + kRatio - 1) / kRatio;  // whole micro-blocks that hold a token
       const uint8_t* src = a.kv + (((size_t)page * a.hkv + w.g) * kBlocksPerPage +
-                                   (size_t)(t % kTilesPerPage) * kTileRuns) * LY::kRunBytes;
+                                   (size_t)(t % LY::kTilesPerPage) * LY::kTileRuns) * LY::kRunBytes;
       const uint32_t mine = T + lane;
       const int stage = (int)(mine % LY::kStages);
       const uint32_t bar = full + stage * 8, dst = ring + stage * LY::kStageBytes;
@@ -264,7 +280,7 @@ __device__ void copy_warp(const DenseArgs& a, uint8_t* smem, Walk w, int x1) {
             mbar_arrive_expect_tx(bar, runs * LY::kRunBytes);
             if constexpr (F8) {
 #pragma unroll
-              for (int r = 0; r < kTileRuns; ++r)
+              for (int r = 0; r < LY::kTileRuns; ++r)
                 if (r < runs) bulk_g2s(dst + r * LY::kRunStride, src + r * LY::kRunBytes, LY::kRunBytes, bar, policy);
             } else {
               bulk_g2s(dst, src, runs * LY::kRunBytes, bar, policy);
@@ -277,8 +293,8 @@ __device__ void copy_warp(const DenseArgs& a, uint8_t* smem, Walk w, int x1) {
       page = page_next;
     }
     if (!stop) {
-      more = has_next(w, x1);
-      if (more) next_piece(a, w, x1);
+      more = has_next<LY>(w, x1);
+      if (more) next_piece<LY>(a, w, x1);
     }
   }
   // never leave the CTA with copies in flight: each lane waits for one stage's last copy
@@ -341,7 +357,7 @@ __device__ void consumers(const DenseArgs& a, uint8_t* smem, Walk w, const Share
   float* row_scale = reinterpret_cast<float*>(smem + LY::kOffScale);
   constexpr int kWarps = LY::kWarps, kConsumerThreads = LY::kConsumerThreads;
   const int G = a.G;
-  const int64_t max_tiles = (int64_t)a.mpps * kTilesPerPage;
+  const int64_t max_strips = (int64_t)a.mpps * kStripsPerPage;
 
   // K: column n = gq of n-tile j, V: this lane's tokens (j, e)
   const int ke = gq & 1, kt = gq >> 1;
@@ -413,11 +429,15 @@ __device__ void consumers(const DenseArgs& a, uint8_t* smem, Walk w, const Share
       if (!__all_sync(0xffffffffu, got)) break;
       const int nv = valid[stage];
       const uint32_t kb = ring + stage * LY::kStageBytes;
+      constexpr int kS = LY::kStrips;
+      constexpr uint32_t kStripBytes = kStripRuns * LY::kRunStride;
 
-      // ---- S = Q K^T, two n-tiles of 8 tokens
-      float s[2][4];
+      // ---- S = Q K^T, two n-tiles of 8 tokens per strip
+      float s[kS][2][4];
 #pragma unroll
-      for (int j = 0; j < 2; ++j) s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.f;
+      for (int b = 0; b < kS; ++b)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) s[b][j][0] = s[b][j][1] = s[b][j][2] = s[b][j][3] = 0.f;
       if constexpr (F8) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {  // 64 dims: lane tq holds dims 64i + 16tq .. + 15
@@ -425,16 +445,21 @@ __device__ void consumers(const DenseArgs& a, uint8_t* smem, Walk w, const Share
           const uint4 qa0 = lds128(qb + gq * kQStride + qo), qa1 = lds128(qb + gq * kQStride + qo + 16);
           const uint4 qc0 = lds128(qb + (gq + 8) * kQStride + qo), qc1 = lds128(qb + (gq + 8) * kQStride + qo + 16);
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const uint4 kk = lds128(kb + k_off[j] + (4 * i + tq) * 16);
-            const uint4 k0 = e4m3x8_to_f16x8(make_uint2(kk.x, kk.y)), k1 = e4m3x8_to_f16x8(make_uint2(kk.z, kk.w));
-            mma_f16_16816(s[j], qa0.x, qc0.x, qa0.y, qc0.y, k0.x, k0.y);
-            mma_f16_16816(s[j], qa0.z, qc0.z, qa0.w, qc0.w, k0.z, k0.w);
-            mma_f16_16816(s[j], qa1.x, qc1.x, qa1.y, qc1.y, k1.x, k1.y);
-            mma_f16_16816(s[j], qa1.z, qc1.z, qa1.w, qc1.w, k1.z, k1.w);
-          }
+          for (int b = 0; b < kS; ++b)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const uint4 kk = lds128(kb + b * kStripBytes + k_off[j] + (4 * i + tq) * 16);
+              const uint4 k0 = e4m3x8_to_f16x8(make_uint2(kk.x, kk.y)), k1 = e4m3x8_to_f16x8(make_uint2(kk.z, kk.w));
+              mma_f16_16816(s[b][j], qa0.x, qc0.x, qa0.y, qc0.y, k0.x, k0.y);
+              mma_f16_16816(s[b][j], qa0.z, qc0.z, qa0.w, qc0.w, k0.z, k0.w);
+              mma_f16_16816(s[b][j], qa1.x, qc1.x, qa1.y, qc1.y, k1.x, k1.y);
+              mma_f16_16816(s[b][j], qa1.z, qc1.z, qa1.w, qc1.w, k1.z, k1.w);
+            }
         }
       } else {
+        float s2[2][4];  // a second accumulator each: half the chain of dependent products
+#pragma unroll
+        for (int j = 0; j < 2; ++j) s2[j][0] = s2[j][1] = s2[j][2] = s2[j][3] = 0.f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {  // 32 dims of atom i / 2: lane tq holds chunk 2tq + i % 2
           const int ch = 2 * tq + (i & 1);
@@ -443,28 +468,42 @@ __device__ void consumers(const DenseArgs& a, uint8_t* smem, Walk w, const Share
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             const uint4 kk = lds128(kb + k_off[j] + (i >> 1) * 1024 + ((ch ^ kr0) << 4));
-            mma_bf16_16816(s[j], qa.x, qc.x, qa.y, qc.y, kk.x, kk.y);
-            mma_bf16_16816(s[j], qa.z, qc.z, qa.w, qc.w, kk.z, kk.w);
+            mma_bf16_16816(s[0][j], qa.x, qc.x, qa.y, qc.y, kk.x, kk.y);
+            mma_bf16_16816(s2[j], qa.z, qc.z, qa.w, qc.w, kk.z, kk.w);
           }
         }
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) s[0][j][c] += s2[j][c];
       }
-      // ---- mask, running maximum and sum (base 2)
-      bool ok[2][2];
+      // ---- mask, running maximum and sum (base 2; the scale is positive, so the largest
+      // product is the largest logit)
+      const bool whole = nv == LY::kTile;
+      auto seen = [&](int b, int j, int e) {
+        return b * kStrip + tile_run<F8>(j, tq, e) * kRatio + tile_row<F8>(j, tq, e) < nv;
+      };
+      if (!whole) {
+#pragma unroll
+        for (int b = 0; b < kS; ++b)
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              if (!seen(b, j, e)) s[b][j][e] = s[b][j][2 + e] = -INFINITY;
+      }
       float r0 = -INFINITY, r1 = -INFINITY;
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
+      for (int b = 0; b < kS; ++b)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          ok[j][e] = tile_run<F8>(j, tq, e) * kRatio + tile_row<F8>(j, tq, e) < nv;
-          s[j][e] = ok[j][e] ? s[j][e] * sc0 : -INFINITY;
-          s[j][2 + e] = ok[j][e] ? s[j][2 + e] * sc1 : -INFINITY;
-          r0 = fmaxf(r0, s[j][e]);
-          r1 = fmaxf(r1, s[j][2 + e]);
+        for (int j = 0; j < 2; ++j) {
+          r0 = fmaxf(r0, fmaxf(s[b][j][0], s[b][j][1]));
+          r1 = fmaxf(r1, fmaxf(s[b][j][2], s[b][j][3]));
         }
       r0 = fmaxf(r0, __shfl_xor_sync(0xffffffffu, r0, 1));
       r1 = fmaxf(r1, __shfl_xor_sync(0xffffffffu, r1, 1));
-      r0 = fmaxf(r0, __shfl_xor_sync(0xffffffffu, r0, 2));
-      r1 = fmaxf(r1, __shfl_xor_sync(0xffffffffu, r1, 2));
+      r0 = fmaxf(r0, __shfl_xor_sync(0xffffffffu, r0, 2)) * sc0;
+      r1 = fmaxf(r1, __shfl_xor_sync(0xffffffffu, r1, 2)) * sc1;
       const bool up0 = r0 > m0 + kLag, up1 = r1 > m1 + kLag;  // -inf + 8 = -inf: the first logit always moves it
       if (__any_sync(0xffffffffu, up0 || up1)) {
         const float n0 = up0 ? r0 : m0, n1 = up1 ? r1 : m1;
@@ -481,96 +520,112 @@ __device__ void consumers(const DenseArgs& a, uint8_t* smem, Walk w, const Share
           o[nt][3] *= al1;
         }
       }
-      // rows that have seen no token yet keep every logit at -inf
-      const float sub0 = m0 == -INFINITY ? 0.f : m0, sub1 = m1 == -INFINITY ? 0.f : m1;
-      float p[2][4];
+      // rows that have seen no token yet keep every weight at 0
+      const float sub0 = m0 == -INFINITY ? 0.f : -m0, sub1 = m1 == -INFINITY ? 0.f : -m1;
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        p[j][0] = exp2_fast(s[j][0] - sub0);
-        p[j][1] = exp2_fast(s[j][1] - sub0);
-        p[j][2] = exp2_fast(s[j][2] - sub1);
-        p[j][3] = exp2_fast(s[j][3] - sub1);
-      }
-      l0 += (p[0][0] + p[0][1]) + (p[1][0] + p[1][1]);
-      l1 += (p[0][2] + p[0][3]) + (p[1][2] + p[1][3]);
+      for (int b = 0; b < kS; ++b) {
+        float(&p)[2][4] = s[b];  // the weights take the products' place
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          p[j][0] = exp2_fast(fmaf(p[j][0], sc0, sub0));
+          p[j][1] = exp2_fast(fmaf(p[j][1], sc0, sub0));
+          p[j][2] = exp2_fast(fmaf(p[j][2], sc1, sub1));
+          p[j][3] = exp2_fast(fmaf(p[j][3], sc1, sub1));
+        }
+        if (!whole) {  // also where a scale has underflowed to 0
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              if (!seen(b, j, e)) p[j][e] = p[j][2 + e] = 0.f;
+        }
+        l0 += (p[0][0] + p[0][1]) + (p[1][0] + p[1][1]);
+        l1 += (p[0][2] + p[0][3]) + (p[1][2] + p[1][3]);
 
-      // ---- weight of each micro-block: sums over its 4 tokens, one per quad lane
-      if (a.bsum) {
-        float b0, b1;
-        if constexpr (F8) {  // lane tq has rows 0, 2 of run tq and rows 1, 3 of run tq ^ 2
-          b0 = p[0][0] + p[1][0] + __shfl_xor_sync(0xffffffffu, p[0][1] + p[1][1], 2);
-          b1 = p[0][2] + p[1][2] + __shfl_xor_sync(0xffffffffu, p[0][3] + p[1][3], 2);
-        } else {  // run 2j + e over the quad: halve the runs a lane carries twice
-          const bool hi = tq & 2, odd = tq & 1;
-          const float a0 = (hi ? p[1][0] : p[0][0]) + __shfl_xor_sync(0xffffffffu, hi ? p[0][0] : p[1][0], 2);
-          const float a1 = (hi ? p[1][1] : p[0][1]) + __shfl_xor_sync(0xffffffffu, hi ? p[0][1] : p[1][1], 2);
-          const float c0 = (hi ? p[1][2] : p[0][2]) + __shfl_xor_sync(0xffffffffu, hi ? p[0][2] : p[1][2], 2);
-          const float c1 = (hi ? p[1][3] : p[0][3]) + __shfl_xor_sync(0xffffffffu, hi ? p[0][3] : p[1][3], 2);
-          b0 = (odd ? a1 : a0) + __shfl_xor_sync(0xffffffffu, odd ? a0 : a1, 1);
-          b1 = (odd ? c1 : c0) + __shfl_xor_sync(0xffffffffu, odd ? c0 : c1, 1);
-        }
-        const int64_t base = ((int64_t)w.q * a.hq + (int64_t)w.g * G) * max_tiles + w.t0 + ti;
-        if (gq < G) {
-          const int64_t at = base + gq * max_tiles;
-          a.bsum[at * 4 + tq] = b0;
-          if (tq == 0) a.bmax[at] = m0;
-        }
-        if (gq + 8 < G) {
-          const int64_t at = base + (gq + 8) * max_tiles;
-          a.bsum[at * 4 + tq] = b1;
-          if (tq == 0) a.bmax[at] = m1;
+        // ---- weight of each micro-block: sums over its 4 tokens, one per quad lane
+        if (a.bsum) {
+          float b0, b1;
+          if constexpr (F8) {  // lane tq has rows 0, 2 of run tq and rows 1, 3 of run tq ^ 2
+            b0 = p[0][0] + p[1][0] + __shfl_xor_sync(0xffffffffu, p[0][1] + p[1][1], 2);
+            b1 = p[0][2] + p[1][2] + __shfl_xor_sync(0xffffffffu, p[0][3] + p[1][3], 2);
+          } else {  // run 2j + e over the quad: halve the runs a lane carries twice
+            const bool hi = tq & 2, odd = tq & 1;
+            const float a0 = (hi ? p[1][0] : p[0][0]) + __shfl_xor_sync(0xffffffffu, hi ? p[0][0] : p[1][0], 2);
+            const float a1 = (hi ? p[1][1] : p[0][1]) + __shfl_xor_sync(0xffffffffu, hi ? p[0][1] : p[1][1], 2);
+            const float c0 = (hi ? p[1][2] : p[0][2]) + __shfl_xor_sync(0xffffffffu, hi ? p[0][2] : p[1][2], 2);
+            const float c1 = (hi ? p[1][3] : p[0][3]) + __shfl_xor_sync(0xffffffffu, hi ? p[0][3] : p[1][3], 2);
+            b0 = (odd ? a1 : a0) + __shfl_xor_sync(0xffffffffu, odd ? a0 : a1, 1);
+            b1 = (odd ? c1 : c0) + __shfl_xor_sync(0xffffffffu, odd ? c0 : c1, 1);
+          }
+          const int64_t base = ((int64_t)w.q * a.hq + (int64_t)w.g * G) * max_strips + (int64_t)(w.t0 + ti) * kS + b;
+          if (gq < G) {
+            const int64_t at = base + gq * max_strips;
+            a.bsum[at * 4 + tq] = b0;
+            if (tq == 0) a.bmax[at] = m0;
+          }
+          if (gq + 8 < G) {
+            const int64_t at = base + (gq + 8) * max_strips;
+            a.bsum[at * 4 + tq] = b1;
+            if (tq == 0) a.bmax[at] = m1;
+          }
         }
       }
 
       // ---- O += P V.  BF16 V: the weights enter as a BF16 hi + lo pair (about 17
-      // significant bits; 8 alone would show in short contexts).  e4m3 V: FP16 weights,
-      // 11 bits against the cache's 4.
-      uint32_t pa[4], pl[4];
-      if constexpr (F8) {
-        pa[0] = pack_f16_sat(p[0][0], p[0][1]);
-        pa[1] = pack_f16_sat(p[0][2], p[0][3]);
-        pa[2] = pack_f16_sat(p[1][0], p[1][1]);
-        pa[3] = pack_f16_sat(p[1][2], p[1][3]);
-      } else {
-        split_bf16(p[0][0], p[0][1], pa[0], pl[0]);
-        split_bf16(p[0][2], p[0][3], pa[1], pl[1]);
-        split_bf16(p[1][0], p[1][1], pa[2], pl[2]);
-        split_bf16(p[1][2], p[1][3], pa[3], pl[3]);
-      }
-      const bool whole = nv == kTile;
-      constexpr int kSlices = F8 ? 2 : 4;  // e4m3: 128 dims per 16-byte read of the 8 column groups; BF16: 64
+      // significant bits; 8 alone would show in short contexts).  e4m3 V: FP16 weights
+      // (at most 2^8), 11 bits against the cache's 4.
+      uint32_t pa[kS][4], pl[4];
 #pragma unroll
-      for (int c = 0; c < kSlices; ++c) {
-        uint4 x[2][2];
+      for (int b = 0; b < kS; ++b)
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            x[j][e] = lds128(kb + v_off[j][e] + c * (F8 ? 128 : 1024));
-            if (!whole && !ok[j][e]) x[j][e] = make_uint4(0, 0, 0, 0);  // rows behind the end may hold anything
-          }
-        const uint32_t x00[4] = {x[0][0].x, x[0][0].y, x[0][0].z, x[0][0].w};
-        const uint32_t x01[4] = {x[0][1].x, x[0][1].y, x[0][1].z, x[0][1].w};
-        const uint32_t x10[4] = {x[1][0].x, x[1][0].y, x[1][0].z, x[1][0].w};
-        const uint32_t x11[4] = {x[1][1].x, x[1][1].y, x[1][1].z, x[1][1].w};
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          if constexpr (F8) {  // 4 dims: the two tokens' bytes are paired, then widened
-            const uint2 t0 = e4m3x4_to_f16x4(__byte_perm(x00[r], x01[r], 0x5140));
-            const uint2 t1 = e4m3x4_to_f16x4(__byte_perm(x00[r], x01[r], 0x7362));
-            const uint2 u0 = e4m3x4_to_f16x4(__byte_perm(x10[r], x11[r], 0x5140));
-            const uint2 u1 = e4m3x4_to_f16x4(__byte_perm(x10[r], x11[r], 0x7362));
-            mma_f16_16816(o[c * 16 + 4 * r + 0], pa[0], pa[1], pa[2], pa[3], t0.x, u0.x);
-            mma_f16_16816(o[c * 16 + 4 * r + 1], pa[0], pa[1], pa[2], pa[3], t0.y, u0.y);
-            mma_f16_16816(o[c * 16 + 4 * r + 2], pa[0], pa[1], pa[2], pa[3], t1.x, u1.x);
-            mma_f16_16816(o[c * 16 + 4 * r + 3], pa[0], pa[1], pa[2], pa[3], t1.y, u1.y);
+        for (int k = 0; k < 4; ++k) {
+          const float x = s[b][k >> 1][2 * (k & 1)], y = s[b][k >> 1][2 * (k & 1) + 1];
+          if constexpr (F8) {
+            const __half2 h = __floats2half2_rn(x, y);
+            pa[b][k] = *reinterpret_cast<const uint32_t*>(&h);
           } else {
-            const uint32_t lo0 = __byte_perm(x00[r], x01[r], 0x5410), hi0 = __byte_perm(x00[r], x01[r], 0x7632);
-            const uint32_t lo1 = __byte_perm(x10[r], x11[r], 0x5410), hi1 = __byte_perm(x10[r], x11[r], 0x7632);
-            mma_bf16_16816(o[c * 8 + 2 * r], pa[0], pa[1], pa[2], pa[3], lo0, lo1);
-            mma_bf16_16816(o[c * 8 + 2 * r + 1], pa[0], pa[1], pa[2], pa[3], hi0, hi1);
-            mma_bf16_16816(o[c * 8 + 2 * r], pl[0], pl[1], pl[2], pl[3], lo0, lo1);
-            mma_bf16_16816(o[c * 8 + 2 * r + 1], pl[0], pl[1], pl[2], pl[3], hi0, hi1);
+            split_bf16(x, y, pa[b][k], pl[k]);
+          }
+        }
+      constexpr int kParts = F8 ? 2 : 4;  // e4m3: 128 dims per 16-byte read of the 8 column groups; BF16: 64
+#pragma unroll
+      for (int c = 0; c < kParts; ++c) {
+#pragma unroll
+        for (int b = 0; b < kS; ++b) {
+          uint32_t x[2][2][4];
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              uint4 v = lds128(kb + b * kStripBytes + v_off[j][e] + c * (F8 ? 128 : 1024));
+              if (!whole && !seen(b, j, e)) v = make_uint4(0, 0, 0, 0);  // rows behind the end may hold anything
+              x[j][e][0] = v.x;
+              x[j][e][1] = v.y;
+              x[j][e][2] = v.z;
+              x[j][e][3] = v.w;
+            }
+          const uint32_t(&pb)[4] = pa[b];
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            if constexpr (F8) {  // 4 dims: the two tokens' bytes are paired, then widened
+              const uint2 t0 = e4m3x4_to_f16x4(__byte_perm(x[0][0][r], x[0][1][r], 0x5140));
+              const uint2 t1 = e4m3x4_to_f16x4(__byte_perm(x[0][0][r], x[0][1][r], 0x7362));
+              const uint2 u0 = e4m3x4_to_f16x4(__byte_perm(x[1][0][r], x[1][1][r], 0x5140));
+              const uint2 u1 = e4m3x4_to_f16x4(__byte_perm(x[1][0][r], x[1][1][r], 0x7362));
+              mma_f16_16816(o[c * 16 + 4 * r + 0], pb[0], pb[1], pb[2], pb[3], t0.x, u0.x);
+              mma_f16_16816(o[c * 16 + 4 * r + 1], pb[0], pb[1], pb[2], pb[3], t0.y, u0.y);
+              mma_f16_16816(o[c * 16 + 4 * r + 2], pb[0], pb[1], pb[2], pb[3], t1.x, u1.x);
+              mma_f16_16816(o[c * 16 + 4 * r + 3], pb[0], pb[1], pb[2], pb[3], t1.y, u1.y);
+            } else {
+              const uint32_t lo0 = __byte_perm(x[0][0][r], x[0][1][r], 0x5410);
+              const uint32_t hi0 = __byte_perm(x[0][0][r], x[0][1][r], 0x7632);
+              const uint32_t lo1 = __byte_perm(x[1][0][r], x[1][1][r], 0x5410);
+              const uint32_t hi1 = __byte_perm(x[1][0][r], x[1][1][r], 0x7632);
+              mma_bf16_16816(o[c * 8 + 2 * r], pb[0], pb[1], pb[2], pb[3], lo0, lo1);
+              mma_bf16_16816(o[c * 8 + 2 * r + 1], pb[0], pb[1], pb[2], pb[3], hi0, hi1);
+              mma_bf16_16816(o[c * 8 + 2 * r], pl[0], pl[1], pl[2], pl[3], lo0, lo1);
+              mma_bf16_16816(o[c * 8 + 2 * r + 1], pl[0], pl[1], pl[2], pl[3], hi0, hi1);
+            }
           }
         }
       }
@@ -610,7 +665,7 @@ __device__ void consumers(const DenseArgs& a, uint8_t* smem, Walk w, const Share
     }
     // whole pair here: straight to out; else to the partial slot of the pair that this
     // CTA took over (0) or leaves unfinished (1)
-    const int nt_pair = tiles_of(w.len);
+    const int nt_pair = tiles_of<LY>(w.len);
     const bool direct = w.t0 == 0 && w.t1 == nt_pair;
     const int slot = 2 * blockIdx.x + (w.t0 == 0 ? 1 : 0);
     if (warp == 0 && tq == 0) {
@@ -627,11 +682,11 @@ __device__ void consumers(const DenseArgs& a, uint8_t* smem, Walk w, const Share
     }
     if (w.t0 == 0 && tid == 0)
       a.span[w.q * a.hkv + w.g] =
-          make_int2(blockIdx.x, direct ? blockIdx.x : share_of(sh, w.begin + kPieceCost + nt_pair - 1));
+          make_int2(blockIdx.x, direct ? blockIdx.x : share_of(sh, w.begin + LY::kPieceCost + nt_pair - 1));
     // O: slices of 32 dims go through shared memory, every warp's to its own place, and a
     // thread adds up one float4 of them.  After the share's last piece the ring is free and
     // takes all the slices at once; before, one slice at a time.
-    const bool last = !has_next(w, x1);
+    const bool last = !has_next<LY>(w, x1);
     const size_t out_row = direct ? (size_t)w.q * a.hq + (size_t)w.g * G : (size_t)slot * G;
     auto add_up = [&](const float* base, int sl, int item) {
       const int row = item >> 3, col = (item & 7) * 4;
@@ -669,6 +724,7 @@ __device__ void consumers(const DenseArgs& a, uint8_t* smem, Walk w, const Share
         for (int hr = 0; hr < 2; ++hr)
 #pragma unroll
           for (int k = 0; k < 2; ++k)
+            if (8 * hr < G)
             *reinterpret_cast<float4*>(put_at + sl * put_step + 8 * hr * kCombRow + 4 * k) =
                 make_float4(o[i0 + 4 * k][2 * hr + e] * fac[hr], o[i0 + 4 * k + 1][2 * hr + e] * fac[hr],
                             o[i0 + 4 * k + 2][2 * hr + e] * fac[hr], o[i0 + 4 * k + 3][2 * hr + e] * fac[hr]);
@@ -686,7 +742,7 @@ __device__ void consumers(const DenseArgs& a, uint8_t* smem, Walk w, const Share
         add_up(reinterpret_cast<float*>(smem) + (i >> 7) * kWarps * LY::kCombWarp, i >> 7, i & 127);
       break;
     }
-    next_piece(a, w, x1);
+    next_piece<LY>(a, w, x1);
   }
 }
 
@@ -720,7 +776,7 @@ __global__ void __launch_bounds__(Lay<F8>::kThreads, 1) dense_decode_kernel(Dens
   auto scan_round = [&](int base, bool report) {  // places before query base + tid; total moves on
     const int q = base + tid;
     len = q < a.nq ? query_len(a, q, report) : 0;
-    const int n = places_of(len) * a.hkv;
+    const int n = places_of<LY>(len) * a.hkv;
     int inc = n;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -745,11 +801,11 @@ __global__ void __launch_bounds__(Lay<F8>::kThreads, 1) dense_decode_kernel(Dens
       for (int g = 0; g < a.hkv; ++g) a.span[(b + tid) * a.hkv + g] = make_int2(0, -1);
   }
   if (total == 0) return;
-  const Shares sh = make_shares(total, a.ctas);
+  const Shares sh = make_shares<LY>(total, a.ctas);
   if ((int)blockIdx.x >= sh.n) return;
   const int x0 = share_begin(sh, blockIdx.x), x1 = share_begin(sh, blockIdx.x + 1);
   auto find_first = [&](int base) {  // the query that holds place x0
-    if (len > 0 && first <= x0 && x0 < first + places_of(len) * a.hkv) {
+    if (len > 0 && first <= x0 && x0 < first + places_of<LY>(len) * a.hkv) {
       plan[0] = base + tid;
       plan[1] = first;
     }
@@ -775,9 +831,9 @@ __global__ void __launch_bounds__(Lay<F8>::kThreads, 1) dense_decode_kernel(Dens
   }
   w.len = tab[w.q - w.q_tab].x;
   w.seq = tab[w.q - w.q_tab].y;
-  w.g = (x0 - w.begin) / places_of(w.len);
-  w.begin += w.g * places_of(w.len);
-  if (!set_span(w, x0, x1)) return;  // the share ends before the pair's first tile
+  w.g = (x0 - w.begin) / places_of<LY>(w.len);
+  w.begin += w.g * places_of<LY>(w.len);
+  if (!set_span<LY>(w, x0, x1)) return;  // the share ends before the pair's first tile
   if (warp < kWarps)
     consumers<F8>(a, smem, w, sh, x1);
   else
@@ -917,7 +973,7 @@ __global__ void __launch_bounds__(kJoinThreads) dense_join_kernel(JoinArgs ja) {
   for (int q = 0; q < q0; ++q)
     if (a.q_seq[q] == seq && query_len(a, q, false) > 0) return;
   const int tile = (int)(wb % ja.mass_blocks) * kJoinThreads + tid;
-  const int64_t max_tiles = (int64_t)a.mpps * kTilesPerPage;
+  const int64_t max_tiles = (int64_t)a.mpps * kStripsPerPage;
   float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
   int longest = 0;
   for (int q = q0; q < a.nq; ++q) {
@@ -931,7 +987,7 @@ __global__ void __launch_bounds__(kJoinThreads) dense_join_kernel(JoinArgs ja) {
         if ((tid & 31) == 0) lse_s[h - h0] = v;
       }
       __syncthreads();
-      if (tile < tiles_of(len)) {
+      if (tile < (len + kStrip - 1) / kStrip) {
         for (int h = h0; h < min(a.hq, h0 + kMaxCtas); ++h) {
           const int64_t at = ((int64_t)q * a.hq + h) * max_tiles + tile;
           const float l2 = lse_s[h - h0], bm = a.bmax[at];
@@ -951,7 +1007,7 @@ __global__ void __launch_bounds__(kJoinThreads) dense_join_kernel(JoinArgs ja) {
   const int64_t row = (int64_t)seq * ja.mass_ld;
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    const int b = tile * kTileRuns + k;
+    const int b = tile * kStripRuns + k;
     if (b < blocks) ja.mass_out[row + b] = ja.decay * ja.mass_in[row + b] + v[k];
   }
 }
@@ -969,7 +1025,7 @@ WorkspaceMap workspace_map(const qsa_cache_t& c, int32_t nq, int32_t hq, bool wi
   m.part_lse = align256((int64_t)nq * c.num_kv_heads * 8);
   m.part_o = m.part_lse + align256(2 * kMaxCtas * G * 4);
   m.bsum = m.part_o + align256(2 * kMaxCtas * G * kHeadDim * 4);
-  const int64_t tiles = with_mass ? (int64_t)nq * hq * c.max_pages_per_seq * kTilesPerPage : 0;
+  const int64_t tiles = with_mass ? (int64_t)nq * hq * c.max_pages_per_seq * kStripsPerPage : 0;
   m.bmax = m.bsum + align256(tiles * 16);
   m.total = m.bmax + align256(tiles * 4);
   return m;
@@ -982,7 +1038,7 @@ int check_shape(const qsa_cache_t* cache, int32_t nq, int32_t hq) {
   if (hq % c.num_kv_heads != 0) return QSA_ERR_INVALID_ARG;
   if (hq / c.num_kv_heads > QSA_MAX_GROUP) return QSA_ERR_UNSUPPORTED;
   if (c.max_pages_per_seq > 0x7fffffff / kPage) return QSA_ERR_UNSUPPORTED;  // positions are int32
-  if (((int64_t)c.max_pages_per_seq * kTilesPerPage + kPieceCost) * c.num_kv_heads > 0x7fffffff / (nq > 0 ? nq : 1))
+  if (((int64_t)c.max_pages_per_seq * kStripsPerPage + 8) * c.num_kv_heads > 0x7fffffff / (nq > 0 ? nq : 1))
     return QSA_ERR_UNSUPPORTED;  // places are int32
   return QSA_OK;
 }
@@ -1062,7 +1118,7 @@ extern "C" int qsa_dense_decode(const qsa_cache_t* cache, const void* q, int32_t
   j.mass_out = mass_out;
   j.mass_ld = mass_ld;
   j.decay = decay;
-  const int64_t tiles = (int64_t)c.max_pages_per_seq * kTilesPerPage;
+  const int64_t tiles = (int64_t)c.max_pages_per_seq * kStripsPerPage;
   j.mass_blocks = (int32_t)((tiles + kJoinThreads - 1) / kJoinThreads);
   const int64_t grid = (int64_t)nq * hq + (mass ? (int64_t)nq * j.mass_blocks : 0);
   if (grid > 0x7fffffff) return QSA_ERR_UNSUPPORTED;
