@@ -713,34 +713,38 @@ __device__ void consumers(const DenseArgs& a, uint8_t* smem, Walk w, const Share
     //       slice sl takes e = sl & 1.
     // e4m3: n-tile 16c + i, column 2tq + e, dim 128c + 32tq + 16e + i: slice sl takes
     //       c = sl >> 2, e = (sl >> 1) & 1 and i = 8 (sl & 1) .. + 7.
-    float* const put_at = (last ? reinterpret_cast<float*>(smem) : comb) + rank * LY::kCombWarp + gq * kCombRow + 8 * tq;
-    const int put_step = last ? kWarps * LY::kCombWarp : 0;
+    auto put = [&](float* base, int sl) {
+      const int e = F8 ? (sl >> 1) & 1 : sl & 1;
+      const int i0 = F8 ? 16 * (sl >> 2) + 8 * (sl & 1) : 8 * (sl >> 1);
+      float* at = base + rank * LY::kCombWarp + gq * kCombRow + 8 * tq;
 #pragma unroll
-    for (int sl = 0; sl < kSlices; ++sl) {
-      if (rank < nw) {
-        const int e = F8 ? (sl >> 1) & 1 : sl & 1;
-        const int i0 = F8 ? 16 * (sl >> 2) + 8 * (sl & 1) : 8 * (sl >> 1);
-#pragma unroll
-        for (int hr = 0; hr < 2; ++hr)
+      for (int hr = 0; hr < 2; ++hr)
+        if (8 * hr < G) {
 #pragma unroll
           for (int k = 0; k < 2; ++k)
-            if (8 * hr < G)
-            *reinterpret_cast<float4*>(put_at + sl * put_step + 8 * hr * kCombRow + 4 * k) =
+            *reinterpret_cast<float4*>(at + 8 * hr * kCombRow + 4 * k) =
                 make_float4(o[i0 + 4 * k][2 * hr + e] * fac[hr], o[i0 + 4 * k + 1][2 * hr + e] * fac[hr],
                             o[i0 + 4 * k + 2][2 * hr + e] * fac[hr], o[i0 + 4 * k + 3][2 * hr + e] * fac[hr]);
-      }
-      if (!last) {
-        named_bar_sync(kBarConsumers, kConsumerThreads);
-        if (tid < 128) add_up(comb, sl, tid);
-        named_bar_sync(kBarConsumers, kConsumerThreads);
-      }
-    }
+        }
+    };
     if (last) {
+      float* const ring_f = reinterpret_cast<float*>(smem);
+      if (rank < nw) {
+#pragma unroll
+        for (int sl = 0; sl < kSlices; ++sl) put(ring_f + sl * kWarps * LY::kCombWarp, sl);
+      }
       named_bar_sync(kBarConsumers, kConsumerThreads);
 #pragma unroll 1
       for (int i = tid; i < kSlices * 128; i += kConsumerThreads)
-        add_up(reinterpret_cast<float*>(smem) + (i >> 7) * kWarps * LY::kCombWarp, i >> 7, i & 127);
+        add_up(ring_f + (i >> 7) * kWarps * LY::kCombWarp, i >> 7, i & 127);
       break;
+    }
+#pragma unroll
+    for (int sl = 0; sl < kSlices; ++sl) {
+      if (rank < nw) put(comb, sl);
+      named_bar_sync(kBarConsumers, kConsumerThreads);
+      if (tid < 128) add_up(comb, sl, tid);
+      named_bar_sync(kBarConsumers, kConsumerThreads);
     }
     next_piece<LY>(a, w, x1);
   }
