@@ -10,18 +10,21 @@
 // together.
 //
 // evict_select_kernel, one CTA per sequence: radix select of the cut (11 + 11 +
-// 10 bits of the order-preserving key), then one ordered pass that writes the
-// kept indices, the number kept before every page, and the moved mass row.
+// 10 bits of the order-preserving key) over masses held in registers, then one
+// ordered pass that writes the kept indices, the number kept before every page,
+// and the moved mass row.
 //
-// evict_move_kernel, one CTA per (sequence, destination page, KV head).  What
-// bounds it is the traffic: each kept run is read once and written once.  The
-// move is in place (or into other pages), so a page may be written only when
+// evict_move_kernel: units of one destination page and KV head (16 runs, 64 KiB
+// BF16) are claimed by warps, three to a CTA and one CTA per SM, each with a
+// buffer of its own in shared memory; lane b moves block b with bulk copies.
+// What bounds it is the traffic: each kept run is read once and written once.
+// The move is in place (or into other pages), so a page may be written only when
 // the blocks it held have been read.  Kept blocks move towards lower indices
-// only; hence page c's old blocks go to pages <= c, and a CTA that has read its
-// own 16 blocks into registers has only to wait until the one or two lower
-// pages that took blocks out of page c have been read as well.  CTAs take their
-// work by ticket, lower pages first, and read before they wait, so every wait
-// is for a CTA that is running and reads without waiting.
+// only; hence page c's old blocks go to pages <= c, and a warp that has read its
+// own 16 blocks has only to wait until the one or two lower pages that took
+// blocks out of page c have been read as well.  Units are claimed by ticket,
+// lower pages first, and read before they wait, so the lowest unit at work
+// never waits and every wait ends.
 #include "qsa_common.cuh"
 
 namespace {
@@ -31,7 +34,7 @@ using namespace qsa;
 constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kBins = 2048;
-constexpr int kMoveThreads = 256;
+constexpr int kHeld = 16;  // masses a thread of the selection keeps in registers
 constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s
 
 struct EvictArgs {
@@ -103,25 +106,49 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictArgs a) 
   const bool cut = nb > a.budget;
   const int lo = cut ? a.sink : nb, hi = cut ? nb - a.recent : nb;  // blocks that compete
   const int want = cut ? a.budget - a.sink - a.recent : 0;
+  const int count = cut ? a.budget : nb, left = count + (tail ? 1 : 0), blocks = nb + (tail ? 1 : 0);
+  // Each warp owns a run of blocks, a lane every 32nd of it; the first kHeld of a
+  // lane's blocks stay in registers (sequences of up to 64K tokens entirely).
+  const int steps = (nb + kSelThreads - 1) / kSelThreads;
+  const int b0 = warp * steps * 32 + lane;
+  const bool held = steps <= kHeld;
+  float m[kHeld];
+#pragma unroll
+  for (int k = 0; k < kHeld; ++k) {
+    const int b = b0 + 32 * k;
+    m[k] = k < steps && b < nb ? mass[b] : 0.f;
+  }
+  const float m_open = tail && tid == 0 ? mass[nb] : 0.f;
+  // every block of this lane: f(block, mass)
+  auto each = [&](auto f) {
+#pragma unroll
+    for (int k = 0; k < kHeld; ++k)
+      if (k < steps) f(b0 + 32 * k, m[k]);
+    for (int k = kHeld; k < steps; ++k) {
+      const int b = b0 + 32 * k;
+      f(b, b < nb ? mass[b] : 0.f);
+    }
+  };
   // ---- the cut: the want-th largest key of [lo, hi), and how many equal to it are kept
   uint32_t T = 0xffffffffu;
   int need = 0;
   if (want > 0) {
     uint32_t prefix = 0;
-    int left = want;
-    const int shifts[3] = {21, 10, 0}, widths[3] = {11, 11, 10};
+    int rest = want;
+#pragma unroll 1
     for (int pass = 0; pass < 3; ++pass) {
-      const int sh = shifts[pass], bins = 1 << widths[pass];
+      const int sh = pass == 0 ? 21 : pass == 1 ? 10 : 0, width = pass == 2 ? 10 : 11;
+      const int bins = 1 << width;
       for (int k = tid; k < bins; k += kSelThreads) hist[k] = 0;
       __syncthreads();
-      const uint32_t mask = pass == 0 ? 0u : ~0u << (sh + widths[pass]);
-      for (int b = lo + tid; b < hi; b += kSelThreads) {
-        const uint32_t key = mass_key(mass[b]);
-        if ((key & mask) == prefix) atomicAdd(&hist[(key >> sh) & (bins - 1)], 1u);
-      }
+      const uint32_t mask = pass == 0 ? 0u : ~0u << (sh + width);
+      each([&](int b, float x) {
+        const uint32_t key = mass_key(x);
+        if (b >= lo && b < hi && (key & mask) == prefix) atomicAdd(&hist[(key >> sh) & (bins - 1)], 1u);
+      });
       __syncthreads();
-      // suffix counts: thread t owns bins 2t, 2t + 1 counted from the top
-      const int per = bins / kSelThreads;  // 2 or 1
+      // counts from the top: thread t owns bins 2t, 2t + 1 (t of 1,024 bins) from there
+      const int per = bins / kSelThreads;
       uint32_t own = 0;
       for (int k = 0; k < per; ++k) own += hist[bins - 1 - (tid * per + k)];
       uint32_t inc = own;
@@ -132,15 +159,15 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictArgs a) 
       }
       if (lane == 31) warp_sum[0][warp] = (int)inc;
       __syncthreads();
-      uint32_t before = inc - own;
-      for (int w = 0; w < warp; ++w) before += (uint32_t)warp_sum[0][w];
-      if (before < (uint32_t)left && before + own >= (uint32_t)left) {
+      uint32_t before = lane < warp ? (uint32_t)warp_sum[0][lane] : 0u;
+      before = __reduce_add_sync(0xffffffffu, before) + inc - own;
+      if (before < (uint32_t)rest && before + own >= (uint32_t)rest) {
         uint32_t acc = before;
         for (int k = 0; k < per; ++k) {
           const int bin = bins - 1 - (tid * per + k);
-          if (acc + hist[bin] >= (uint32_t)left) {
+          if (acc + hist[bin] >= (uint32_t)rest) {
             s_prefix = prefix | ((uint32_t)bin << sh);
-            s_need = (uint32_t)left - acc;
+            s_need = (uint32_t)rest - acc;
             break;
           }
           acc += hist[bin];
@@ -148,91 +175,68 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictArgs a) 
       }
       __syncthreads();
       prefix = s_prefix;
-      left = (int)s_need;
-      __syncthreads();
+      rest = (int)s_need;
     }
     T = prefix;
-    need = left;
+    need = rest;
   }
-  // ---- kept blocks in order: each warp owns a run of whole pages' worth of blocks
-  const int per_warp = ((nb + kSelWarps * 32 - 1) / (kSelWarps * 32)) * 32;
-  const int b0 = warp * per_warp, b1 = min(nb, b0 + per_warp);
-  int gt = 0, eq = 0;  // blocks kept for certain, and ties
-  for (int b = b0 + lane; b - lane < b1; b += 32) {
-    bool g = false, e = false;
-    if (b < b1) {
-      if (b < lo || b >= hi) {
-        g = true;
-      } else if (want > 0) {
-        const uint32_t key = mass_key(mass[b]);
-        g = key > T;
-        e = key == T;
-      }
-    }
-    gt += __popc(__ballot_sync(0xffffffffu, g));
-    eq += __popc(__ballot_sync(0xffffffffu, e));
-  }
+  // ---- blocks kept for certain, and ties, before each warp's run
+  auto classify = [&](int b, float x, bool& g, bool& e) {
+    const uint32_t key = mass_key(x);
+    const bool competes = b >= lo && b < hi;
+    g = b < nb && (!competes || (want > 0 && key > T));
+    e = b < nb && competes && want > 0 && key == T;
+  };
+  int gt = 0, eq = 0;
+  each([&](int b, float x) {
+    bool g, e;
+    classify(b, x, g, e);
+    gt += g;
+    eq += e;
+  });
+  gt = __reduce_add_sync(0xffffffffu, gt);
+  eq = __reduce_add_sync(0xffffffffu, eq);
   if (lane == 0) {
     warp_sum[0][warp] = gt;
     warp_sum[1][warp] = eq;
   }
-  __syncthreads();
-  int gt0 = 0, eq0 = 0;
-  for (int w = 0; w < warp; ++w) {
-    gt0 += warp_sum[0][w];
-    eq0 += warp_sum[1][w];
-  }
-  const int count = cut ? a.budget : nb;
-  float* tmp = a.mass_tmp + (int64_t)i * (a.budget + 1);
-  for (int b = b0 + lane; b - lane < b1; b += 32) {
-    bool g = false, e = false;
-    float m = 0.f;
-    if (b < b1) {
-      m = mass[b];
-      if (b < lo || b >= hi) {
-        g = true;
-      } else if (want > 0) {
-        const uint32_t key = mass_key(m);
-        g = key > T;
-        e = key == T;
-      }
-    }
+  __syncthreads();  // every mass that is held has been read: its row may be overwritten
+  int gt0 = __reduce_add_sync(0xffffffffu, lane < warp ? warp_sum[0][lane] : 0);
+  int eq0 = __reduce_add_sync(0xffffffffu, lane < warp ? warp_sum[1][lane] : 0);
+  // ---- in order: kept indices, blocks kept before each page, and the moved masses
+  // (rows too long to be held pass through the workspace)
+  float* out = a.mass_out + (int64_t)seq * a.mass_ld;
+  float* tmp = held ? out : a.mass_tmp + (int64_t)i * (a.budget + 1);
+  each([&](int b, float x) {
+    bool g, e;
+    classify(b, x, g, e);
     const unsigned gm = __ballot_sync(0xffffffffu, g), em = __ballot_sync(0xffffffffu, e);
     const unsigned below = (1u << lane) - 1u;
     const int eb = eq0 + __popc(em & below);
     const int at = gt0 + __popc(gm & below) + min(eb, need);
-    if (b < b1) {
+    if (b < nb) {
       if (b % kBlocksPerPage == 0) rank[b / kBlocksPerPage] = at;
       if (g || (e && eb < need)) {
         keep[at] = b;
-        tmp[at] = m;
+        tmp[at] = x;
       }
     }
     gt0 += __popc(gm);
     eq0 += __popc(em);
-  }
+  });
   for (int k = count + tid; k < a.budget; k += kSelThreads) keep[k] = -1;
   for (int P = (nb + kBlocksPerPage - 1) / kBlocksPerPage + tid; P <= a.c.max_pages_per_seq; P += kSelThreads)
     rank[P] = count;
   if (tid == 0) {
-    if (tail) tmp[count] = mass[nb];
+    if (tail) tmp[count] = m_open;
     a.keep_count[i] = count;
     a.new_len[i] = count * kRatio + tail;
   }
-  __syncthreads();  // the whole row has been read: it may be overwritten
-  const int blocks = nb + (tail ? 1 : 0), left = count + (tail ? 1 : 0);
-  float* out = a.mass_out + (int64_t)seq * a.mass_ld;
-  for (int b = tid; b < blocks; b += kSelThreads) out[b] = b < left ? tmp[b] : 0.f;
-}
-
-// 16-byte load that other CTAs' stores of this launch must not be cached against.
-__device__ __forceinline__ uint4 ld_l2(const void* p) {
-  uint4 r;
-  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
-               : "l"(p)
-               : "memory");
-  return r;
+  if (!held) {
+    __syncthreads();  // the whole row has been read
+    for (int b = tid; b < left; b += kSelThreads) out[b] = tmp[b];
+  }
+  for (int b = left + tid; b < blocks; b += kSelThreads) out[b] = 0.f;
 }
 
 __device__ __forceinline__ int ld_acquire(const int* p) {
@@ -245,105 +249,150 @@ __device__ __forceinline__ void st_release(int* p, int v) {
   asm volatile("st.release.gpu.global.s32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
 }
 
-// Runs of kRunBytes: 4096 (BF16) or 2048 (e4m3).
-template <int kRunBytes>
-__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(EvictArgs a) {
-  constexpr int kRunThreads = kRunBytes / 16;              // threads that carry one run
-  constexpr int kRunsAtOnce = kMoveThreads / kRunThreads;  // 1 or 2
-  constexpr int kRounds = kBlocksPerPage / kRunsAtOnce;
+// 1-D bulk async copy shared -> global; addresses 16-byte aligned, bytes a multiple of 16.
+__device__ __forceinline__ void bulk_s2g(void* dst, uint32_t src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+__device__ __forceinline__ void fence_proxy_async_all() { asm volatile("fence.proxy.async;" ::: "memory"); }
+
+// A unit of the move, as lane b of a warp sees it: block b of the destination page.
+struct Unit {
+  int page, g;           // destination page of the sequence, KV head
+  const int32_t* rank;
+  int32_t* done;         // read flags of the sequence and head
+  int src, dst;          // physical page * 16 + slot; src -1: nothing to move
+  bool any;              // the page receives blocks
+};
+
+// kRunBytes: 4096 (BF16) or 2048 (e4m3); kWorkers warps, each with a buffer of one unit.
+template <int kRunBytes, int kWorkers>
+struct MoveLay {
+  static constexpr int kKcBytes = kIdxDim * 2;
+  static constexpr int kBuf = kBlocksPerPage * (kRunBytes + kKcBytes);
+  static constexpr int kSmem = kWorkers * kBuf + kWorkers * 8;
+  static_assert(kSmem <= 232448, "shared memory budget");
+};
+
+template <int kRunBytes, int kWorkers>
+__global__ void __launch_bounds__(kWorkers * 32) evict_move_kernel(EvictArgs a, int units) {
+  using LY = MoveLay<kRunBytes, kWorkers>;
+  extern __shared__ __align__(128) uint8_t smem[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t buf = smem_u32(smem) + warp * LY::kBuf, bar = smem_u32(smem) + kWorkers * LY::kBuf + warp * 8;
   pdl_launch_dependents();
+  if (lane == 0) {
+    mbar_init(bar, 1);
+    fence_mbar_init();
+  }
+  __syncwarp();
   pdl_wait_previous();
-  const int tid = threadIdx.x;
-  __shared__ int s_ticket, s_ok;
-  __shared__ int s_src[kBlocksPerPage], s_dst;  // source page * 16 + slot (-1: none) of each block, destination page
-  if (tid == 0) s_ticket = atomicAdd(a.ticket, 1);
-  __syncthreads();
   const int hkv = a.c.num_kv_heads;
-  const int g = s_ticket % hkv, page = (s_ticket / hkv) % a.pages, i = s_ticket / (hkv * a.pages);
-  const int32_t* rank = a.rank + (int64_t)i * (a.c.max_pages_per_seq + 2);
-  const int count = a.keep_count[i], len = rank[a.c.max_pages_per_seq + 1], seq = a.seq_ids[i];
-  const int tail = len % kRatio, first = page * kBlocksPerPage;
-  const int total = count + (tail ? 1 : 0);
-  if (first >= total) return;
-  const int nblk = min(kBlocksPerPage, total - first);
-  const int64_t row = (int64_t)seq * a.c.max_pages_per_seq;
-  if (tid < kBlocksPerPage) {
-    int src = -1;
-    if (tid < nblk) {
-      const int b = first + tid < count ? a.keep[(int64_t)i * a.budget + first + tid] : len / kRatio;
-      const int sp = a.c.block_table[row + b / kBlocksPerPage];
-      if (sp < 0 || sp >= a.c.num_pages)
-        flag(a.st, QSA_DEV_BAD_PAGE);
-      else
-        src = b % kBlocksPerPage + kBlocksPerPage * sp;
-    }
-    s_src[tid] = src;
-  }
-  if (tid == 32) {
-    int dp = a.dst_table[row + page];
-    if (dp < 0 || dp >= a.c.num_pages) {
-      flag(a.st, QSA_DEV_BAD_PAGE);
-      dp = -1;
-    }
-    s_dst = dp;
-  }
-  __syncthreads();
-  const int dp = s_dst;
-  // ---- read
   uint8_t* kv = static_cast<uint8_t*>(a.c.kv_pages);
-  const int sub = tid / kRunThreads, off = (tid % kRunThreads) * 16;
-  auto run_at = [&](int64_t unit) {  // page * 16 + slot -> the run of head g
-    return ((unit / kBlocksPerPage * hkv + g) * kBlocksPerPage + unit % kBlocksPerPage) * kRunBytes + off;
+  uint8_t* kc = static_cast<uint8_t*>(a.c.kc_pages);
+  auto claim = [&]() {
+    int t = 0;
+    if (lane == 0) t = atomicAdd(a.ticket, 1);
+    return __shfl_sync(0xffffffffu, t, 0);
   };
-  uint4 x[kRounds], kc = make_uint4(0, 0, 0, 0);
-  uint32_t landed = 0;
-#pragma unroll
-  for (int r = 0; r < kRounds; ++r) {
-    x[r] = make_uint4(0, 0, 0, 0);
-    const int src = s_src[r * kRunsAtOnce + sub];
-    if (kv && src >= 0 && src != dp * kBlocksPerPage + r * kRunsAtOnce + sub) x[r] = ld_l2(kv + run_at(src));
-  }
-  uint8_t* kcp = static_cast<uint8_t*>(a.c.kc_pages);
-  const int kblk = tid >> 4;
-  const bool with_kc = kcp && g == 0 && s_src[kblk] >= 0 && s_src[kblk] != dp * kBlocksPerPage + kblk;
-  if (with_kc) kc = ld_l2(kcp + (int64_t)s_src[kblk] * 256 + (tid & 15) * 16);
-#pragma unroll
-  for (int r = 0; r < kRounds; ++r) landed |= x[r].x;
-  __syncthreads_or((landed | kc.x) != 0);  // takes the loaded values: every thread's reads have landed before the flag
-  int32_t* done = a.read_done + ((int64_t)i * hkv + g) * a.pages;
-  if (tid == 0) {
-    __threadfence();
-    st_release(done + page, 1);
-    // ---- wait for the lower pages that took blocks out of this one
-    const int k0 = rank[page], k1 = rank[page + 1];
-    int ok = 1;
-    if (k1 > k0) {
-      const int p1 = min(page - 1, (k1 - 1) / kBlocksPerPage);
-      for (int p = k0 / kBlocksPerPage; p <= p1 && ok; ++p) {
-        const uint64_t t0 = global_timer_ns();
-        while (!ld_acquire(done + p)) {
-          if (global_timer_ns() - t0 > kWaitLimitNs) {
-            flag(a.st, QSA_DEV_TIMEOUT);
-            ok = 0;
-            break;
-          }
-        }
+  // head fastest, then page, then sequence: lower pages of a sequence and head come first
+  auto look_up = [&](int t) {
+    Unit u;
+    const int i = t / (hkv * a.pages);
+    u.g = t % hkv;
+    u.page = t / hkv % a.pages;
+    u.rank = a.rank + (int64_t)i * (a.c.max_pages_per_seq + 2);
+    u.done = a.read_done + ((int64_t)i * hkv + u.g) * a.pages;
+    u.src = -1;
+    u.dst = 0;
+    const int k = u.page * kBlocksPerPage + lane;
+    // independent loads first; keep may hold nothing meaningful at k, then it is not used
+    const int count = a.keep_count[i], len = u.rank[a.c.max_pages_per_seq + 1], seq = a.seq_ids[i];
+    const int kept = lane < kBlocksPerPage && k < a.budget ? a.keep[(int64_t)i * a.budget + k] : 0;
+    const int total = count + (len % kRatio ? 1 : 0);
+    u.any = u.page * kBlocksPerPage < total;
+    if (lane < kBlocksPerPage && k < total) {
+      const int b = k < count ? kept : len / kRatio;
+      const int64_t row = (int64_t)seq * a.c.max_pages_per_seq;
+      const int sp = a.c.block_table[row + b / kBlocksPerPage], dp = a.dst_table[row + u.page];
+      if (sp < 0 || sp >= a.c.num_pages || dp < 0 || dp >= a.c.num_pages) {
+        flag(a.st, QSA_DEV_BAD_PAGE);
+      } else {
+        u.src = sp * kBlocksPerPage + b % kBlocksPerPage;
+        u.dst = dp * kBlocksPerPage + lane;
+        if (u.src == u.dst) u.src = -1;  // stays where it is
       }
     }
-    __threadfence();
-    s_ok = ok;
+    return u;
+  };
+  auto run_at = [&](int unit, int g) {  // page * 16 + slot -> the run of head g
+    return kv + (((int64_t)(unit / kBlocksPerPage) * hkv + g) * kBlocksPerPage + unit % kBlocksPerPage) * kRunBytes;
+  };
+  const uint64_t policy = l2_policy_evict_first();
+  const uint32_t my_run = buf + lane * kRunBytes, my_kc = buf + kBlocksPerPage * kRunBytes + lane * LY::kKcBytes;
+  uint32_t parity = 0;
+  bool sound = true;
+  int t = claim();
+  Unit u;
+  if (t < units) u = look_up(t);
+  while (t < units) {
+    const bool moves = u.src >= 0, with_kc = kc && u.g == 0;
+    const unsigned movers = __ballot_sync(0xffffffffu, moves);
+    // ---- read
+    if (movers) {
+      const int bytes = (kv ? kRunBytes : 0) + (with_kc ? LY::kKcBytes : 0);
+      bulk_wait_read();  // the last unit's blocks have left the buffer
+      __syncwarp();
+      if (lane == 0) mbar_arrive_expect_tx(bar, bytes * __popc(movers));
+      __syncwarp();
+      if (moves) {
+        if (kv) bulk_g2s(my_run, run_at(u.src, u.g), kRunBytes, bar, policy);
+        if (with_kc) bulk_g2s(my_kc, kc + (int64_t)u.src * LY::kKcBytes, LY::kKcBytes, bar, policy);
+      }
+    }
+    // ---- the next unit's tables meanwhile (a claimed unit reads before it waits for anything)
+    const Unit now = u;
+    const int t_next = claim();
+    if (t_next < units) u = look_up(t_next);
+    if (movers) {
+      if (!mbar_wait_bounded(bar, parity, kWaitLimitNs)) sound = false;
+      parity ^= 1u;
+    }
+    sound = __all_sync(0xffffffffu, sound);
+    if (now.any && lane == 0) st_release(now.done + now.page, 1);
+    if (movers) {
+      // ---- wait for the lower pages that took blocks out of this one
+      const int k0 = now.rank[now.page], k1 = now.rank[now.page + 1];
+      if (k1 > k0) {
+        const int p0 = k0 / kBlocksPerPage, p1 = min(now.page - 1, (k1 - 1) / kBlocksPerPage);
+        const uint64_t t0 = global_timer_ns();
+        for (int p = p0 + lane; p <= p1 && sound; p += 32)
+          while (!ld_acquire(now.done + p))
+            if (global_timer_ns() - t0 > kWaitLimitNs) {
+              sound = false;
+              break;
+            }
+      }
+      sound = __all_sync(0xffffffffu, sound);
+      if (!sound) {  // never store what may be wrong; the buffer's copies have been waited for
+        if (lane == 0) flag(a.st, QSA_DEV_TIMEOUT);
+        break;
+      }
+      __syncwarp();
+      fence_proxy_async_all();  // the flags were read as ordinary memory, the stores are asynchronous
+      // ---- write
+      if (moves) {
+        if (kv) bulk_s2g(run_at(now.dst, now.g), my_run, kRunBytes);
+        if (with_kc) bulk_s2g(kc + (int64_t)now.dst * LY::kKcBytes, my_kc, LY::kKcBytes);
+      }
+      bulk_commit();
+    }
+    t = t_next;
   }
-  __syncthreads();
-  if (!s_ok || dp < 0) return;
-  // ---- write
-#pragma unroll
-  for (int r = 0; r < kRounds; ++r) {
-    const int b = r * kRunsAtOnce + sub, src = s_src[b];
-    if (kv && src >= 0 && src != dp * kBlocksPerPage + b)
-      *reinterpret_cast<uint4*>(kv + run_at((int64_t)dp * kBlocksPerPage + b)) = x[r];
-  }
-  if (with_kc)
-    *reinterpret_cast<uint4*>(kcp + ((int64_t)dp * kBlocksPerPage + kblk) * 256 + (tid & 15) * 16) = kc;
+  bulk_wait_all();
 }
 
 struct WorkspaceMap {
@@ -372,6 +421,19 @@ int check_evict(const qsa_cache_t* cache, int32_t n, int32_t budget) {
     return QSA_ERR_UNSUPPORTED;  // positions and page * 16 + slot are int32
   if ((int64_t)budget > (int64_t)c.max_pages_per_seq * kBlocksPerPage) return QSA_ERR_INVALID_ARG;
   return QSA_OK;
+}
+
+template <int kRunBytes, int kWorkers>
+int launch_move(const EvictArgs& a, int units, int sms, cudaStream_t s) {
+  constexpr int smem = MoveLay<kRunBytes, kWorkers>::kSmem;
+  if (cudaFuncSetAttribute(evict_move_kernel<kRunBytes, kWorkers>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           smem) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return QSA_ERR_CUDA;
+  }
+  const int grid = units < sms ? units : sms;  // at least a unit per CTA: few units spread over the SMs
+  return qsa_host::launch(evict_move_kernel<kRunBytes, kWorkers>, dim3((unsigned)grid), dim3(kWorkers * 32),
+                          (size_t)smem, s, a, units);
 }
 
 }  // namespace
@@ -425,12 +487,17 @@ extern "C" int qsa_evict(const qsa_cache_t* cache, const int32_t* dst_table, con
   a.pages = pages_of_budget(budget);
   if (a.pages > c.max_pages_per_seq) a.pages = c.max_pages_per_seq;
   a.st = dev_status;
-  const int64_t grid = (int64_t)n * c.num_kv_heads * a.pages;
-  if (grid > 0x7fffffff) return QSA_ERR_UNSUPPORTED;
+  const int64_t units = (int64_t)n * c.num_kv_heads * a.pages;
+  if (units > 0x3fffffff) return QSA_ERR_UNSUPPORTED;
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return QSA_ERR_CUDA;
+  }
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int r = qsa_host::launch(evict_select_kernel, dim3((unsigned)n), dim3(kSelThreads), 0, s, a);
   if (r != QSA_OK) return r;
-  return c.kv_dtype == QSA_KV_FP8_E4M3
-             ? qsa_host::launch(evict_move_kernel<2048>, dim3((unsigned)grid), dim3(kMoveThreads), 0, s, a)
-             : qsa_host::launch(evict_move_kernel<4096>, dim3((unsigned)grid), dim3(kMoveThreads), 0, s, a);
+  return c.kv_dtype == QSA_KV_FP8_E4M3 ? launch_move<2048, 6>(a, (int)units, sms, s)
+                                       : launch_move<4096, 3>(a, (int)units, sms, s);
 }

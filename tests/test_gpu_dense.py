@@ -487,6 +487,14 @@ def test_evict_patterns_of_a_long_sequence_in_place(shape):
     check_evict(grp, nb // 3, 5, 40, mass)
 
 
+@pytest.mark.parametrize("alias", [False, True])
+def test_evict_rows_too_long_for_registers(alias):
+    """More than 16,384 blocks: masses are read again and pass through the workspace."""
+    grp = Group([64 * 1100 + 3, 500], 1, seed=13)
+    mass = masses(random.Random(5), (2, 1101 * 16))
+    check_evict(grp, 9000, 3, 100, mass, alias=alias)
+
+
 @pytest.mark.parametrize("seed", range(4))
 def test_evict_in_place_random(seed):
     rng = random.Random(seed)
