@@ -10,7 +10,7 @@
 // together.
 //
 // evict_select_kernel, one CTA per sequence: radix select of the cut (11 + 11 +
-// 10 bits of the order-preserving key) over masses held in registers, then one
+// 10 bits of the order-preserving key) over masses held in shared memory, then one
 // ordered pass that writes the kept indices, the number kept before every page,
 // and the moved mass row.
 //
@@ -33,8 +33,8 @@ using namespace qsa;
 
 constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
-constexpr int kBins = 2048;
-constexpr int kHeld = 16;  // masses a thread of the selection keeps in registers
+constexpr int kBins0 = 2048, kBins1 = 2048, kBins2 = 1024;  // 11 + 11 + 10 bits of a key
+constexpr int kMaxRoom = 48 * 1024;  // masses the selection keeps in shared memory: 192 KiB, 196,608 tokens
 constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s
 
 struct EvictArgs {
@@ -74,11 +74,12 @@ __device__ __forceinline__ int entry_seq(const EvictArgs& a, int i, bool report)
   return bad ? -1 : seq;
 }
 
-__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictArgs a) {
+__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictArgs a, int room) {
+  extern __shared__ float mass_s[];
   pdl_launch_dependents();
   pdl_wait_previous();
   const int i = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  __shared__ uint32_t hist[kBins];
+  __shared__ uint32_t hist[kBins0 + kBins1 + kBins2];
   __shared__ int warp_sum[2][kSelWarps];
   __shared__ uint32_t s_prefix, s_need;
   const int hkv = a.c.num_kv_heads;
@@ -107,75 +108,64 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictArgs a) 
   const int lo = cut ? a.sink : nb, hi = cut ? nb - a.recent : nb;  // blocks that compete
   const int want = cut ? a.budget - a.sink - a.recent : 0;
   const int count = cut ? a.budget : nb, left = count + (tail ? 1 : 0), blocks = nb + (tail ? 1 : 0);
-  // Each warp owns a run of blocks, a lane every 32nd of it; the first kHeld of a
-  // lane's blocks stay in registers (sequences of up to 64K tokens entirely).
+  // Each warp owns a run of blocks, a lane every 32nd of it.  The masses of the first
+  // `room` blocks stay in shared memory, later ones are read again.
   const int steps = (nb + kSelThreads - 1) / kSelThreads;
   const int b0 = warp * steps * 32 + lane;
-  const bool held = steps <= kHeld;
-  float m[kHeld];
-#pragma unroll
-  for (int k = 0; k < kHeld; ++k) {
-    const int b = b0 + 32 * k;
-    m[k] = k < steps && b < nb ? mass[b] : 0.f;
-  }
+  const bool held = nb <= room;
+#pragma unroll 4
+  for (int b = tid; b < min(nb, room); b += kSelThreads) mass_s[b] = mass[b];
   const float m_open = tail && tid == 0 ? mass[nb] : 0.f;
-  // every block of this lane: f(block, mass)
-  auto each = [&](auto f) {
-#pragma unroll
-    for (int k = 0; k < kHeld; ++k)
-      if (k < steps) f(b0 + 32 * k, m[k]);
-    for (int k = kHeld; k < steps; ++k) {
+  auto each = [&](auto f) {  // every block of this lane: f(block, mass)
+#pragma unroll 2
+    for (int k = 0; k < steps; ++k) {
       const int b = b0 + 32 * k;
-      f(b, b < nb ? mass[b] : 0.f);
+      f(b, b < nb ? (b < room ? mass_s[b] : mass[b]) : 0.f);
     }
   };
+  for (int k = tid; k < kBins0 + kBins1 + kBins2; k += kSelThreads) hist[k] = 0;
+  __syncthreads();
   // ---- the cut: the want-th largest key of [lo, hi), and how many equal to it are kept
   uint32_t T = 0xffffffffu;
   int need = 0;
   if (want > 0) {
     uint32_t prefix = 0;
     int rest = want;
+    uint32_t* h = hist;
 #pragma unroll 1
     for (int pass = 0; pass < 3; ++pass) {
-      const int sh = pass == 0 ? 21 : pass == 1 ? 10 : 0, width = pass == 2 ? 10 : 11;
-      const int bins = 1 << width;
-      for (int k = tid; k < bins; k += kSelThreads) hist[k] = 0;
-      __syncthreads();
-      const uint32_t mask = pass == 0 ? 0u : ~0u << (sh + width);
+      const int sh = pass == 0 ? 21 : pass == 1 ? 10 : 0, bins = pass == 2 ? kBins2 : kBins0;
+      const uint32_t mask = pass == 0 ? 0u : ~0u << (pass == 1 ? 21 : 10);
       each([&](int b, float x) {
         const uint32_t key = mass_key(x);
-        if (b >= lo && b < hi && (key & mask) == prefix) atomicAdd(&hist[(key >> sh) & (bins - 1)], 1u);
+        if (b >= lo && b < hi && (key & mask) == prefix) atomicAdd(&h[(key >> sh) & (bins - 1)], 1u);
       });
       __syncthreads();
-      // counts from the top: thread t owns bins 2t, 2t + 1 (t of 1,024 bins) from there
-      const int per = bins / kSelThreads;
-      uint32_t own = 0;
-      for (int k = 0; k < per; ++k) own += hist[bins - 1 - (tid * per + k)];
-      uint32_t inc = own;
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const uint32_t y = __shfl_up_sync(0xffffffffu, inc, d);
-        if (lane >= d) inc += y;
-      }
-      if (lane == 31) warp_sum[0][warp] = (int)inc;
+      // counts from the top: thread t owns 2 bins (or 1) from there, warp w the t of its lanes
+      const int per = bins / kSelThreads, top = bins - 1 - tid * per;
+      const uint32_t first = h[top], own = first + (per == 2 ? h[top - 1] : 0u);
+      const uint32_t sum = __reduce_add_sync(0xffffffffu, own);
+      if (lane == 0) warp_sum[0][warp] = (int)sum;
       __syncthreads();
-      uint32_t before = lane < warp ? (uint32_t)warp_sum[0][lane] : 0u;
-      before = __reduce_add_sync(0xffffffffu, before) + inc - own;
-      if (before < (uint32_t)rest && before + own >= (uint32_t)rest) {
-        uint32_t acc = before;
-        for (int k = 0; k < per; ++k) {
-          const int bin = bins - 1 - (tid * per + k);
-          if (acc + hist[bin] >= (uint32_t)rest) {
-            s_prefix = prefix | ((uint32_t)bin << sh);
-            s_need = (uint32_t)rest - acc;
-            break;
-          }
-          acc += hist[bin];
+      const uint32_t before_warp = __reduce_add_sync(0xffffffffu, lane < warp ? (uint32_t)warp_sum[0][lane] : 0u);
+      if (before_warp < (uint32_t)rest && before_warp + sum >= (uint32_t)rest) {  // the cut is in this warp's bins
+        uint32_t inc = own;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+          const uint32_t y = __shfl_up_sync(0xffffffffu, inc, d);
+          if (lane >= d) inc += y;
+        }
+        const uint32_t before = before_warp + inc - own;
+        if (before < (uint32_t)rest && before + own >= (uint32_t)rest) {
+          const bool second = before + first < (uint32_t)rest;
+          s_prefix = prefix | ((uint32_t)(top - second) << sh);
+          s_need = (uint32_t)rest - before - (second ? first : 0u);
         }
       }
       __syncthreads();
       prefix = s_prefix;
       rest = (int)s_need;
+      h += bins;
     }
     T = prefix;
     need = rest;
@@ -262,10 +252,11 @@ __device__ __forceinline__ void fence_proxy_async_all() { asm volatile("fence.pr
 // A unit of the move, as lane b of a warp sees it: block b of the destination page.
 struct Unit {
   int page, g;           // destination page of the sequence, KV head
-  const int32_t* rank;
   int32_t* done;         // read flags of the sequence and head
   int src, dst;          // physical page * 16 + slot; src -1: nothing to move
-  bool any;              // the page receives blocks
+  int p0, p1;            // lower pages that take blocks out of this one (none: p1 < p0); only a page
+                         // of the sequence's own, written in place, still holds them
+  bool any, in_place;    // the page receives blocks; it is the sequence's own
 };
 
 // kRunBytes: 4096 (BF16) or 2048 (e4m3); kWorkers warps, each with a buffer of one unit.
@@ -304,20 +295,25 @@ __global__ void __launch_bounds__(kWorkers * 32) evict_move_kernel(EvictArgs a, 
     const int i = t / (hkv * a.pages);
     u.g = t % hkv;
     u.page = t / hkv % a.pages;
-    u.rank = a.rank + (int64_t)i * (a.c.max_pages_per_seq + 2);
+    const int32_t* rank = a.rank + (int64_t)i * (a.c.max_pages_per_seq + 2);
     u.done = a.read_done + ((int64_t)i * hkv + u.g) * a.pages;
     u.src = -1;
     u.dst = 0;
     const int k = u.page * kBlocksPerPage + lane;
     // independent loads first; keep may hold nothing meaningful at k, then it is not used
-    const int count = a.keep_count[i], len = u.rank[a.c.max_pages_per_seq + 1], seq = a.seq_ids[i];
+    const int count = a.keep_count[i], len = rank[a.c.max_pages_per_seq + 1], seq = a.seq_ids[i];
+    const int k0 = rank[u.page], k1 = rank[u.page + 1];
+    const int64_t row = (int64_t)max(0, min(seq, a.c.max_seqs - 1)) * a.c.max_pages_per_seq;
+    const int dp = a.dst_table[row + u.page], own = a.c.block_table[row + u.page];
     const int kept = lane < kBlocksPerPage && k < a.budget ? a.keep[(int64_t)i * a.budget + k] : 0;
     const int total = count + (len % kRatio ? 1 : 0);
+    u.in_place = dp == own;
     u.any = u.page * kBlocksPerPage < total;
+    u.p0 = k0 / kBlocksPerPage;
+    u.p1 = k1 > k0 && dp == own ? min(u.page - 1, (k1 - 1) / kBlocksPerPage) : -1;
     if (lane < kBlocksPerPage && k < total) {
       const int b = k < count ? kept : len / kRatio;
-      const int64_t row = (int64_t)seq * a.c.max_pages_per_seq;
-      const int sp = a.c.block_table[row + b / kBlocksPerPage], dp = a.dst_table[row + u.page];
+      const int sp = a.c.block_table[row + b / kBlocksPerPage];
       if (sp < 0 || sp >= a.c.num_pages || dp < 0 || dp >= a.c.num_pages) {
         flag(a.st, QSA_DEV_BAD_PAGE);
       } else {
@@ -357,24 +353,26 @@ __global__ void __launch_bounds__(kWorkers * 32) evict_move_kernel(EvictArgs a, 
     const Unit now = u;
     const int t_next = claim();
     if (t_next < units) u = look_up(t_next);
+    // ---- the lower pages that take blocks out of this one: usually read by now (at most
+    // 16 kept blocks came from here, so they went to two pages)
+    const int dep = now.p0 + lane;
+    const bool has_dep = movers && dep <= now.p1;
+    bool clear = !has_dep || ld_acquire(now.done + dep);
     if (movers) {
       if (!mbar_wait_bounded(bar, parity, kWaitLimitNs)) sound = false;
       parity ^= 1u;
     }
-    sound = __all_sync(0xffffffffu, sound);
-    if (now.any && lane == 0) st_release(now.done + now.page, 1);
+    const bool wait = !__all_sync(0xffffffffu, clear);
+    const bool early = now.in_place || !movers;  // its neighbours wait; else the flag keeps out of the stores' way
+    if (early && now.any && lane == 0) st_release(now.done + now.page, 1);
     if (movers) {
-      // ---- wait for the lower pages that took blocks out of this one
-      const int k0 = now.rank[now.page], k1 = now.rank[now.page + 1];
-      if (k1 > k0) {
-        const int p0 = k0 / kBlocksPerPage, p1 = min(now.page - 1, (k1 - 1) / kBlocksPerPage);
+      if (wait && !clear) {
         const uint64_t t0 = global_timer_ns();
-        for (int p = p0 + lane; p <= p1 && sound; p += 32)
-          while (!ld_acquire(now.done + p))
-            if (global_timer_ns() - t0 > kWaitLimitNs) {
-              sound = false;
-              break;
-            }
+        while (!ld_acquire(now.done + dep))
+          if (global_timer_ns() - t0 > kWaitLimitNs) {
+            sound = false;
+            break;
+          }
       }
       sound = __all_sync(0xffffffffu, sound);
       if (!sound) {  // never store what may be wrong; the buffer's copies have been waited for
@@ -389,6 +387,7 @@ __global__ void __launch_bounds__(kWorkers * 32) evict_move_kernel(EvictArgs a, 
         if (with_kc) bulk_s2g(kc + (int64_t)now.dst * LY::kKcBytes, my_kc, LY::kKcBytes);
       }
       bulk_commit();
+      if (!early && lane == 0) st_release(now.done + now.page, 1);
     }
     t = t_next;
   }
@@ -496,7 +495,15 @@ extern "C" int qsa_evict(const qsa_cache_t* cache, const int32_t* dst_table, con
     return QSA_ERR_CUDA;
   }
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const int r = qsa_host::launch(evict_select_kernel, dim3((unsigned)n), dim3(kSelThreads), 0, s, a);
+  const int64_t blocks = (int64_t)c.max_pages_per_seq * kBlocksPerPage;
+  const int room = blocks < kMaxRoom ? (int)blocks : kMaxRoom;
+  if (cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxRoom * 4) !=
+      cudaSuccess) {
+    (void)cudaGetLastError();
+    return QSA_ERR_CUDA;
+  }
+  const int r = qsa_host::launch(evict_select_kernel, dim3((unsigned)n), dim3(kSelThreads), (size_t)room * 4, s, a,
+                                 room);
   if (r != QSA_OK) return r;
   return c.kv_dtype == QSA_KV_FP8_E4M3 ? launch_move<2048, 6>(a, (int)units, sms, s)
                                        : launch_move<4096, 3>(a, (int)units, sms, s);
