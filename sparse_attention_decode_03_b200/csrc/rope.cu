@@ -9,10 +9,12 @@
 // position of a quarter-million tokens times a frequency near 1 has lost about
 // 2^-7 rad in fp32.  sin and cos of the reduced turn are taken in fp32.
 //
-// What bounds it: the bytes of the rows for a prompt chunk, launch latency for a
-// decode step.  A CTA takes kTokens tokens; it computes their R/2 angles once
-// (shared by every head), then its warps take the rows: 16 bytes per lane, a
-// half-split pair's partner chunk by shuffle.  Rows of 128 dims go two to a warp.
+// What bounds it: the bytes of the rows for a prompt chunk, latency for a decode
+// step.  A CTA takes up to 8 tokens and a share of their rows, a warp each row
+// (two of up to 128 dims), 16 bytes per lane; a half-split pair's partner chunk
+// comes by shuffle.  The rows of 4 tokens are requested together, before the
+// angles are computed: each CTA computes its tokens' R/2 sines and cosines once,
+// for all heads.  Few tokens spread their rows over more CTAs instead.
 #include "qsa_common.cuh"
 
 namespace {
@@ -21,7 +23,8 @@ using namespace qsa;
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kTokens = 2;  // tokens of a CTA
+constexpr int kTokens = 8;  // tokens of a CTA at most
+constexpr int kAhead = 4;   // tokens whose rows a warp requests together
 constexpr int kMaxPairs = QSA_ROPE_MAX_PAIRS;
 
 struct RopeArgs {
@@ -32,81 +35,125 @@ struct RopeArgs {
   const int32_t* pos;
   int64_t pos_stride;
   int32_t n;
+  int32_t tokens;  // of a CTA
 };
 
+// 16-byte load that leaves L1 alone.  Not the read-only path: out may be in.
+__device__ __forceinline__ uint4 ld_row(const void* p) {
+  uint4 r;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+               : "l"(p));
+  return r;
+}
+
+// A warp-sized piece of a token's rows: 256-dim rows take a warp, rows of up to
+// 128 dims half of one.
+struct Piece {
+  const __nv_bfloat16* in;
+  __nv_bfloat16* out;
+  int64_t in_stride, out_stride;
+  int chunk;  // the lane's 8 dims of its row
+  bool live;
+};
+
+__device__ __forceinline__ Piece find_piece(const RopeArgs& a, int item, int lane) {
+  int ti = 0, rows_per;
+  for (;; ++ti) {
+    rows_per = a.t[ti].head_dim <= 128 ? 2 : 1;
+    const int cnt = (a.t[ti].heads + rows_per - 1) / rows_per;
+    if (item < cnt) break;
+    item -= cnt;
+  }
+  const qsa_rope_tensor_t& x = a.t[ti];
+  const int lanes = 32 / rows_per;
+  Piece p;
+  p.chunk = lane % lanes;
+  const int head = item * rows_per + lane / lanes;
+  // in place, the dims that do not turn stay where they are
+  p.live = head < x.heads && p.chunk * 8 < x.head_dim && !(x.in == x.out && p.chunk * 8 >= a.plan.rot_dim);
+  const int64_t at = (int64_t)head * x.head_dim + p.chunk * 8;
+  p.in = static_cast<const __nv_bfloat16*>(x.in) + at;
+  p.out = static_cast<__nv_bfloat16*>(x.out) + at;
+  p.in_stride = x.in_stride;
+  p.out_stride = x.out_stride;
+  return p;
+}
+
+template <bool kAdjacent>
 __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeArgs a) {
   __shared__ float2 cs[kTokens][kMaxPairs];  // cos, sin
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int half = a.plan.rot_dim / 2;
-  const int64_t tok0 = (int64_t)blockIdx.x * kTokens;
-  const int ntok = (int)min((int64_t)kTokens, a.n - tok0);
+  const int half = a.plan.rot_dim / 2, rot_chunks = a.plan.rot_dim / 8;
+  const int64_t tok0 = (int64_t)blockIdx.x * a.tokens;
+  const int ntok = (int)min((int64_t)a.tokens, a.n - tok0);
+  const int step = gridDim.y * kWarps;
   pdl_wait_previous();
-  for (int k = tid; k < ntok * half; k += kThreads) {
-    const int i = k % half, t = k / half;
-    const int p = a.pos[a.plan.axis[i] * a.pos_stride + tok0 + t];
-    double turn = (double)p * a.plan.freq[i] * 0.15915494309189533577;  // 1 / 2 pi
-    turn -= rint(turn);
-    float s, c;
-    sincospif(2.f * (float)turn, &s, &c);
-    cs[t][i] = make_float2(c, s);
-  }
-  __syncthreads();
-  const int total = ntok * a.items;
-  for (int k = warp; k < total; k += kWarps) {
-    const int t = k / a.items;
-    int item = k % a.items, ti = 0;
-    // the tensor and row of this piece: 256-dim rows take a warp, rows of up to 128 half of one
-    int rows_per = 1, cnt = 0;
-    for (;; ++ti) {
-      rows_per = a.t[ti].head_dim <= 128 ? 2 : 1;
-      cnt = (a.t[ti].heads + rows_per - 1) / rows_per;
-      if (item < cnt) break;
-      item -= cnt;
-    }
-    const qsa_rope_tensor_t& x = a.t[ti];
-    const int lanes = 32 / rows_per;
-    const int c = lane % lanes, head = item * rows_per + lane / lanes;
-    const int rot_chunks = a.plan.rot_dim / 8;
-    const bool in_place = x.in == x.out;
-    const bool live = head < x.heads && c * 8 < x.head_dim && !(in_place && c >= rot_chunks);
-    uint4 v = make_uint4(0, 0, 0, 0);
-    const int64_t tok = tok0 + t;
-    if (live)
-      v = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(x.in) + tok * x.in_stride +
-                                          (int64_t)head * x.head_dim + c * 8);
-    uint32_t w[4] = {v.x, v.y, v.z, v.w}, r[4];
-    if (a.plan.adjacent) {
-      if (c < rot_chunks) {
+  bool angles = false;
+  for (int item = blockIdx.y * kWarps + warp; item < a.items || !angles; item += step) {
+    const bool has = item < a.items;
+    Piece p;
+    if (has) p = find_piece(a, item, lane);
+    for (int t0 = 0; t0 < ntok; t0 += kAhead) {
+      uint4 v[kAhead];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float2 k2 = cs[t][c * 4 + e];
-          const float x0 = __uint_as_float(w[e] << 16), x1 = __uint_as_float(w[e] & 0xffff0000u);
-          r[e] = pack_bf16(x0 * k2.x - x1 * k2.y, x1 * k2.x + x0 * k2.y);
-        }
-      } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) r[e] = w[e];
+      for (int u = 0; u < kAhead; ++u) {
+        v[u] = make_uint4(0, 0, 0, 0);
+        if (has && t0 + u < ntok && p.live)
+          v[u] = ld_row(p.in + (tok0 + t0 + u) * p.in_stride);
       }
-    } else {
-      const int hc = rot_chunks / 2;  // chunks of a half
-      const bool low = c < hc;
-      const int from = lane + (low ? hc : -hc);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const uint32_t o = __shfl_sync(0xffffffffu, w[e], from & 31);
-        r[e] = w[e];
-        if (c < rot_chunks) {
-          const int i = (low ? c : c - hc) * 8 + 2 * e;
-          const float2 k0 = cs[t][i], k1 = cs[t][i + 1];
-          const float s0 = low ? -k0.y : k0.y, s1 = low ? -k1.y : k1.y;
-          r[e] = pack_bf16(__uint_as_float(w[e] << 16) * k0.x + __uint_as_float(o << 16) * s0,
-                           __uint_as_float(w[e] & 0xffff0000u) * k1.x + __uint_as_float(o & 0xffff0000u) * s1);
+      if (!angles) {  // every warp once, with its first rows on their way
+        for (int k = tid; k < ntok * half; k += kThreads) {
+          const int i = k % half, t = k / half;
+          double turn = (double)a.pos[a.plan.axis[i] * a.pos_stride + tok0 + t] * a.plan.freq[i] *
+                        0.15915494309189533577;  // 1 / 2 pi
+          turn -= rint(turn);
+          float s, c;
+          sincospif(2.f * (float)turn, &s, &c);
+          cs[t][i] = make_float2(c, s);
         }
+        __syncthreads();
+        angles = true;
+      }
+      if (!has) break;
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        if (t0 + u >= ntok) break;
+        const float2* k2 = cs[t0 + u];
+        const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+        uint32_t r[4];
+        if constexpr (kAdjacent) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            r[e] = w[e];
+            if (p.chunk < rot_chunks) {
+              const float2 k = k2[p.chunk * 4 + e];
+              const float x0 = __uint_as_float(w[e] << 16), x1 = __uint_as_float(w[e] & 0xffff0000u);
+              r[e] = pack_bf16(x0 * k.x - x1 * k.y, x1 * k.x + x0 * k.y);
+            }
+          }
+        } else {
+          const int hc = rot_chunks / 2;  // chunks of a half
+          const bool low = p.chunk < hc;
+          const int from = lane + (low ? hc : -hc);
+          uint32_t o[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[e] = __shfl_sync(0xffffffffu, w[e], from & 31);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            r[e] = w[e];
+            if (p.chunk < rot_chunks) {
+              const float4 k = *reinterpret_cast<const float4*>(k2 + (low ? p.chunk : p.chunk - hc) * 8 + 2 * e);
+              const float s0 = low ? -k.y : k.y, s1 = low ? -k.w : k.w;
+              r[e] = pack_bf16(__uint_as_float(w[e] << 16) * k.x + __uint_as_float(o[e] << 16) * s0,
+                               __uint_as_float(w[e] & 0xffff0000u) * k.z + __uint_as_float(o[e] & 0xffff0000u) * s1);
+            }
+          }
+        }
+        if (p.live)
+          *reinterpret_cast<uint4*>(p.out + (tok0 + t0 + u) * p.out_stride) = make_uint4(r[0], r[1], r[2], r[3]);
       }
     }
-    if (live)
-      *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(x.out) + tok * x.out_stride +
-                                (int64_t)head * x.head_dim + c * 8) = make_uint4(r[0], r[1], r[2], r[3]);
   }
 }
 
@@ -173,6 +220,16 @@ extern "C" int qsa_rope(const qsa_rope_plan_t* plan, const qsa_rope_tensor_t* te
       if (j < k && rows_overlap(o, ok, n)) return QSA_ERR_INVALID_ARG;
     }
   }
-  const unsigned grid = (unsigned)(((int64_t)n + kTokens - 1) / kTokens);
-  return qsa_host::launch(rope_kernel, dim3(grid), dim3(kThreads), 0, static_cast<cudaStream_t>(stream), a);
+  // 8 tokens a CTA when that still fills the GPU (148 SMs x 8 CTAs), else fewer; then
+  // rows spread over grid.y until there are about as many CTAs, a row per warp at least
+  constexpr int kFill = 1024;
+  a.tokens = n >= 8 * kFill ? 8 : n >= 4 * kFill ? 4 : n >= 2 * kFill ? 2 : 1;
+  const int64_t gx = ((int64_t)n + a.tokens - 1) / a.tokens;
+  const int rounds = (a.items + kWarps - 1) / kWarps;
+  int gy = (int)(kFill / gx);
+  gy = gy < 1 ? 1 : gy > rounds ? rounds : gy;
+  const dim3 grid((unsigned)gx, (unsigned)gy);
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return plan->adjacent ? qsa_host::launch(rope_kernel<true>, grid, dim3(kThreads), 0, s, a)
+                        : qsa_host::launch(rope_kernel<false>, grid, dim3(kThreads), 0, s, a);
 }

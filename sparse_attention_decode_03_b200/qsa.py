@@ -780,18 +780,20 @@ class LaunchCall:
 
     def __init__(self, name: str, args: tuple, keep: tuple, device: torch.device, stream=None):
         self.name = name
-        self.fn = getattr(LIB, name)
-        self.args = args
+        self.fn = LIB[name]  # a function object of its own: its arguments are converted here, once
+        self.fn.restype = ctypes.c_int
+        self.args = tuple(x if t is None or not isinstance(x, (int, float, type(None))) else t(x)
+                          for x, t in zip(args, getattr(LIB, name).argtypes))
         self._keep = keep
         self.device = device.index if device.index is not None else torch.cuda.current_device()
         self.stream = stream
 
     def __call__(self):
-        if torch.cuda.current_device() != self.device:
+        if torch._C._cuda_getDevice() != self.device:
             with torch.cuda.device(self.device):
                 return self()
-        s = self.stream if self.stream is not None else torch.cuda.current_stream(self.device)
-        rc = self.fn(*self.args, ctypes.c_void_p(s.cuda_stream))
+        s = (self.stream.cuda_stream if self.stream is not None else torch._C._cuda_getCurrentRawStream(self.device))
+        rc = self.fn(*self.args, ctypes.c_void_p(s))
         if rc != QSA_OK:
             raise QSAError(self.name, rc)
 
