@@ -10,11 +10,14 @@
 // 2^-7 rad in fp32.  sin and cos of the reduced turn are taken in fp32.
 //
 // What bounds it: the bytes of the rows for a prompt chunk, latency for a decode
-// step.  A CTA takes up to 8 tokens and a share of their rows, a warp each row
-// (two of up to 128 dims), 16 bytes per lane; a half-split pair's partner chunk
-// comes by shuffle.  The rows of 4 tokens are requested together, before the
-// angles are computed: each CTA computes its tokens' R/2 sines and cosines once,
-// for all heads.  Few tokens spread their rows over more CTAs instead.
+// step.  A CTA takes up to 4 tokens and a share of their rows, 16 bytes per lane.
+// The chunks that turn (R / 8 of a row) and those that are only copied go to
+// different warps: with R = 64 of 256 dims a warp turns 4 rows at once instead of
+// one with three quarters of its lanes idle, which took 139 instructions a row
+// and 55 us for 8,192 tokens of 24 + 2 heads and an indexer's (now 48 us, 5.3 TB/s).  A half-split pair's partner chunk comes by
+// shuffle.  The chunks of all its tokens are requested together, before the angles
+// are computed: each CTA computes its tokens' R/2 sines and cosines once, for all
+// heads.  Few tokens spread their rows over more CTAs instead.
 #include "qsa_common.cuh"
 
 namespace {
@@ -23,13 +26,28 @@ using namespace qsa;
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kTokens = 8;  // tokens of a CTA at most
-constexpr int kAhead = 4;   // tokens whose rows a warp requests together
+constexpr int kTokens = 4;  // tokens of a CTA at most; a warp requests its chunks of all of them together
 constexpr int kMaxPairs = QSA_ROPE_MAX_PAIRS;
+
+// What turns a tensor's rows into warp-sized pieces: first the chunks that turn,
+// rows_per rows to a warp, then the copied ones, 32 to a warp (none in place).
+struct Cut {
+  int turn_chunks, copy_chunks, rows_per, turns, copies;
+};
+Cut cut_of(const qsa_rope_tensor_t& t, int rot_dim) {
+  Cut c;
+  c.turn_chunks = rot_dim / 8;
+  c.copy_chunks = (t.head_dim - rot_dim) / 8;
+  c.rows_per = 32 / c.turn_chunks;
+  c.turns = (t.heads + c.rows_per - 1) / c.rows_per;
+  c.copies = t.in == t.out ? 0 : (t.heads * c.copy_chunks + 31) / 32;
+  return c;
+}
 
 struct RopeArgs {
   qsa_rope_plan_t plan;
   qsa_rope_tensor_t t[QSA_ROPE_MAX_TENSORS];
+  Cut cut[QSA_ROPE_MAX_TENSORS];
   int32_t num_tensors;
   int32_t items;  // warp-sized pieces of one token's rows
   const int32_t* pos;
@@ -47,31 +65,36 @@ __device__ __forceinline__ uint4 ld_row(const void* p) {
   return r;
 }
 
-// A warp-sized piece of a token's rows: 256-dim rows take a warp, rows of up to
-// 128 dims half of one.
+// A piece, as one lane sees it.
 struct Piece {
   const __nv_bfloat16* in;
   __nv_bfloat16* out;
   int64_t in_stride, out_stride;
   int chunk;  // the lane's 8 dims of its row
-  bool live;
+  bool turns, live;
 };
 
 __device__ __forceinline__ Piece find_piece(const RopeArgs& a, int item, int lane) {
-  int ti = 0, rows_per;
-  for (;; ++ti) {
-    rows_per = a.t[ti].head_dim <= 128 ? 2 : 1;
-    const int cnt = (a.t[ti].heads + rows_per - 1) / rows_per;
-    if (item < cnt) break;
-    item -= cnt;
+  int ti = 0;
+  while (item >= a.cut[ti].turns + a.cut[ti].copies) {
+    item -= a.cut[ti].turns + a.cut[ti].copies;
+    ++ti;
   }
+  const Cut& c = a.cut[ti];
   const qsa_rope_tensor_t& x = a.t[ti];
-  const int lanes = 32 / rows_per;
   Piece p;
-  p.chunk = lane % lanes;
-  const int head = item * rows_per + lane / lanes;
-  // in place, the dims that do not turn stay where they are
-  p.live = head < x.heads && p.chunk * 8 < x.head_dim && !(x.in == x.out && p.chunk * 8 >= a.plan.rot_dim);
+  p.turns = item < c.turns;
+  int head;
+  if (p.turns) {
+    head = item * c.rows_per + lane / c.turn_chunks;
+    p.chunk = lane % c.turn_chunks;
+    p.live = head < x.heads && lane / c.turn_chunks < c.rows_per;
+  } else {
+    const int k = (item - c.turns) * 32 + lane;
+    head = k / c.copy_chunks;
+    p.chunk = c.turn_chunks + k % c.copy_chunks;
+    p.live = head < x.heads;
+  }
   const int64_t at = (int64_t)head * x.head_dim + p.chunk * 8;
   p.in = static_cast<const __nv_bfloat16*>(x.in) + at;
   p.out = static_cast<__nv_bfloat16*>(x.out) + at;
@@ -82,9 +105,9 @@ __device__ __forceinline__ Piece find_piece(const RopeArgs& a, int item, int lan
 
 template <bool kAdjacent>
 __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeArgs a) {
-  __shared__ float2 cs[kTokens][kMaxPairs];  // cos, sin
+  __shared__ __align__(16) float2 cs[kTokens][kMaxPairs];  // cos, sin
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int half = a.plan.rot_dim / 2, rot_chunks = a.plan.rot_dim / 8;
+  const int half = a.plan.rot_dim / 2;
   const int64_t tok0 = (int64_t)blockIdx.x * a.tokens;
   const int ntok = (int)min((int64_t)a.tokens, a.n - tok0);
   const int step = gridDim.y * kWarps;
@@ -92,68 +115,64 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
   bool angles = false;
   for (int item = blockIdx.y * kWarps + warp; item < a.items || !angles; item += step) {
     const bool has = item < a.items;
-    Piece p;
+    Piece p = {};
     if (has) p = find_piece(a, item, lane);
-    for (int t0 = 0; t0 < ntok; t0 += kAhead) {
-      uint4 v[kAhead];
+    uint4 v[kTokens];
+    const __nv_bfloat16* src = p.in + tok0 * p.in_stride;
 #pragma unroll
-      for (int u = 0; u < kAhead; ++u) {
-        v[u] = make_uint4(0, 0, 0, 0);
-        if (has && t0 + u < ntok && p.live)
-          v[u] = ld_row(p.in + (tok0 + t0 + u) * p.in_stride);
+    for (int u = 0; u < kTokens; ++u) {
+      v[u] = make_uint4(0, 0, 0, 0);
+      if (p.live && u < ntok) v[u] = ld_row(src + u * p.in_stride);
+    }
+    if (!angles) {  // every warp once, with its first rows on their way
+      for (int k = tid; k < ntok * half; k += kThreads) {
+        const int i = k % half, t = k / half;
+        double turn = (double)a.pos[a.plan.axis[i] * a.pos_stride + tok0 + t] * a.plan.freq[i] *
+                      0.15915494309189533577;  // 1 / 2 pi
+        turn -= rint(turn);
+        float s, c;
+        sincospif(2.f * (float)turn, &s, &c);
+        cs[t][i] = make_float2(c, s);
       }
-      if (!angles) {  // every warp once, with its first rows on their way
-        for (int k = tid; k < ntok * half; k += kThreads) {
-          const int i = k % half, t = k / half;
-          double turn = (double)a.pos[a.plan.axis[i] * a.pos_stride + tok0 + t] * a.plan.freq[i] *
-                        0.15915494309189533577;  // 1 / 2 pi
-          turn -= rint(turn);
-          float s, c;
-          sincospif(2.f * (float)turn, &s, &c);
-          cs[t][i] = make_float2(c, s);
-        }
-        __syncthreads();
-        angles = true;
-      }
-      if (!has) break;
+      __syncthreads();
+      angles = true;
+    }
+    if (!has) continue;
+    if (p.turns) {
 #pragma unroll
-      for (int u = 0; u < kAhead; ++u) {
-        if (t0 + u >= ntok) break;
-        const float2* k2 = cs[t0 + u];
+      for (int u = 0; u < kTokens; ++u) {
+        if (u >= ntok) break;
+        const float2* k2 = cs[u];
         const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
         uint32_t r[4];
         if constexpr (kAdjacent) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            r[e] = w[e];
-            if (p.chunk < rot_chunks) {
-              const float2 k = k2[p.chunk * 4 + e];
-              const float x0 = __uint_as_float(w[e] << 16), x1 = __uint_as_float(w[e] & 0xffff0000u);
-              r[e] = pack_bf16(x0 * k.x - x1 * k.y, x1 * k.x + x0 * k.y);
-            }
+            const float2 k = k2[p.chunk * 4 + e];
+            const float x0 = __uint_as_float(w[e] << 16), x1 = __uint_as_float(w[e] & 0xffff0000u);
+            r[e] = pack_bf16(x0 * k.x - x1 * k.y, x1 * k.x + x0 * k.y);
           }
         } else {
-          const int hc = rot_chunks / 2;  // chunks of a half
+          const int hc = a.plan.rot_dim / 16;  // chunks of a half
           const bool low = p.chunk < hc;
           const int from = lane + (low ? hc : -hc);
-          uint32_t o[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) o[e] = __shfl_sync(0xffffffffu, w[e], from & 31);
+          const float2* k8 = k2 + (low ? p.chunk : p.chunk - hc) * 8;
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            r[e] = w[e];
-            if (p.chunk < rot_chunks) {
-              const float4 k = *reinterpret_cast<const float4*>(k2 + (low ? p.chunk : p.chunk - hc) * 8 + 2 * e);
-              const float s0 = low ? -k.y : k.y, s1 = low ? -k.w : k.w;
-              r[e] = pack_bf16(__uint_as_float(w[e] << 16) * k.x + __uint_as_float(o[e] << 16) * s0,
-                               __uint_as_float(w[e] & 0xffff0000u) * k.z + __uint_as_float(o[e] & 0xffff0000u) * s1);
-            }
+            const uint32_t o = __shfl_sync(0xffffffffu, w[e], from & 31);
+            const float4 k = *reinterpret_cast<const float4*>(k8 + 2 * e);
+            const float s0 = low ? -k.y : k.y, s1 = low ? -k.w : k.w;
+            r[e] = pack_bf16(__uint_as_float(w[e] << 16) * k.x + __uint_as_float(o << 16) * s0,
+                             __uint_as_float(w[e] & 0xffff0000u) * k.z + __uint_as_float(o & 0xffff0000u) * s1);
           }
         }
-        if (p.live)
-          *reinterpret_cast<uint4*>(p.out + (tok0 + t0 + u) * p.out_stride) = make_uint4(r[0], r[1], r[2], r[3]);
+        v[u] = make_uint4(r[0], r[1], r[2], r[3]);
       }
     }
+    __nv_bfloat16* dst = p.out + tok0 * p.out_stride;
+#pragma unroll
+    for (int u = 0; u < kTokens; ++u)
+      if (p.live && u < ntok) *reinterpret_cast<uint4*>(dst + u * p.out_stride) = v[u];
   }
 }
 
@@ -205,7 +224,8 @@ extern "C" int qsa_rope(const qsa_rope_plan_t* plan, const qsa_rope_tensor_t* te
         (n > 1 && ((t.in_stride & 7) || (t.out_stride & 7))))
       return QSA_ERR_INVALID_ARG;
     a.t[k] = t;
-    a.items += t.head_dim <= 128 ? (t.heads + 1) / 2 : t.heads;
+    a.cut[k] = cut_of(t, plan->rot_dim);
+    a.items += a.cut[k].turns + a.cut[k].copies;
   }
   // an output may be its own input; any other overlap would read rotated rows
   for (int j = 0; j < num_tensors; ++j) {
@@ -220,10 +240,11 @@ extern "C" int qsa_rope(const qsa_rope_plan_t* plan, const qsa_rope_tensor_t* te
       if (j < k && rows_overlap(o, ok, n)) return QSA_ERR_INVALID_ARG;
     }
   }
-  // 8 tokens a CTA when that still fills the GPU (148 SMs x 8 CTAs), else fewer; then
-  // rows spread over grid.y until there are about as many CTAs, a row per warp at least
+  // 4 tokens a CTA when that still fills the GPU (148 SMs x 5 CTAs), else fewer; then rows
+  // spread over grid.y until there are about as many CTAs, a piece per warp at least
+  // (8,192 tokens: 4 of them 48 us, 2: 50, 8: 50; 57 tokens: 2.5 us, unspread 3.8)
   constexpr int kFill = 1024;
-  a.tokens = n >= 8 * kFill ? 8 : n >= 4 * kFill ? 4 : n >= 2 * kFill ? 2 : 1;
+  a.tokens = n >= 4 * kFill ? 4 : n >= 2 * kFill ? 2 : 1;
   const int64_t gx = ((int64_t)n + a.tokens - 1) / a.tokens;
   const int rounds = (a.items + kWarps - 1) / kWarps;
   int gy = (int)(kFill / gx);
