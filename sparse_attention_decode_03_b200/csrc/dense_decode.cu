@@ -992,16 +992,31 @@ __global__ void __launch_bounds__(kJoinThreads) dense_join_kernel(JoinArgs ja) {
       }
       __syncthreads();
       if (tile < (len + kStrip - 1) / kStrip) {
-        for (int h = h0; h < min(a.hq, h0 + kMaxCtas); ++h) {
-          const int64_t at = ((int64_t)q * a.hq + h) * max_tiles + tile;
-          const float l2 = lse_s[h - h0], bm = a.bmax[at];
-          if (l2 == -INFINITY || bm == -INFINITY) continue;  // no token seen
-          const float f = exp2f(bm - l2);
-          const float4 b = reinterpret_cast<const float4*>(a.bsum)[at];
-          sum.x += f * b.x;
-          sum.y += f * b.y;
-          sum.z += f * b.z;
-          sum.w += f * b.w;
+        const int n = min(a.hq - h0, kMaxCtas);
+        const int64_t at = ((int64_t)q * a.hq + h0) * max_tiles + tile;
+        constexpr int kHeads = 8;  // heads requested together
+        for (int h = 0; h < n; h += kHeads) {
+          float bm[kHeads];
+          float4 b[kHeads];
+#pragma unroll
+          for (int k = 0; k < kHeads; ++k) {
+            bm[k] = -INFINITY;
+            b[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (h + k < n) {
+              bm[k] = a.bmax[at + (h + k) * max_tiles];
+              b[k] = reinterpret_cast<const float4*>(a.bsum)[at + (h + k) * max_tiles];
+            }
+          }
+#pragma unroll
+          for (int k = 0; k < kHeads; ++k) {
+            if (h + k >= n) break;
+            const float l2 = lse_s[h + k];
+            const float f = l2 == -INFINITY || bm[k] == -INFINITY ? 0.f : exp2f(bm[k] - l2);  // 0: no token seen
+            sum.x += f * b[k].x;
+            sum.y += f * b[k].y;
+            sum.z += f * b[k].z;
+            sum.w += f * b[k].w;
+          }
         }
       }
     }
