@@ -860,29 +860,31 @@ struct JoinArgs {
 // The partial slot of CTA c's piece of a pair that spans several CTAs.
 __device__ __forceinline__ int slot_of(const int2& span, int c) { return 2 * c + (c == span.x ? 1 : 0); }
 
-// Base-2 lse of (q, h), by one warp: the joined pieces' or, for a pair that one
-// CTA held, the one already in lse.
+// Base-2 lse of (q, h), by 8 neighbouring lanes: the joined pieces' or, for a
+// pair that one CTA held, the one already in lse.
 __device__ __forceinline__ float joined_lse2(const DenseArgs& a, int q, int h) {
-  const int lane = threadIdx.x & 31;
+  const int sub = threadIdx.x & 7;
+  const unsigned lanes = 0xffu << (threadIdx.x & 24);
   const int2 p = a.span[q * a.hkv + h / a.G];
   if (p.y < p.x) return -INFINITY;
   if (p.x == p.y) return a.lse[(size_t)q * a.hq + h] * 1.44269504088896340736f;
   const int row = h % a.G;
   float M = -INFINITY;
-  for (int c = p.x + lane; c <= p.y; c += 32) M = fmaxf(M, a.part_lse[(size_t)slot_of(p, c) * a.G + row]);
+  for (int c = p.x + sub; c <= p.y; c += 8) M = fmaxf(M, a.part_lse[(size_t)slot_of(p, c) * a.G + row]);
 #pragma unroll
-  for (int d = 16; d; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+  for (int d = 4; d; d >>= 1) M = fmaxf(M, __shfl_xor_sync(lanes, M, d));
   if (M == -INFINITY) return -INFINITY;
   float L = 0.f;
-  for (int c = p.x + lane; c <= p.y; c += 32) L += exp2f(a.part_lse[(size_t)slot_of(p, c) * a.G + row] - M);
+  for (int c = p.x + sub; c <= p.y; c += 8) L += exp2f(a.part_lse[(size_t)slot_of(p, c) * a.G + row] - M);
 #pragma unroll
-  for (int d = 16; d; d >>= 1) L += __shfl_xor_sync(0xffffffffu, L, d);
+  for (int d = 4; d; d >>= 1) L += __shfl_xor_sync(lanes, L, d);
   return M + log2f(L);
 }
 
 // Blocks 0 .. nq*hq-1: one (query, head) each; the pieces are spread over 4
 // groups of 64 threads (4 dims each) and summed in a fixed order.  The blocks
-// after them: 256 tiles (1,024 micro-blocks) of one query's sequence each.
+// after them add up weights: 64 strips (256 micro-blocks) of one query's sequence
+// each, the heads spread over the 4 groups.
 __global__ void __launch_bounds__(kJoinThreads) dense_join_kernel(JoinArgs ja) {
   const DenseArgs& a = ja.d;
   pdl_launch_dependents();
@@ -970,47 +972,51 @@ __global__ void __launch_bounds__(kJoinThreads) dense_join_kernel(JoinArgs ja) {
   }
   // ---- weights.  The first query of a sequence adds up all of the sequence's
   // queries in order, so the total does not depend on which block runs first.
+  constexpr int kHeads = 8, kRound = 4 * kHeads;  // heads of a group and of the block at once
   const int64_t wb = blockIdx.x - n_join;
   const int q0 = (int)(wb / ja.mass_blocks);
+  const int strip = (int)(wb % ja.mass_blocks) * 64 + (tid & 63), grp = tid >> 6;
   const int seq = a.q_seq[q0];
   if (query_len(a, q0, false) == 0) return;
-  for (int q = 0; q < q0; ++q)
-    if (a.q_seq[q] == seq && query_len(a, q, false) > 0) return;
-  const int tile = (int)(wb % ja.mass_blocks) * kJoinThreads + tid;
-  const int64_t max_tiles = (int64_t)a.mpps * kStripsPerPage;
+  const int64_t max_strips = (int64_t)a.mpps * kStripsPerPage;
+  __shared__ unsigned same_s[kJoinThreads / 32];  // queries of this sequence, 256 at a time
   float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
   int longest = 0;
-  for (int q = q0; q < a.nq; ++q) {
-    const int len = query_len(a, q, false);
-    if (len == 0 || a.q_seq[q] != seq) continue;
-    longest = max(longest, len);
-    for (int h0 = 0; h0 < a.hq; h0 += kMaxCtas) {
-      __syncthreads();
-      for (int h = h0 + (tid >> 5); h < min(a.hq, h0 + kMaxCtas); h += kJoinThreads / 32) {
-        const float v = joined_lse2(a, q, h);
-        if ((tid & 31) == 0) lse_s[h - h0] = v;
-      }
-      __syncthreads();
-      if (tile < (len + kStrip - 1) / kStrip) {
-        const int n = min(a.hq - h0, kMaxCtas);
-        const int64_t at = ((int64_t)q * a.hq + h0) * max_tiles + tile;
-        constexpr int kHeads = 8;  // heads requested together
-        for (int h = 0; h < n; h += kHeads) {
+  for (int qb = 0; qb < a.nq; qb += kJoinThreads) {
+    const int qt = qb + tid;
+    const unsigned same = __ballot_sync(0xffffffffu, qt < a.nq && a.q_seq[qt] == seq && query_len(a, qt, false) > 0);
+    __syncthreads();
+    if (lane == 0) same_s[warp] = same;
+    __syncthreads();
+    for (int v = 0; v < kJoinThreads / 32; ++v)
+      for (unsigned bits = same_s[v]; bits; bits &= bits - 1) {
+        const int q = qb + v * 32 + __ffs(bits) - 1;
+        if (q < q0) return;  // not the first: the same in every thread
+        const int len = query_len(a, q, false);
+        const bool on = strip < (len + kStrip - 1) / kStrip;
+        longest = max(longest, len);
+        for (int h0 = 0; h0 < a.hq; h0 += kRound) {
           float bm[kHeads];
           float4 b[kHeads];
 #pragma unroll
-          for (int k = 0; k < kHeads; ++k) {
+          for (int k = 0; k < kHeads; ++k) {  // head h0 + 4k + grp, requested before its lse is known
+            const int h = h0 + 4 * k + grp;
             bm[k] = -INFINITY;
             b[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (h + k < n) {
-              bm[k] = a.bmax[at + (h + k) * max_tiles];
-              b[k] = reinterpret_cast<const float4*>(a.bsum)[at + (h + k) * max_tiles];
+            if (on && h < a.hq) {
+              const int64_t at = ((int64_t)q * a.hq + h) * max_strips + strip;
+              bm[k] = a.bmax[at];
+              b[k] = reinterpret_cast<const float4*>(a.bsum)[at];
             }
           }
+          const int hl = h0 + (tid >> 3);
+          const float v2 = hl < a.hq ? joined_lse2(a, q, hl) : -INFINITY;
+          __syncthreads();
+          if ((tid & 7) == 0) lse_s[tid >> 3] = v2;
+          __syncthreads();
 #pragma unroll
           for (int k = 0; k < kHeads; ++k) {
-            if (h + k >= n) break;
-            const float l2 = lse_s[h + k];
+            const float l2 = lse_s[4 * k + grp];
             const float f = l2 == -INFINITY || bm[k] == -INFINITY ? 0.f : exp2f(bm[k] - l2);  // 0: no token seen
             sum.x += f * b[k].x;
             sum.y += f * b[k].y;
@@ -1019,14 +1025,24 @@ __global__ void __launch_bounds__(kJoinThreads) dense_join_kernel(JoinArgs ja) {
           }
         }
       }
-    }
+  }
+  acc_s[grp][tid & 63] = sum;
+  __syncthreads();
+  if (grp) return;
+#pragma unroll
+  for (int k = 1; k < 4; ++k) {
+    const float4 y = acc_s[k][tid];
+    sum.x += y.x;
+    sum.y += y.y;
+    sum.z += y.z;
+    sum.w += y.w;
   }
   const int blocks = (longest + kRatio - 1) / kRatio;
   const float v[4] = {sum.x, sum.y, sum.z, sum.w};
   const int64_t row = (int64_t)seq * ja.mass_ld;
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    const int b = tile * kStripRuns + k;
+    const int b = strip * kStripRuns + k;
     if (b < blocks) ja.mass_out[row + b] = ja.decay * ja.mass_in[row + b] + v[k];
   }
 }
@@ -1138,7 +1154,7 @@ extern "C" int qsa_dense_decode(const qsa_cache_t* cache, const void* q, int32_t
   j.mass_ld = mass_ld;
   j.decay = decay;
   const int64_t tiles = (int64_t)c.max_pages_per_seq * kStripsPerPage;
-  j.mass_blocks = (int32_t)((tiles + kJoinThreads - 1) / kJoinThreads);
+  j.mass_blocks = (int32_t)((tiles + 63) / 64);
   const int64_t grid = (int64_t)nq * hq + (mass ? (int64_t)nq * j.mass_blocks : 0);
   if (grid > 0x7fffffff) return QSA_ERR_UNSUPPORTED;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
