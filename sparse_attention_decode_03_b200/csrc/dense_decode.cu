@@ -39,12 +39,14 @@ constexpr int kStripRuns = kStrip / kRatio;
 constexpr int kStripsPerPage = kPage / kStrip;
 constexpr int kMaxCtas = 256;                    // partial slots reserved: 2 per CTA
 constexpr int kQStride = kHeadDim * 2 + 16;      // Q rows 528 B apart: conflict-free 16-byte fragment reads
-constexpr int kQBytes = 16 * kQStride;
 constexpr int kSlice = 32;                       // dims of O that the warps join at once
 constexpr int kSlices = kHeadDim / kSlice;
-constexpr int kCombRow = kSlice + 4;             // floats; the skew spreads the rows over the banks
+constexpr int kSliceBytes = 16 * kSlice * 4;     // of one warp
 constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s
-constexpr int kTab = 64;  // queries whose length a CTA keeps in shared memory
+constexpr int kTab = 48;  // queries whose length a CTA keeps in shared memory
+// Q rows of the next pairs: 32 rows' room, as many groups of G rows as fit (6 at most);
+// row 31 stays zero for the rows beyond G
+constexpr int kQRows = 32, kMaxQ = 6;
 constexpr int kBarConsumers = 1;
 // The running maximum a warp subtracts may lag the true one by this much (base
 // 2), so that O is seldom rescaled: exp2 stays below 2^8, harmless in fp32 sums
@@ -72,20 +74,19 @@ struct Lay {
   // seen the stage's last phase end before it waits for the next.  A parity wait
   // cannot tell a phase from the one two before, so another warp could run ahead.
   static_assert(kStages % kWarps == 0, "a stage has one consumer");
-  static constexpr int kCombWarp = 16 * kCombRow;               // floats of one warp's slice
-  static constexpr int kOffQ = kStages * kStageBytes;           // two pieces' Q rows
-  static constexpr int kOffComb = kOffQ + 2 * kQBytes;
-  static constexpr int kOffML = kOffComb + kWarps * kCombWarp * 4;  // [warp][16 rows] (m, l)
+  static constexpr int kOffQ = kStages * kStageBytes;           // the pieces' Q rows
+  static constexpr int kOffML = kOffQ + kQRows * kQStride;      // [warp][16 rows] (m, l)
   static constexpr int kOffScale = kOffML + kWarps * 16 * 8;    // e4m3: logit scale of each row
-  static constexpr int kOffValid = kOffScale + 16 * 4;          // tokens in each stage
+  static constexpr int kOffHeld = kOffScale + kMaxQ * 16 * 4;   // each warp's held stage
+  static constexpr int kOffValid = kOffHeld + 8 * 4;          // tokens in each stage
   static constexpr int kOffPlan = (kOffValid + kStages * 4 + 15) & ~15;
   static constexpr int kOffTab = kOffPlan + 16 * 8;             // (len, seq) of queries q0 ..
-  static constexpr int kOffBar = kOffTab + kTab * 8;            // full, empty, Q full [2], Q empty [2]
-  static constexpr int kOffAbort = kOffBar + (2 * kStages + 4) * 8;
+  static constexpr int kOffBar = kOffTab + kTab * 8;            // full, empty, Q full, Q empty
+  static constexpr int kOffAbort = kOffBar + 2 * (kStages + kMaxQ) * 8;
   static constexpr int kSmem = kOffAbort + 16;
   static constexpr int kIssue = 3;  // copy-warp lanes that wait and issue together, a tile each
   static_assert(kSmem <= 232448, "shared memory budget");
-  static_assert(kWarps * kSlices * kCombWarp * 4 <= kOffQ, "a whole O of every warp fits the ring");
+  static_assert(kSlices * kSliceBytes <= kStageBytes, "a warp's O fits the stage it holds");
 };
 
 struct DenseArgs {
@@ -105,6 +106,7 @@ struct DenseArgs {
   float* bsum;  // [nq][hq][max tiles][4] sums of exp2(z - bmax) per micro-block, or null
   float* bmax;  // [nq][hq][max tiles]
   int32_t ctas;
+  int32_t q_bufs;  // groups of Q rows held at once
   int32_t* st;
 };
 
@@ -149,8 +151,12 @@ __device__ __forceinline__ int share_of(const Shares& s, int x) {  // the CTA th
 }
 
 template <class LY>
+__device__ __forceinline__ int cost_of(int tiles) {  // a pair of one tile joins nothing
+  return tiles > 1 ? LY::kPieceCost : 1;
+}
+template <class LY>
 __device__ __forceinline__ int places_of(int len) {
-  return len ? tiles_of<LY>(len) + LY::kPieceCost : 0;
+  return len ? tiles_of<LY>(len) + cost_of<LY>(tiles_of<LY>(len)) : 0;
 }
 
 // A CTA's position in the list: a piece of pair (q, g).
@@ -165,21 +171,18 @@ struct Walk {
 
 template <class LY>
 __device__ __forceinline__ bool set_span(Walk& w, int x0, int x1) {
-  const int lo = w.begin + LY::kPieceCost;
+  const int nt = tiles_of<LY>(w.len), lo = w.begin + cost_of<LY>(nt);
   w.t0 = max(0, x0 - lo);
-  w.t1 = min(tiles_of<LY>(w.len), x1 - lo);
+  w.t1 = min(nt, x1 - lo);
   return w.t1 > 0;
 }
 
-// Whether tiles of a pair after this one lie in the share.
+// Step to the next pair with tiles in the share; false when there is none.
 template <class LY>
-__device__ __forceinline__ bool has_next(const Walk& w, int x1) {
-  return w.begin + places_of<LY>(w.len) + LY::kPieceCost < x1;
-}
-
-template <class LY>
-__device__ __forceinline__ void next_piece(const DenseArgs& a, Walk& w, int x1) {
-  w.begin += places_of<LY>(w.len);
+__device__ __forceinline__ bool next_piece(const DenseArgs& a, Walk& w, int x1) {
+  const int begin = w.begin + places_of<LY>(w.len);
+  if (begin >= x1) return false;
+  w.begin = begin;
   if (w.g + 1 < a.hkv) {
     ++w.g;
   } else {
@@ -192,7 +195,7 @@ __device__ __forceinline__ void next_piece(const DenseArgs& a, Walk& w, int x1) 
     } while (w.len == 0);
     w.g = 0;
   }
-  set_span<LY>(w, 0, x1);
+  return set_span<LY>(w, 0, x1);
 }
 
 // Bounded wait; false (and the abort flag) when the limit passed.
@@ -224,34 +227,41 @@ __device__ void copy_warp(const DenseArgs& a, uint8_t* smem, Walk w, int x1) {
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + LY::kOffAbort);
   const uint64_t policy = l2_policy_evict_first(), policy_q = l2_policy_evict_normal();
   uint32_t T = 0, n_issued = 0;  // tiles taken up, tiles whose copies were issued
-  uint32_t piece = 0;            // pieces whose Q rows were issued
-  const uint32_t q_full = empty + LY::kStages * 8, q_empty = q_full + 16;
+  uint32_t piece = 0, qi = 0, lap = 0;  // pieces whose Q rows were issued; the next one's place and its round
+  const uint32_t q_full = empty + LY::kStages * 8, q_empty = q_full + kMaxQ * 8;
+  auto lookup = [&](const Walk& at, int t) {
+    int page = -1;
+    if (t < at.t1) page = __ldg(a.bt + (int64_t)at.seq * a.mpps + t / LY::kTilesPerPage);
+    return page;
+  };
+  int page = lookup(w, w.t0 + lane);
   bool more = true, stop = false;
   while (more && !stop) {
     {  // Q rows of the group, 512 bytes each
-      const uint32_t b = piece & 1u;
-      if (piece >= 2 && !wait_bar(a, q_empty + b * 8, ((piece >> 1) - 1) & 1u, abort_flag)) stop = true;
+      if (lap > 0 && !wait_bar(a, q_empty + qi * 8, (lap - 1) & 1u, abort_flag)) stop = true;
       if (__any_sync(0xffffffffu, stop)) {
         stop = true;
         break;
       }
-      if (lane == 0) mbar_arrive_expect_tx(q_full + b * 8, a.G * kHeadDim * 2);
+      if (lane == 0) mbar_arrive_expect_tx(q_full + qi * 8, a.G * kHeadDim * 2);
       __syncwarp();
       if (lane < a.G)
-        bulk_g2s(smem_u32(smem + LY::kOffQ) + b * kQBytes + lane * kQStride,
-                 a.q + ((size_t)w.q * a.hq + (size_t)w.g * a.G + lane) * kHeadDim, kHeadDim * 2, q_full + b * 8,
+        bulk_g2s(smem_u32(smem + LY::kOffQ) + (qi * a.G + lane) * kQStride,
+                 a.q + ((size_t)w.q * a.hq + (size_t)w.g * a.G + lane) * kHeadDim, kHeadDim * 2, q_full + qi * 8,
                  policy_q);
       ++piece;
+      if (++qi == (uint32_t)a.q_bufs) {
+        qi = 0;
+        ++lap;
+      }
     }
-    // lane = tile: pages of 32 tiles at a time, the next batch's loads issued before this batch's copies
-    auto lookup = [&](int t) {
-      int page = -1;
-      if (t < w.t1) page = __ldg(a.bt + (int64_t)w.seq * a.mpps + t / LY::kTilesPerPage);
-      return page;
-    };
-    int page = lookup(w.t0 + lane);
+    // lane = tile: pages of 32 tiles at a time, the next batch's (of this pair or the
+    // next one) requested before this batch's copies
+    Walk after = w;
+    more = next_piece<LY>(a, after, x1);
+    const int page_after = more ? lookup(after, after.t0 + lane) : -1;
     for (int tb = w.t0; tb < w.t1 && !stop; tb += 32) {
-      const int page_next = lookup(tb + 32 + lane);
+      const int page_next = lookup(w, tb + 32 + lane);
       const int n = min(32, w.t1 - tb), t = tb + lane;
       const bool bad = page < 0 || page >= a.num_pages;
       if (lane < n && bad) flag(a.st, QSA_DEV_BAD_PAGE);
@@ -292,23 +302,22 @@ __device__ void copy_warp(const DenseArgs& a, uint8_t* smem, Walk w, int x1) {
       T += n;
       page = page_next;
     }
-    if (!stop) {
-      more = has_next<LY>(w, x1);
-      if (more) next_piece<LY>(a, w, x1);
-    }
+    w = after;
+    page = page_after;
   }
   // never leave the CTA with copies in flight: each lane waits for one stage's last copy
-  const uint32_t left = min(n_issued, (uint32_t)LY::kStages), left_q = min(piece, 2u);
+  const uint32_t left = min(n_issued, (uint32_t)LY::kStages), left_q = min(piece, (uint32_t)a.q_bufs);
   uint32_t bar = 0, parity = 0;
   if (lane < (int)left) {
     const uint32_t t = n_issued - 1 - lane;
     bar = full + (t % LY::kStages) * 8;
     parity = (t / LY::kStages) & 1u;
-  } else if (lane >= 30 && lane - 30 < (int)left_q) {
-    const uint32_t t = piece - 1 - (lane - 30);
-    bar = q_full + (t & 1u) * 8;
-    parity = (t >> 1) & 1u;
+  } else if (lane >= 24 && lane - 24 < (int)left_q) {
+    const uint32_t t = piece - 1 - (lane - 24);
+    bar = q_full + (t % a.q_bufs) * 8;
+    parity = (t / a.q_bufs) & 1u;
   }
+  static_assert(LY::kStages <= 24 && kMaxQ <= 8, "a lane per copy that may be in flight");
   if (bar) {
     const uint64_t s0 = global_timer_ns();
     while (!mbar_try_wait(bar, parity))
@@ -349,12 +358,12 @@ __device__ void consumers(const DenseArgs& a, uint8_t* smem, Walk w, const Share
   const int gq = lane >> 2, tq = lane & 3;
   const uint32_t ring = smem_u32(smem);
   const uint32_t full = smem_u32(smem + LY::kOffBar), empty = full + LY::kStages * 8;
-  const uint32_t q_full = empty + LY::kStages * 8, q_empty = q_full + 16;
+  const uint32_t q_full = empty + LY::kStages * 8, q_empty = q_full + kMaxQ * 8;
   const volatile int* valid = reinterpret_cast<const volatile int*>(smem + LY::kOffValid);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + LY::kOffAbort);
-  float* comb = reinterpret_cast<float*>(smem + LY::kOffComb);
+  int* held_s = reinterpret_cast<int*>(smem + LY::kOffHeld);
   float2* ml = reinterpret_cast<float2*>(smem + LY::kOffML);
-  float* row_scale = reinterpret_cast<float*>(smem + LY::kOffScale);
+  float* scales = reinterpret_cast<float*>(smem + LY::kOffScale);
   constexpr int kWarps = LY::kWarps, kConsumerThreads = LY::kConsumerThreads;
   const int G = a.G;
   const int64_t max_strips = (int64_t)a.mpps * kStripsPerPage;
@@ -378,20 +387,24 @@ __device__ void consumers(const DenseArgs& a, uint8_t* smem, Walk w, const Share
   const int kr0 = tile_row<F8>(0, kt, ke);  // BF16: the row, for the chunk swizzle
 
   uint32_t T_base = 0;
-  for (uint32_t piece = 0;; ++piece) {
+  uint32_t qi = 0, lap = 0;  // place and round of the piece's Q rows
+  for (;;) {
     const int n_tiles = w.t1 - w.t0;
-    // ---- Q rows of the group (rows beyond it are zero, written once at the start)
-    const uint32_t qb = smem_u32(smem + LY::kOffQ) + (piece & 1u) * kQBytes;
-    if (!*abort_flag) wait_bar(a, q_full + (piece & 1u) * 8, (piece >> 1) & 1u, abort_flag);
+    // ---- Q rows of the group (for the rows beyond it, the one that stays zero)
+    const uint32_t q_at = smem_u32(smem + LY::kOffQ), qb = q_at + qi * G * kQStride;
+    const uint32_t q_row0 = gq < G ? qb + gq * kQStride : q_at + (kQRows - 1) * kQStride;
+    const uint32_t q_row1 = gq + 8 < G ? qb + (gq + 8) * kQStride : q_at + (kQRows - 1) * kQStride;
+    if (!*abort_flag) wait_bar(a, q_full + qi * 8, lap & 1u, abort_flag);
     __syncwarp();
     float sc0 = a.scale_log2, sc1 = a.scale_log2;
     if constexpr (F8) {
+      float* row_scale = scales + qi * 16;
       // FP16 operands: each row is scaled by a power of two into FP16's range (exact down
       // to 2^-38 of its largest element) and its logit scale takes the factor back
 #pragma unroll
       for (int it = 0; it < 3; ++it) {
         const int row = warp + kWarps * it;
-        if (row >= 16) break;
+        if (row >= G) break;
         const uint4 v = lds128(qb + row * kQStride + lane * 16);
         uint32_t x[4] = {v.x, v.y, v.z, v.w};
         uint32_t mx = 0;  // largest magnitude, as ordered bits
@@ -411,8 +424,8 @@ __device__ void consumers(const DenseArgs& a, uint8_t* smem, Walk w, const Share
       }
       fence_proxy_async();  // these writes come before the copy of the piece after next
       named_bar_sync(kBarConsumers, kConsumerThreads);
-      sc0 = row_scale[gq];
-      sc1 = row_scale[gq + 8];
+      if (gq < G) sc0 = row_scale[gq];
+      if (gq + 8 < G) sc1 = row_scale[gq + 8];
     }
 
     float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
@@ -421,6 +434,7 @@ __device__ void consumers(const DenseArgs& a, uint8_t* smem, Walk w, const Share
     for (int nt = 0; nt < 32; ++nt) o[nt][0] = o[nt][1] = o[nt][2] = o[nt][3] = 0.f;
 
     const int rank = (int)((warp + kWarps - T_base % kWarps) % kWarps);  // this warp's first tile of the piece
+    int held = -1;
     for (int ti = rank; ti < n_tiles; ti += kWarps) {
       const uint32_t T = T_base + ti;
       const int stage = (int)(T % LY::kStages);
@@ -442,8 +456,8 @@ __device__ void consumers(const DenseArgs& a, uint8_t* smem, Walk w, const Share
 #pragma unroll
         for (int i = 0; i < 4; ++i) {  // 64 dims: lane tq holds dims 64i + 16tq .. + 15
           const uint32_t qo = (4 * i + tq) * 32;
-          const uint4 qa0 = lds128(qb + gq * kQStride + qo), qa1 = lds128(qb + gq * kQStride + qo + 16);
-          const uint4 qc0 = lds128(qb + (gq + 8) * kQStride + qo), qc1 = lds128(qb + (gq + 8) * kQStride + qo + 16);
+          const uint4 qa0 = lds128(q_row0 + qo), qa1 = lds128(q_row0 + qo + 16);
+          const uint4 qc0 = lds128(q_row1 + qo), qc1 = lds128(q_row1 + qo + 16);
 #pragma unroll
           for (int b = 0; b < kS; ++b)
 #pragma unroll
@@ -463,8 +477,8 @@ __device__ void consumers(const DenseArgs& a, uint8_t* smem, Walk w, const Share
 #pragma unroll
         for (int i = 0; i < 8; ++i) {  // 32 dims of atom i / 2: lane tq holds chunk 2tq + i % 2
           const int ch = 2 * tq + (i & 1);
-          const uint4 qa = lds128(qb + gq * kQStride + (8 * (i >> 1) + ch) * 16);
-          const uint4 qc = lds128(qb + (gq + 8) * kQStride + (8 * (i >> 1) + ch) * 16);
+          const uint4 qa = lds128(q_row0 + (8 * (i >> 1) + ch) * 16);
+          const uint4 qc = lds128(q_row1 + (8 * (i >> 1) + ch) * 16);
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             const uint4 kk = lds128(kb + k_off[j] + (i >> 1) * 1024 + ((ch ^ kr0) << 4));
@@ -629,18 +643,78 @@ __device__ void consumers(const DenseArgs& a, uint8_t* smem, Walk w, const Share
           }
         }
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(empty + stage * 8);
+      held = stage;
+      if (ti + kWarps < n_tiles) {  // the last stage is kept for the join
+        __syncwarp();
+        if (lane == 0) mbar_arrive(empty + stage * 8);
+      }
     }
     T_base += n_tiles;
     __syncwarp();
-    if (lane == 0) mbar_arrive(q_empty + (piece & 1u) * 8);
+    if (lane == 0) mbar_arrive(q_empty + qi * 8);
+    if (++qi == (uint32_t)a.q_bufs) {
+      qi = 0;
+      ++lap;
+    }
 
     // ---- join the warps' (m, l, O)
     l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
     l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
     l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
     l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
+    // whole pair here: straight to out; else to the partial slot of the pair that this
+    // CTA took over (0) or leaves unfinished (1)
+    const int nt_pair = tiles_of<LY>(w.len);
+    const bool direct = w.t0 == 0 && w.t1 == nt_pair;
+    const int slot = 2 * blockIdx.x + (w.t0 == 0 ? 1 : 0);
+    const size_t out_row = direct ? (size_t)w.q * a.hq + (size_t)w.g * G : (size_t)slot * G;
+    auto put_lse = [&](float lse_0, float lse_1) {  // by one warp; base 2
+      float* at = (direct ? a.lse : a.part_lse) + out_row;
+      const float f = direct ? 0.69314718055994530942f : 1.f;
+      if (tq == 0) {
+        if (gq < G) at[gq] = lse_0 * f;
+        if (gq + 8 < G) at[gq + 8] = lse_1 * f;
+      }
+      if (w.t0 == 0 && lane == 0)
+        a.span[w.q * a.hkv + w.g] =
+            make_int2(blockIdx.x, direct ? blockIdx.x
+                                         : share_of(sh, w.begin + cost_of<LY>(nt_pair) + nt_pair - 1));
+    };
+    // the columns and n-tiles of dim slice sl (see the join below)
+    auto e_of = [](int sl) { return F8 ? (sl >> 1) & 1 : sl & 1; };
+    auto i0_of = [](int sl) { return F8 ? 16 * (sl >> 2) + 8 * (sl & 1) : 8 * (sl >> 1); };
+    if (n_tiles == 1) {
+      // one warp had the piece: nothing to join, the others go on to the next one
+      if (held >= 0 && lane == 0) mbar_arrive(empty + held * 8);
+      if (rank == 0) {
+        const float f0 = l0 > 0.f ? 1.f / l0 : l0, f1 = l1 > 0.f ? 1.f / l1 : l1;  // 0: no token; NaN stays NaN
+        put_lse(m0 + log2f(l0), m1 + log2f(l1));
+#pragma unroll
+        for (int sl = 0; sl < kSlices; ++sl) {
+          const int e = e_of(sl), i0 = i0_of(sl);
+          const int dim = F8 ? 128 * (sl >> 2) + 32 * tq + 16 * e + 8 * (sl & 1) : kSlice * sl + 8 * tq;
+#pragma unroll
+          for (int hr = 0; hr < 2; ++hr) {
+            if (gq + 8 * hr >= G) continue;
+            const float f = hr ? f1 : f0;
+            float y[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) y[k] = o[i0 + k][2 * hr + e] * f;
+            const size_t at = (out_row + gq + 8 * hr) * kHeadDim + dim;
+            if (direct) {
+              *reinterpret_cast<uint4*>(a.out + at) = make_uint4(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]),
+                                                                 pack_bf16(y[4], y[5]), pack_bf16(y[6], y[7]));
+            } else {
+              *reinterpret_cast<float4*>(a.part_o + at) = make_float4(y[0], y[1], y[2], y[3]);
+              *reinterpret_cast<float4*>(a.part_o + at + 4) = make_float4(y[4], y[5], y[6], y[7]);
+            }
+          }
+        }
+      }
+      if (!next_piece<LY>(a, w, x1)) break;
+      continue;
+    }
+    if (lane == 0) held_s[rank] = held;
     if (tq == 0) {
       ml[rank * 16 + gq] = make_float2(m0, l0);
       ml[rank * 16 + gq + 8] = make_float2(m1, l1);
@@ -663,90 +737,64 @@ __device__ void consumers(const DenseArgs& a, uint8_t* smem, Walk w, const Share
       fac[hr] = L > 0.f ? exp2_fast((hr ? m1 : m0) - sub) / L : L;  // L = 0: no token; NaN stays NaN
       lse2[hr] = M + log2f(L);                                      // -inf when L = 0
     }
-    // whole pair here: straight to out; else to the partial slot of the pair that this
-    // CTA took over (0) or leaves unfinished (1)
-    const int nt_pair = tiles_of<LY>(w.len);
-    const bool direct = w.t0 == 0 && w.t1 == nt_pair;
-    const int slot = 2 * blockIdx.x + (w.t0 == 0 ? 1 : 0);
-    if (warp == 0 && tq == 0) {
-#pragma unroll
-      for (int hr = 0; hr < 2; ++hr) {
-        const int row = gq + 8 * hr;
-        if (row < G) {
-          if (direct)
-            a.lse[(size_t)w.q * a.hq + (size_t)w.g * G + row] = lse2[hr] * 0.69314718055994530942f;
-          else
-            a.part_lse[(size_t)slot * G + row] = lse2[hr];
-        }
-      }
-    }
-    if (w.t0 == 0 && tid == 0)
-      a.span[w.q * a.hkv + w.g] =
-          make_int2(blockIdx.x, direct ? blockIdx.x : share_of(sh, w.begin + LY::kPieceCost + nt_pair - 1));
-    // O: slices of 32 dims go through shared memory, every warp's to its own place, and a
-    // thread adds up one float4 of them.  After the share's last piece the ring is free and
-    // takes all the slices at once; before, one slice at a time.
-    const bool last = !has_next<LY>(w, x1);
-    const size_t out_row = direct ? (size_t)w.q * a.hq + (size_t)w.g * G : (size_t)slot * G;
-    auto add_up = [&](const float* base, int sl, int item) {
-      const int row = item >> 3, col = (item & 7) * 4;
-      if (row >= G) return;
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int v = 0; v < kWarps; ++v) {
-        if (v >= nw) break;
-        const float4 y = *reinterpret_cast<const float4*>(base + v * LY::kCombWarp + row * kCombRow + col);
-        acc.x += y.x;
-        acc.y += y.y;
-        acc.z += y.z;
-        acc.w += y.w;
-      }
-      const int dim = F8 ? 128 * (sl >> 2) + 32 * (col >> 3) + 16 * ((sl >> 1) & 1) + 8 * (sl & 1) + (col & 7)
-                         : kSlice * sl + col;
-      const size_t at = (out_row + row) * kHeadDim + dim;
-      if (direct)
-        *reinterpret_cast<uint2*>(a.out + at) = make_uint2(pack_bf16(acc.x, acc.y), pack_bf16(acc.z, acc.w));
-      else
-        *reinterpret_cast<float4*>(a.part_o + at) = acc;
-    };
+    if (warp == 0) put_lse(lse2[0], lse2[1]);
+    // O: every warp puts its own into the stage it holds, and a thread adds up float4s of
+    // them: 8 slices of 16 rows x 32 dims, 16-byte chunks swizzled by the row.
     // BF16: n-tile 8 (sl >> 1) + i holds, in column 2tq + e, dim 64 (sl >> 1) + 32e + 8tq + i:
     //       slice sl takes e = sl & 1.
     // e4m3: n-tile 16c + i, column 2tq + e, dim 128c + 32tq + 16e + i: slice sl takes
     //       c = sl >> 2, e = (sl >> 1) & 1 and i = 8 (sl & 1) .. + 7.
-    auto put = [&](float* base, int sl) {
-      const int e = F8 ? (sl >> 1) & 1 : sl & 1;
-      const int i0 = F8 ? 16 * (sl >> 2) + 8 * (sl & 1) : 8 * (sl >> 1);
-      float* at = base + rank * LY::kCombWarp + gq * kCombRow + 8 * tq;
+    if (held >= 0) {
+      uint8_t* at = smem + held * LY::kStageBytes + gq * (kSlice * 4);
 #pragma unroll
-      for (int hr = 0; hr < 2; ++hr)
-        if (8 * hr < G) {
+      for (int sl = 0; sl < kSlices; ++sl) {
+        const int e = e_of(sl), i0 = i0_of(sl);
 #pragma unroll
-          for (int k = 0; k < 2; ++k)
-            *reinterpret_cast<float4*>(at + 8 * hr * kCombRow + 4 * k) =
-                make_float4(o[i0 + 4 * k][2 * hr + e] * fac[hr], o[i0 + 4 * k + 1][2 * hr + e] * fac[hr],
-                            o[i0 + 4 * k + 2][2 * hr + e] * fac[hr], o[i0 + 4 * k + 3][2 * hr + e] * fac[hr]);
-        }
-    };
-    if (last) {
-      float* const ring_f = reinterpret_cast<float*>(smem);
-      if (rank < nw) {
+        for (int hr = 0; hr < 2; ++hr)
+          if (8 * hr < G) {
 #pragma unroll
-        for (int sl = 0; sl < kSlices; ++sl) put(ring_f + sl * kWarps * LY::kCombWarp, sl);
+            for (int k = 0; k < 2; ++k)
+              *reinterpret_cast<float4*>(at + sl * kSliceBytes + 8 * hr * (kSlice * 4) + (((2 * tq + k) ^ gq) << 4)) =
+                  make_float4(o[i0 + 4 * k][2 * hr + e] * fac[hr], o[i0 + 4 * k + 1][2 * hr + e] * fac[hr],
+                              o[i0 + 4 * k + 2][2 * hr + e] * fac[hr], o[i0 + 4 * k + 3][2 * hr + e] * fac[hr]);
+          }
       }
-      named_bar_sync(kBarConsumers, kConsumerThreads);
-#pragma unroll 1
-      for (int i = tid; i < kSlices * 128; i += kConsumerThreads)
-        add_up(ring_f + (i >> 7) * kWarps * LY::kCombWarp, i >> 7, i & 127);
-      break;
     }
+    named_bar_sync(kBarConsumers, kConsumerThreads);
+    {
+      const uint8_t* from[kWarps];
 #pragma unroll
-    for (int sl = 0; sl < kSlices; ++sl) {
-      if (rank < nw) put(comb, sl);
-      named_bar_sync(kBarConsumers, kConsumerThreads);
-      if (tid < 128) add_up(comb, sl, tid);
-      named_bar_sync(kBarConsumers, kConsumerThreads);
+      for (int v = 0; v < kWarps; ++v) from[v] = smem + max(held_s[v], 0) * LY::kStageBytes;
+#pragma unroll 1
+      for (int i = tid; i < kSlices * 128; i += kConsumerThreads) {
+        const int sl = i >> 7, row = (i >> 3) & 15, chunk = i & 7;
+        if (row >= G) continue;
+        const int off = sl * kSliceBytes + row * (kSlice * 4) + ((chunk ^ (row & 7)) << 4);
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int v = 0; v < kWarps; ++v) {
+          if (v >= nw) break;
+          const float4 y = *reinterpret_cast<const float4*>(from[v] + off);
+          acc.x += y.x;
+          acc.y += y.y;
+          acc.z += y.z;
+          acc.w += y.w;
+        }
+        const int dim = F8 ? 128 * (sl >> 2) + 32 * (chunk >> 1) + 16 * ((sl >> 1) & 1) + 8 * (sl & 1) + 4 * (chunk & 1)
+                           : kSlice * sl + 4 * chunk;
+        const size_t at = (out_row + row) * kHeadDim + dim;
+        if (direct)
+          *reinterpret_cast<uint2*>(a.out + at) = make_uint2(pack_bf16(acc.x, acc.y), pack_bf16(acc.z, acc.w));
+        else
+          *reinterpret_cast<float4*>(a.part_o + at) = acc;
+      }
     }
-    next_piece<LY>(a, w, x1);
+    if (!next_piece<LY>(a, w, x1)) break;
+    // every stage has been read: hand the held ones back to the copies, which come after
+    // these ordinary writes
+    fence_proxy_async();
+    named_bar_sync(kBarConsumers, kConsumerThreads);
+    if (held >= 0 && lane == 0) mbar_arrive(empty + held * 8);
   }
 }
 
@@ -761,16 +809,14 @@ __global__ void __launch_bounds__(Lay<F8>::kThreads, 1) dense_decode_kernel(Dens
   int2* tab = reinterpret_cast<int2*>(smem + LY::kOffTab);
   if (tid == 0) {
     const uint32_t bars = smem_u32(smem + LY::kOffBar);
-    for (int i = 0; i < 2 * LY::kStages + 2; ++i) mbar_init(bars + i * 8, 1);
-    for (int i = 0; i < 2; ++i) mbar_init(bars + (2 * LY::kStages + 2 + i) * 8, LY::kWarps);
+    for (int i = 0; i < 2 * LY::kStages + kMaxQ; ++i) mbar_init(bars + i * 8, 1);
+    for (int i = 0; i < kMaxQ; ++i) mbar_init(bars + (2 * LY::kStages + kMaxQ + i) * 8, LY::kWarps);
     fence_mbar_init();
     *reinterpret_cast<volatile int*>(smem + LY::kOffAbort) = 0;
   }
-  // Q rows beyond the group stay zero
-  for (int i = tid; i < 2 * (16 - a.G) * 32; i += kThreads) {
-    const int row = a.G + (i >> 5) % (16 - a.G), b = (i >> 5) / (16 - a.G);
-    sts128(smem_u32(smem + LY::kOffQ) + b * kQBytes + row * kQStride + (i & 31) * 16, make_uint4(0, 0, 0, 0));
-  }
+  // the zero row (a group of 16 needs none, and fills all 32)
+  if (a.G < 16 && warp == 1)
+    sts128(smem_u32(smem + LY::kOffQ) + (kQRows - 1) * kQStride + lane * 16, make_uint4(0, 0, 0, 0));
   pdl_wait_previous();
   // ---- the share of this CTA.  A thread per query, kThreads of them a round; with
   // one round (the usual batch) the lengths are loaded once and kept.
@@ -1146,6 +1192,7 @@ extern "C" int qsa_dense_decode(const qsa_cache_t* cache, const void* q, int32_t
   a.bsum = mass ? reinterpret_cast<float*>(ws + m.bsum) : nullptr;
   a.bmax = mass ? reinterpret_cast<float*>(ws + m.bmax) : nullptr;
   a.ctas = sms < kMaxCtas ? sms : kMaxCtas;
+  a.q_bufs = a.G == 16 ? 2 : (kQRows - 1) / a.G < kMaxQ ? (kQRows - 1) / a.G : kMaxQ;
   a.st = dev_status;
   JoinArgs j;
   j.d = a;

@@ -189,11 +189,12 @@ def test_shares_cover_every_tile_once_and_partials_have_slots_of_their_own(seed)
     rng = random.Random(seed)
     hkv = rng.choice([1, 2, 4])
     lens = [rng.choice([0, 1, 16, 17, rng.randint(0, 50), rng.randint(0, 9000)]) for _ in range(rng.randint(1, 90))]
-    pairs, T = [], 0                                   # (first place, tiles)
+    pairs, T = [], 0                                   # (first place, tiles, places before them)
     for n in lens:
         for _ in range(hkv if n else 0):
-            pairs.append((T, -(-n // 16)))
-            T += PIECE_COST + -(-n // 16)
+            nt = -(-n // 16)
+            pairs.append((T, nt, PIECE_COST if nt > 1 else 1))
+            T += pairs[-1][2] + nt
     if T == 0:
         return
     ctas = rng.choice([1, 3, 148, 256])
@@ -205,27 +206,26 @@ def test_shares_cover_every_tile_once_and_partials_have_slots_of_their_own(seed)
     done, slots = {}, {}
     for c in range(n):                                 # the walk of CTA c
         x0, x1 = start[c], start[c + 1]
-        k = next(i for i, (b, nt) in enumerate(pairs) if b <= x0 < b + PIECE_COST + nt)
-        b, nt = pairs[k]
-        t0, t1 = max(0, x0 - b - PIECE_COST), min(nt, x1 - b - PIECE_COST)
+        k = next(i for i, (b, nt, cost) in enumerate(pairs) if b <= x0 < b + cost + nt)
+        b, nt, cost = pairs[k]
+        t0, t1 = max(0, x0 - b - cost), min(nt, x1 - b - cost)
         while t1 > 0:
             for t in range(t0, t1):
                 assert (k, t) not in done
                 done[k, t] = c
             if t0 == 0:                                # this CTA names the pair's CTAs
-                last = c if t1 == nt else share_of(base, rem, b + PIECE_COST + nt - 1)
+                last = c if t1 == nt else share_of(base, rem, b + cost + nt - 1)
                 slots.setdefault(k, {})["span"] = (c, last)
             if not (t0 == 0 and t1 == nt):
                 s = 2 * c + (1 if t0 == 0 else 0)
                 assert all(s not in v.get("slots", {}) for v in slots.values())
                 slots.setdefault(k, {}).setdefault("slots", {})[s] = c
-            if not b + PIECE_COST + nt + PIECE_COST < x1:
+            if b + cost + nt >= x1:
                 break
             k += 1
-            b, nt = pairs[k]
-            t0, t1 = 0, min(nt, x1 - b - PIECE_COST)
-            assert t1 > 0
-    assert len(done) == sum(nt for _, nt in pairs)
+            b, nt, cost = pairs[k]
+            t0, t1 = 0, min(nt, x1 - b - cost)
+    assert len(done) == sum(nt for _, nt, _ in pairs)
     for k, v in slots.items():                         # the join looks for each piece where it was put
         first, last = v["span"]
         if first != last:
