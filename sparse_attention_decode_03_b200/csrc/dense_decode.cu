@@ -396,15 +396,24 @@ __device__ void consumers(const DenseArgs& a, uint8_t* smem, Walk w, const Share
     const uint32_t q_row1 = gq + 8 < G ? qb + (gq + 8) * kQStride : q_at + (kQRows - 1) * kQStride;
     if (!*abort_flag) wait_bar(a, q_full + qi * 8, lap & 1u, abort_flag);
     __syncwarp();
+    const int rank = (int)((warp + kWarps - T_base % kWarps) % kWarps);  // this warp's first tile of the piece
+    const bool lone = n_tiles == 1;  // one warp has the piece; the others only let its Q rows go
+    if (lone && rank != 0) {
+      if (lane == 0) mbar_arrive(q_empty + qi * 8);
+      if (++qi == (uint32_t)a.q_bufs) {
+        qi = 0;
+        ++lap;
+      }
+      ++T_base;
+      if (!next_piece<LY>(a, w, x1)) break;
+      continue;
+    }
     float sc0 = a.scale_log2, sc1 = a.scale_log2;
     if constexpr (F8) {
       float* row_scale = scales + qi * 16;
       // FP16 operands: each row is scaled by a power of two into FP16's range (exact down
       // to 2^-38 of its largest element) and its logit scale takes the factor back
-#pragma unroll
-      for (int it = 0; it < 3; ++it) {
-        const int row = warp + kWarps * it;
-        if (row >= G) break;
+      for (int row = lone ? 0 : warp; row < G; row += lone ? 1 : kWarps) {
         const uint4 v = lds128(qb + row * kQStride + lane * 16);
         uint32_t x[4] = {v.x, v.y, v.z, v.w};
         uint32_t mx = 0;  // largest magnitude, as ordered bits
@@ -423,7 +432,10 @@ __device__ void consumers(const DenseArgs& a, uint8_t* smem, Walk w, const Share
         if (lane == 0) row_scale[row] = a.scale_log2 * __uint_as_float((uint32_t)(127 - up) << 23);
       }
       fence_proxy_async();  // these writes come before the copy of the piece after next
-      named_bar_sync(kBarConsumers, kConsumerThreads);
+      if (lone)
+        __syncwarp();
+      else
+        named_bar_sync(kBarConsumers, kConsumerThreads);
       if (gq < G) sc0 = row_scale[gq];
       if (gq + 8 < G) sc1 = row_scale[gq + 8];
     }
@@ -433,7 +445,6 @@ __device__ void consumers(const DenseArgs& a, uint8_t* smem, Walk w, const Share
 #pragma unroll
     for (int nt = 0; nt < 32; ++nt) o[nt][0] = o[nt][1] = o[nt][2] = o[nt][3] = 0.f;
 
-    const int rank = (int)((warp + kWarps - T_base % kWarps) % kWarps);  // this warp's first tile of the piece
     int held = -1;
     for (int ti = rank; ti < n_tiles; ti += kWarps) {
       const uint32_t T = T_base + ti;
@@ -683,31 +694,28 @@ __device__ void consumers(const DenseArgs& a, uint8_t* smem, Walk w, const Share
     // the columns and n-tiles of dim slice sl (see the join below)
     auto e_of = [](int sl) { return F8 ? (sl >> 1) & 1 : sl & 1; };
     auto i0_of = [](int sl) { return F8 ? 16 * (sl >> 2) + 8 * (sl & 1) : 8 * (sl >> 1); };
-    if (n_tiles == 1) {
-      // one warp had the piece: nothing to join, the others go on to the next one
+    if (lone) {  // nothing to join
       if (held >= 0 && lane == 0) mbar_arrive(empty + held * 8);
-      if (rank == 0) {
-        const float f0 = l0 > 0.f ? 1.f / l0 : l0, f1 = l1 > 0.f ? 1.f / l1 : l1;  // 0: no token; NaN stays NaN
-        put_lse(m0 + log2f(l0), m1 + log2f(l1));
+      const float f0 = l0 > 0.f ? 1.f / l0 : l0, f1 = l1 > 0.f ? 1.f / l1 : l1;  // 0: no token; NaN stays NaN
+      put_lse(m0 + log2f(l0), m1 + log2f(l1));
 #pragma unroll
-        for (int sl = 0; sl < kSlices; ++sl) {
-          const int e = e_of(sl), i0 = i0_of(sl);
-          const int dim = F8 ? 128 * (sl >> 2) + 32 * tq + 16 * e + 8 * (sl & 1) : kSlice * sl + 8 * tq;
+      for (int sl = 0; sl < kSlices; ++sl) {
+        const int e = e_of(sl), i0 = i0_of(sl);
+        const int dim = F8 ? 128 * (sl >> 2) + 32 * tq + 16 * e + 8 * (sl & 1) : kSlice * sl + 8 * tq;
 #pragma unroll
-          for (int hr = 0; hr < 2; ++hr) {
-            if (gq + 8 * hr >= G) continue;
-            const float f = hr ? f1 : f0;
-            float y[8];
+        for (int hr = 0; hr < 2; ++hr) {
+          if (gq + 8 * hr >= G) continue;
+          const float f = hr ? f1 : f0;
+          float y[8];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) y[k] = o[i0 + k][2 * hr + e] * f;
-            const size_t at = (out_row + gq + 8 * hr) * kHeadDim + dim;
-            if (direct) {
-              *reinterpret_cast<uint4*>(a.out + at) = make_uint4(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]),
-                                                                 pack_bf16(y[4], y[5]), pack_bf16(y[6], y[7]));
-            } else {
-              *reinterpret_cast<float4*>(a.part_o + at) = make_float4(y[0], y[1], y[2], y[3]);
-              *reinterpret_cast<float4*>(a.part_o + at + 4) = make_float4(y[4], y[5], y[6], y[7]);
-            }
+          for (int k = 0; k < 8; ++k) y[k] = o[i0 + k][2 * hr + e] * f;
+          const size_t at = (out_row + gq + 8 * hr) * kHeadDim + dim;
+          if (direct) {
+            *reinterpret_cast<uint4*>(a.out + at) = make_uint4(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]),
+                                                               pack_bf16(y[4], y[5]), pack_bf16(y[6], y[7]));
+          } else {
+            *reinterpret_cast<float4*>(a.part_o + at) = make_float4(y[0], y[1], y[2], y[3]);
+            *reinterpret_cast<float4*>(a.part_o + at + 4) = make_float4(y[4], y[5], y[6], y[7]);
           }
         }
       }
@@ -765,10 +773,9 @@ __device__ void consumers(const DenseArgs& a, uint8_t* smem, Walk w, const Share
       const uint8_t* from[kWarps];
 #pragma unroll
       for (int v = 0; v < kWarps; ++v) from[v] = smem + max(held_s[v], 0) * LY::kStageBytes;
-#pragma unroll 1
-      for (int i = tid; i < kSlices * 128; i += kConsumerThreads) {
-        const int sl = i >> 7, row = (i >> 3) & 15, chunk = i & 7;
-        if (row >= G) continue;
+#pragma unroll 2
+      for (int i = tid; i < G * 64; i += kConsumerThreads) {
+        const int row = i >> 6, sl = (i >> 3) & 7, chunk = i & 7;
         const int off = sl * kSliceBytes + row * (kSlice * 4) + ((chunk ^ (row & 7)) << 4);
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
