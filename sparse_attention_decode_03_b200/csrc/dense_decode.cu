@@ -29,6 +29,7 @@
 // computes S = Q K^T, a running maximum and sum, and O += P V over all 256 dims,
 // with no exchange between warps until the pair's piece ends.
 #include "qsa_common.cuh"
+#include "tensor_map.cuh"
 
 namespace {
 
@@ -53,22 +54,26 @@ constexpr int kBarConsumers = 1;
 // and in the BF16 / FP16 weights, whose precision is relative.
 constexpr float kLag = 8.f;
 
-// BF16: runs lie in shared memory as in the cache (128-byte swizzled rows).
-// e4m3: rows are plain, so runs are placed 32 B apart to spread the banks.
+// BF16: runs lie in shared memory as in the cache (128-byte swizzled rows), a
+// plain bulk copy each tile.  e4m3: the cache's rows are plain; a tensor-map copy
+// swizzles them on the way, as [row][2 halves of 128 B].
 template <bool F8>
 struct Lay {
-  static constexpr int kWarps = 6;  // consumer warps
+  static constexpr int kWarps = F8 ? 8 : 6;  // consumer warps
   static constexpr int kConsumerThreads = kWarps * 32;
-  static constexpr int kThreads = kConsumerThreads + 32;
+  static constexpr int kThreads = kConsumerThreads + (F8 ? 128 : 32);  // + the copy warp (e4m3: in a warpgroup)
+  // e4m3: 384 threads are launched with 168 registers; the consumers' two warpgroups
+  // take 224, the copy warp's keeps 56: 256 x 224 + 128 x 56 = 384 x 168
+  static constexpr int kRegs = 168, kConsumerRegs = 224, kCopyRegs = 56;
+  static_assert(256 * kConsumerRegs + 128 * kCopyRegs <= 384 * kRegs, "more registers than were launched");
   static constexpr int kRunBytes = 2 * kRatio * kHeadDim * (F8 ? 1 : 2);
-  static constexpr int kRunStride = kRunBytes + (F8 ? 32 : 0);
-  static constexpr int kStrips = F8 ? 2 : 1;  // of a tile
+  static constexpr int kStrips = 1;  // of a tile
   static constexpr int kTile = kStrips * kStrip;
   static constexpr int kTileRuns = kStrips * kStripRuns;
   static constexpr int kTilesPerPage = kPage / kTile;
-  static constexpr int kStageBytes = kTileRuns * kRunStride;
-  static constexpr int kStages = 12;
-  static constexpr int kPieceCost = F8 ? 5 : 8;  // what a pair costs a CTA beside its tiles, in tiles
+  static constexpr int kStageBytes = kTileRuns * kRunBytes;
+  static constexpr int kStages = F8 ? 24 : 12;
+  static constexpr int kPieceCost = 8;  // what a pair costs a CTA beside its tiles, in tiles
   static constexpr int kMinPlaces = 8;            // places a CTA takes at least
   // Tile T and tile T + kStages, which reuses its stage, belong to one warp: it has
   // seen the stage's last phase end before it waits for the next.  A parity wait
@@ -84,9 +89,10 @@ struct Lay {
   static constexpr int kOffBar = kOffTab + kTab * 8;            // full, empty, Q full, Q empty
   static constexpr int kOffAbort = kOffBar + 2 * (kStages + kMaxQ) * 8;
   static constexpr int kSmem = kOffAbort + 16;
-  static constexpr int kIssue = 3;  // copy-warp lanes that wait and issue together, a tile each
+  static constexpr int kIssue = F8 ? 8 : 3;  // copy-warp lanes that wait and issue together, a tile each
   static_assert(kSmem <= 232448, "shared memory budget");
-  static_assert(kSlices * kSliceBytes <= kStageBytes, "a warp's O fits the stage it holds");
+  static constexpr int kRounds = F8 ? 2 : 1;  // the join puts O into a held stage in so many parts
+  static_assert(kSlices * kSliceBytes <= kRounds * kStageBytes, "a part of a warp's O fits the stage it holds");
 };
 
 struct DenseArgs {
@@ -108,6 +114,7 @@ struct DenseArgs {
   int32_t ctas;
   int32_t q_bufs;  // groups of Q rows held at once
   int32_t* st;
+  CUtensorMap tm;  // e4m3: kv_pages as rows of 128 bytes, boxes of one tile
 };
 
 // Tokens query q attends to; 0 for a padding row (q_seq < 0), an empty context
@@ -217,6 +224,16 @@ __device__ __forceinline__ bool wait_bar(const DenseArgs& a, uint32_t bar, uint3
 
 // ------------------------------------------------------------------ copy warp
 
+// 2-D tensor-map copy into this CTA's shared memory, completing on an mbarrier.
+__device__ __forceinline__ void tma2d(uint32_t sdst, const CUtensorMap* map, int x, int y, uint32_t bar,
+                                      uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, "
+      "{%2, %3}], [%4], %5;" ::"r"(sdst),
+      "l"(map), "r"(x), "r"(y), "r"(bar), "l"(policy)
+      : "memory");
+}
+
 template <bool F8>
 __device__ void copy_warp(const DenseArgs& a, uint8_t* smem, Walk w, int x1) {
   using LY = Lay<F8>;
@@ -287,12 +304,13 @@ __device__ void copy_warp(const DenseArgs& a, uint8_t* smem, Walk w, int x1) {
           if (bad) {
             mbar_arrive(bar);
           } else {
-            mbar_arrive_expect_tx(bar, runs * LY::kRunBytes);
-            if constexpr (F8) {
-#pragma unroll
-              for (int r = 0; r < LY::kTileRuns; ++r)
-                if (r < runs) bulk_g2s(dst + r * LY::kRunStride, src + r * LY::kRunBytes, LY::kRunBytes, bar, policy);
+            if constexpr (F8) {  // the whole tile: what lies behind the end is the page's own
+              mbar_arrive_expect_tx(bar, LY::kStageBytes);
+              tma2d(dst, &a.tm, 0,
+                    ((page * a.hkv + w.g) * kBlocksPerPage + t % LY::kTilesPerPage * LY::kTileRuns) * 2 * kRatio * 2, bar,
+                    policy);
             } else {
+              mbar_arrive_expect_tx(bar, runs * LY::kRunBytes);
               bulk_g2s(dst, src, runs * LY::kRunBytes, bar, policy);
             }
           }
@@ -335,20 +353,15 @@ __device__ __forceinline__ float exp2_fast(float x) {
   return y;
 }
 
-// Which token of the tile a lane's logits and V rows belong to.  Columns n = 2tq + e
-// of S's n-tile j (lane tq of each quad holds e = 0, 1):
-//   BF16: micro-block 2j + e, row tq ^ e.  K's column n then reads row (n >> 1) ^ (n & 1):
-//         neighbouring columns read rows of different parity, whose swizzled chunks
-//         fall into different banks; V's four quad lanes read four different rows.
-//   e4m3: micro-block (tq + 2e) & 3, row 2j + e: the quad's lanes read four different
-//         runs, 32 B apart in bank space.
+// Which token of the tile a lane's logits and V rows belong to: columns n = 2tq + e of
+// S's n-tile j (lane tq of each quad holds e = 0, 1) are micro-block 2j + e, row tq ^ e
+// (BF16) or tq ^ 2e (e4m3).  K's columns n, n + 1 are then read from rows whose swizzles
+// send the same chunks to different halves of the banks, and V's four quad lanes from
+// four different rows: both fragments come in conflict-free 16-byte reads.
+__device__ __forceinline__ int tile_run(int j, int e) { return 2 * j + e; }
 template <bool F8>
-__device__ __forceinline__ int tile_run(int j, int tq, int e) {
-  return F8 ? ((tq + 2 * e) & 3) : 2 * j + e;
-}
-template <bool F8>
-__device__ __forceinline__ int tile_row(int j, int tq, int e) {
-  return F8 ? 2 * j + e : (tq ^ e);
+__device__ __forceinline__ int tile_row(int tq, int e) {
+  return F8 ? tq ^ (2 * e) : tq ^ e;
 }
 
 template <bool F8>
@@ -369,22 +382,21 @@ __device__ void consumers(const DenseArgs& a, uint8_t* smem, Walk w, const Share
   const int64_t max_strips = (int64_t)a.mpps * kStripsPerPage;
 
   // K: column n = gq of n-tile j, V: this lane's tokens (j, e)
-  const int ke = gq & 1, kt = gq >> 1;
+  const int ke = gq & 1, kr = tile_row<F8>(gq >> 1, ke);
   uint32_t k_off[2], v_off[2][2];
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
-    const int kr = tile_row<F8>(j, kt, ke);
-    k_off[j] = tile_run<F8>(j, kt, ke) * LY::kRunStride + kr * (F8 ? 256 : 128);
+    k_off[j] = tile_run(j, ke) * LY::kRunBytes + kr * (F8 ? 256 : 128);
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      const int r = tile_row<F8>(j, tq, e);
-      // BF16: V row 4 + r of the run, chunk (gq >> 1) + 4 (gq & 1) of each 64-dim atom; e4m3: 16-dim chunk gq
-      v_off[j][e] = tile_run<F8>(j, tq, e) * LY::kRunStride +
-                    (F8 ? 1024 + r * 256 + gq * 16
+      const int r = tile_row<F8>(tq, e);
+      // BF16: V row 4 + r of the run, chunk (gq >> 1) + 4 (gq & 1) of each 64-dim atom;
+      // e4m3: 128-byte rows 8 + 2r + half of the run, 16-dim chunk gq
+      v_off[j][e] = tile_run(j, e) * LY::kRunBytes +
+                    (F8 ? 1024 + r * 256 + ((gq ^ (2 * r)) << 4)
                         : (4 + r) * 128 + ((((gq >> 1) + 4 * (gq & 1)) ^ (4 + r)) << 4));
     }
   }
-  const int kr0 = tile_row<F8>(0, kt, ke);  // BF16: the row, for the chunk swizzle
 
   uint32_t T_base = 0;
   uint32_t qi = 0, lap = 0;  // place and round of the piece's Q rows
@@ -455,7 +467,7 @@ __device__ void consumers(const DenseArgs& a, uint8_t* smem, Walk w, const Share
       const int nv = valid[stage];
       const uint32_t kb = ring + stage * LY::kStageBytes;
       constexpr int kS = LY::kStrips;
-      constexpr uint32_t kStripBytes = kStripRuns * LY::kRunStride;
+      constexpr uint32_t kStripBytes = kStripRuns * LY::kRunBytes;
 
       // ---- S = Q K^T, two n-tiles of 8 tokens per strip
       float s[kS][2][4];
@@ -473,7 +485,8 @@ __device__ void consumers(const DenseArgs& a, uint8_t* smem, Walk w, const Share
           for (int b = 0; b < kS; ++b)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-              const uint4 kk = lds128(kb + b * kStripBytes + k_off[j] + (4 * i + tq) * 16);
+              const uint4 kk = lds128(kb + b * kStripBytes + k_off[j] + (i >> 1) * 128 +
+                                        (((4 * (i & 1) + tq) ^ (2 * kr + (i >> 1))) << 4));
               const uint4 k0 = e4m3x8_to_f16x8(make_uint2(kk.x, kk.y)), k1 = e4m3x8_to_f16x8(make_uint2(kk.z, kk.w));
               mma_f16_16816(s[b][j], qa0.x, qc0.x, qa0.y, qc0.y, k0.x, k0.y);
               mma_f16_16816(s[b][j], qa0.z, qc0.z, qa0.w, qc0.w, k0.z, k0.w);
@@ -492,7 +505,7 @@ __device__ void consumers(const DenseArgs& a, uint8_t* smem, Walk w, const Share
           const uint4 qc = lds128(q_row1 + (8 * (i >> 1) + ch) * 16);
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            const uint4 kk = lds128(kb + k_off[j] + (i >> 1) * 1024 + ((ch ^ kr0) << 4));
+            const uint4 kk = lds128(kb + k_off[j] + (i >> 1) * 1024 + ((ch ^ kr) << 4));
             mma_bf16_16816(s[0][j], qa.x, qc.x, qa.y, qc.y, kk.x, kk.y);
             mma_bf16_16816(s2[j], qa.z, qc.z, qa.w, qc.w, kk.z, kk.w);
           }
@@ -506,7 +519,7 @@ __device__ void consumers(const DenseArgs& a, uint8_t* smem, Walk w, const Share
       // product is the largest logit)
       const bool whole = nv == LY::kTile;
       auto seen = [&](int b, int j, int e) {
-        return b * kStrip + tile_run<F8>(j, tq, e) * kRatio + tile_row<F8>(j, tq, e) < nv;
+        return b * kStrip + tile_run(j, e) * kRatio + tile_row<F8>(tq, e) < nv;
       };
       if (!whole) {
 #pragma unroll
@@ -569,19 +582,14 @@ __device__ void consumers(const DenseArgs& a, uint8_t* smem, Walk w, const Share
 
         // ---- weight of each micro-block: sums over its 4 tokens, one per quad lane
         if (a.bsum) {
-          float b0, b1;
-          if constexpr (F8) {  // lane tq has rows 0, 2 of run tq and rows 1, 3 of run tq ^ 2
-            b0 = p[0][0] + p[1][0] + __shfl_xor_sync(0xffffffffu, p[0][1] + p[1][1], 2);
-            b1 = p[0][2] + p[1][2] + __shfl_xor_sync(0xffffffffu, p[0][3] + p[1][3], 2);
-          } else {  // run 2j + e over the quad: halve the runs a lane carries twice
-            const bool hi = tq & 2, odd = tq & 1;
-            const float a0 = (hi ? p[1][0] : p[0][0]) + __shfl_xor_sync(0xffffffffu, hi ? p[0][0] : p[1][0], 2);
-            const float a1 = (hi ? p[1][1] : p[0][1]) + __shfl_xor_sync(0xffffffffu, hi ? p[0][1] : p[1][1], 2);
-            const float c0 = (hi ? p[1][2] : p[0][2]) + __shfl_xor_sync(0xffffffffu, hi ? p[0][2] : p[1][2], 2);
-            const float c1 = (hi ? p[1][3] : p[0][3]) + __shfl_xor_sync(0xffffffffu, hi ? p[0][3] : p[1][3], 2);
-            b0 = (odd ? a1 : a0) + __shfl_xor_sync(0xffffffffu, odd ? a0 : a1, 1);
-            b1 = (odd ? c1 : c0) + __shfl_xor_sync(0xffffffffu, odd ? c0 : c1, 1);
-          }
+          // run 2j + e over the quad: halve the runs a lane carries twice
+          const bool hi = tq & 2, odd = tq & 1;
+          const float a0 = (hi ? p[1][0] : p[0][0]) + __shfl_xor_sync(0xffffffffu, hi ? p[0][0] : p[1][0], 2);
+          const float a1 = (hi ? p[1][1] : p[0][1]) + __shfl_xor_sync(0xffffffffu, hi ? p[0][1] : p[1][1], 2);
+          const float c0 = (hi ? p[1][2] : p[0][2]) + __shfl_xor_sync(0xffffffffu, hi ? p[0][2] : p[1][2], 2);
+          const float c1 = (hi ? p[1][3] : p[0][3]) + __shfl_xor_sync(0xffffffffu, hi ? p[0][3] : p[1][3], 2);
+          const float b0 = (odd ? a1 : a0) + __shfl_xor_sync(0xffffffffu, odd ? a0 : a1, 1);
+          const float b1 = (odd ? c1 : c0) + __shfl_xor_sync(0xffffffffu, odd ? c0 : c1, 1);
           const int64_t base = ((int64_t)w.q * a.hq + (int64_t)w.g * G) * max_strips + (int64_t)(w.t0 + ti) * kS + b;
           if (gq < G) {
             const int64_t at = base + gq * max_strips;
@@ -622,7 +630,7 @@ __device__ void consumers(const DenseArgs& a, uint8_t* smem, Walk w, const Share
           for (int j = 0; j < 2; ++j)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              uint4 v = lds128(kb + b * kStripBytes + v_off[j][e] + c * (F8 ? 128 : 1024));
+              uint4 v = lds128(kb + b * kStripBytes + (F8 ? v_off[j][e] ^ (c * (128 + 16)) : v_off[j][e] + c * 1024));
               if (!whole && !seen(b, j, e)) v = make_uint4(0, 0, 0, 0);  // rows behind the end may hold anything
               x[j][e][0] = v.x;
               x[j][e][1] = v.y;
@@ -752,31 +760,34 @@ __device__ void consumers(const DenseArgs& a, uint8_t* smem, Walk w, const Share
     //       slice sl takes e = sl & 1.
     // e4m3: n-tile 16c + i, column 2tq + e, dim 128c + 32tq + 16e + i: slice sl takes
     //       c = sl >> 2, e = (sl >> 1) & 1 and i = 8 (sl & 1) .. + 7.
-    if (held >= 0) {
-      uint8_t* at = smem + held * LY::kStageBytes + gq * (kSlice * 4);
+    constexpr int kPart = kSlices / LY::kRounds;  // slices of a round
 #pragma unroll
-      for (int sl = 0; sl < kSlices; ++sl) {
-        const int e = e_of(sl), i0 = i0_of(sl);
+    for (int rd = 0; rd < LY::kRounds; ++rd) {
+      if (rd) named_bar_sync(kBarConsumers, kConsumerThreads);  // the last part has been read
+      if (held >= 0) {
+        uint8_t* at = smem + held * LY::kStageBytes + gq * (kSlice * 4);
 #pragma unroll
-        for (int hr = 0; hr < 2; ++hr)
-          if (8 * hr < G) {
+        for (int ls = 0; ls < kPart; ++ls) {
+          const int sl = rd * kPart + ls, e = e_of(sl), i0 = i0_of(sl);
 #pragma unroll
-            for (int k = 0; k < 2; ++k)
-              *reinterpret_cast<float4*>(at + sl * kSliceBytes + 8 * hr * (kSlice * 4) + (((2 * tq + k) ^ gq) << 4)) =
-                  make_float4(o[i0 + 4 * k][2 * hr + e] * fac[hr], o[i0 + 4 * k + 1][2 * hr + e] * fac[hr],
-                              o[i0 + 4 * k + 2][2 * hr + e] * fac[hr], o[i0 + 4 * k + 3][2 * hr + e] * fac[hr]);
-          }
+          for (int hr = 0; hr < 2; ++hr)
+            if (8 * hr < G) {
+#pragma unroll
+              for (int k = 0; k < 2; ++k)
+                *reinterpret_cast<float4*>(at + ls * kSliceBytes + 8 * hr * (kSlice * 4) + (((2 * tq + k) ^ gq) << 4)) =
+                    make_float4(o[i0 + 4 * k][2 * hr + e] * fac[hr], o[i0 + 4 * k + 1][2 * hr + e] * fac[hr],
+                                o[i0 + 4 * k + 2][2 * hr + e] * fac[hr], o[i0 + 4 * k + 3][2 * hr + e] * fac[hr]);
+            }
+        }
       }
-    }
-    named_bar_sync(kBarConsumers, kConsumerThreads);
-    {
+      named_bar_sync(kBarConsumers, kConsumerThreads);
       const uint8_t* from[kWarps];
 #pragma unroll
       for (int v = 0; v < kWarps; ++v) from[v] = smem + max(held_s[v], 0) * LY::kStageBytes;
 #pragma unroll 2
-      for (int i = tid; i < G * 64; i += kConsumerThreads) {
-        const int row = i >> 6, sl = (i >> 3) & 7, chunk = i & 7;
-        const int off = sl * kSliceBytes + row * (kSlice * 4) + ((chunk ^ (row & 7)) << 4);
+      for (int i = tid; i < G * kPart * 8; i += kConsumerThreads) {
+        const int row = i / (kPart * 8), ls = i / 8 % kPart, sl = rd * kPart + ls, chunk = i & 7;
+        const int off = ls * kSliceBytes + row * (kSlice * 4) + ((chunk ^ (row & 7)) << 4);
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int v = 0; v < kWarps; ++v) {
@@ -806,7 +817,7 @@ __device__ void consumers(const DenseArgs& a, uint8_t* smem, Walk w, const Share
 }
 
 template <bool F8>
-__global__ void __launch_bounds__(Lay<F8>::kThreads, 1) dense_decode_kernel(DenseArgs a) {
+__global__ void __launch_bounds__(Lay<F8>::kThreads, 1) dense_decode_kernel(const __grid_constant__ DenseArgs a) {
   using LY = Lay<F8>;
   constexpr int kThreads = LY::kThreads, kWarps = LY::kWarps;
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -891,6 +902,13 @@ __global__ void __launch_bounds__(Lay<F8>::kThreads, 1) dense_decode_kernel(Dens
   w.g = (x0 - w.begin) / places_of<LY>(w.len);
   w.begin += w.g * places_of<LY>(w.len);
   if (!set_span<LY>(w, x0, x1)) return;  // the share ends before the pair's first tile
+  if constexpr (F8) {  // by whole warpgroups, and by every one that is left
+    if (warp < kWarps)
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(LY::kConsumerRegs));
+    else
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(LY::kCopyRegs));
+    if (warp > kWarps) return;
+  }
   if (warp < kWarps)
     consumers<F8>(a, smem, w, sh, x1);
   else
@@ -938,7 +956,7 @@ __device__ __forceinline__ float joined_lse2(const DenseArgs& a, int q, int h) {
 // groups of 64 threads (4 dims each) and summed in a fixed order.  The blocks
 // after them add up weights: 64 strips (256 micro-blocks) of one query's sequence
 // each, the heads spread over the 4 groups.
-__global__ void __launch_bounds__(kJoinThreads) dense_join_kernel(JoinArgs ja) {
+__global__ void __launch_bounds__(kJoinThreads) dense_join_kernel(const __grid_constant__ JoinArgs ja) {
   const DenseArgs& a = ja.d;
   pdl_launch_dependents();
   pdl_wait_previous();
@@ -1201,6 +1219,17 @@ extern "C" int qsa_dense_decode(const qsa_cache_t* cache, const void* q, int32_t
   a.ctas = sms < kMaxCtas ? sms : kMaxCtas;
   a.q_bufs = a.G == 16 ? 2 : (kQRows - 1) / a.G < kMaxQ ? (kQRows - 1) / a.G : kMaxQ;
   a.st = dev_status;
+  if (c.kv_dtype == QSA_KV_FP8_E4M3) {
+    const int64_t rows = (int64_t)c.num_pages * c.num_kv_heads * kBlocksPerPage * (2 * kRatio * kHeadDim / 128);
+    if (rows > 0x7fffffff) return QSA_ERR_UNSUPPORTED;  // tensor-map coordinates are int32
+    const auto enc = qsa_host::tensor_map_encoder();
+    const cuuint64_t dims[2] = {128, (cuuint64_t)rows}, strides[1] = {128};
+    const cuuint32_t box[2] = {128, (cuuint32_t)(Lay<true>::kStageBytes / 128)}, es[2] = {1, 1};
+    if (!enc || enc(&a.tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, c.kv_pages, dims, strides, box, es,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return QSA_ERR_CUDA;
+  }
   JoinArgs j;
   j.d = a;
   j.mass_in = mass_in;

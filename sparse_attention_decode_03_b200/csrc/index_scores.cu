@@ -16,6 +16,7 @@
 #include <cudaTypedefs.h>
 
 #include "index_page.cuh"
+#include "tensor_map.cuh"
 
 namespace {
 
@@ -543,17 +544,8 @@ bool aligned(const void* p, unsigned a) { return (reinterpret_cast<uintptr_t>(p)
 // 256 B apart; boxes of 64 dims (128 B, the swizzle span) by 16 rows (one kc
 // page) or 256 rows (the 32 queries x 8 heads of a CTA).
 bool encode_maps(TiledArgs& t, const void* kc, int32_t num_pages, const void* q_idx, int32_t nq) {
-  static PFN_cuTensorMapEncodeTiled_v12000 enc = nullptr;
-  if (!enc) {
-    void* f = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess || !f) {
-      (void)cudaGetLastError();
-      return false;
-    }
-    enc = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
-  }
+  const auto enc = qsa_host::tensor_map_encoder();
+  if (!enc) return false;
   const cuuint64_t strides[1] = {(cuuint64_t)kIdxDim * 2};
   const cuuint32_t es[2] = {1, 1};
   const cuuint64_t kdims[2] = {(cuuint64_t)kIdxDim, (cuuint64_t)num_pages * kBlocksPerPage};
