@@ -34,6 +34,7 @@ using namespace qsa;
 constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kBins0 = 2048, kBins1 = 2048, kBins2 = 1024;  // 11 + 11 + 10 bits of a key
+constexpr int kFew = 256;  // keys that are ranked by comparing each with all
 constexpr int kOnePerSm = 116 * 1024;
 constexpr int kMaxRoom = 48 * 1024;  // masses the selection keeps in shared memory: 192 KiB, 196,608 tokens
 constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s
@@ -82,7 +83,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictArgs a, 
   const int i = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   __shared__ uint32_t hist[kBins0 + kBins1 + kBins2];
   __shared__ int warp_sum[2][kSelWarps];
-  __shared__ uint32_t s_prefix, s_need;
+  __shared__ uint32_t s_prefix, s_need, s_in_bin, s_few;
   const int hkv = a.c.num_kv_heads;
   if (i == 0 && tid == 0) *a.ticket = 0;
   for (int k = tid; k < hkv * a.pages; k += kSelThreads) a.read_done[(int64_t)i * hkv * a.pages + k] = 0;
@@ -125,6 +126,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictArgs a, 
     }
   };
   for (int k = tid; k < kBins0 + kBins1 + kBins2; k += kSelThreads) hist[k] = 0;
+  if (tid == 0) s_few = 0;
   __syncthreads();
   // ---- the cut: the want-th largest key of [lo, hi), and how many equal to it are kept
   uint32_t T = 0xffffffffu;
@@ -161,12 +163,38 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictArgs a, 
           const bool second = before + first < (uint32_t)rest;
           s_prefix = prefix | ((uint32_t)(top - second) << sh);
           s_need = (uint32_t)rest - before - (second ? first : 0u);
+          s_in_bin = second ? own - first : first;
         }
       }
       __syncthreads();
       prefix = s_prefix;
       rest = (int)s_need;
       h += bins;
+      const int n = (int)s_in_bin;
+      if (pass < 2 && n <= kFew) {  // few keys left: each counts those above it (h is free now)
+        each([&](int b, float x) {
+          const uint32_t key = mass_key(x);
+          if (b >= lo && b < hi && (key & ~0u << sh) == prefix) h[atomicAdd(&s_few, 1u)] = key;
+        });
+        __syncthreads();
+        if (tid < n) {
+          const uint32_t key = h[tid];
+          int above = 0, equal = 0;
+#pragma unroll 4
+          for (int k = 0; k < n; ++k) {
+            above += h[k] > key;
+            equal += h[k] == key;
+          }
+          if (above < rest && above + equal >= rest) {  // the same in every thread with this key
+            s_prefix = key;
+            s_need = (uint32_t)(rest - above);
+          }
+        }
+        __syncthreads();
+        prefix = s_prefix;
+        rest = (int)s_need;
+        break;
+      }
     }
     T = prefix;
     need = rest;
@@ -247,7 +275,6 @@ __device__ __forceinline__ void bulk_s2g(void* dst, uint32_t src, uint32_t bytes
 }
 __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
 __device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
-__device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 __device__ __forceinline__ void fence_proxy_async_all() { asm volatile("fence.proxy.async;" ::: "memory"); }
 
 // A unit of the move, as lane b of a warp sees it: block b of the destination page.
@@ -392,7 +419,7 @@ __global__ void __launch_bounds__(kWorkers * 32) evict_move_kernel(EvictArgs a, 
     }
     t = t_next;
   }
-  bulk_wait_all();
+  bulk_wait_read();  // the buffer outlives the stores' reads; the grid's end completes their writes
 }
 
 struct WorkspaceMap {
