@@ -737,23 +737,22 @@ __device__ void consumers(const DenseArgs& a, uint8_t* smem, Walk w, const Share
     }
     named_bar_sync(kBarConsumers, kConsumerThreads);
     const int nw = min(kWarps, n_tiles);  // warps that had a tile: ranks 0 .. nw - 1
-    float fac[2], lse2[2];
+    float fac[2], M[2], L[2];
 #pragma unroll
     for (int hr = 0; hr < 2; ++hr) {
       float2 e[kWarps];
-      float M = -INFINITY, L = 0.f;
 #pragma unroll
-      for (int v = 0; v < kWarps; ++v) {
-        e[v] = ml[v * 16 + gq + 8 * hr];
-        M = fmaxf(M, e[v].x);
-      }
-      const float sub = M == -INFINITY ? 0.f : M;
+      for (int v = 0; v < kWarps; ++v) e[v] = ml[v * 16 + gq + 8 * hr];
+      M[hr] = -INFINITY;
+      L[hr] = 0.f;
 #pragma unroll
-      for (int v = 0; v < kWarps; ++v) L += e[v].y * exp2_fast(e[v].x - sub);
-      fac[hr] = L > 0.f ? exp2_fast((hr ? m1 : m0) - sub) / L : L;  // L = 0: no token; NaN stays NaN
-      lse2[hr] = M + log2f(L);                                      // -inf when L = 0
+      for (int v = 0; v < kWarps; ++v) M[hr] = fmaxf(M[hr], e[v].x);
+      const float sub = M[hr] == -INFINITY ? 0.f : M[hr];
+#pragma unroll
+      for (int v = 0; v < kWarps; ++v) L[hr] += e[v].y * exp2_fast(e[v].x - sub);
+      // L = 0: no token; a NaN stays one
+      fac[hr] = L[hr] > 0.f ? __fdividef(exp2_fast((hr ? m1 : m0) - sub), L[hr]) : L[hr];
     }
-    if (warp == 0) put_lse(lse2[0], lse2[1]);
     // O: every warp puts its own into the stage it holds, and a thread adds up float4s of
     // them: 8 slices of 16 rows x 32 dims, 16-byte chunks swizzled by the row.
     // BF16: n-tile 8 (sl >> 1) + i holds, in column 2tq + e, dim 64 (sl >> 1) + 32e + 8tq + i:
@@ -781,22 +780,23 @@ __device__ void consumers(const DenseArgs& a, uint8_t* smem, Walk w, const Share
         }
       }
       named_bar_sync(kBarConsumers, kConsumerThreads);
-      const uint8_t* from[kWarps];
+      uint32_t from[kWarps];
 #pragma unroll
-      for (int v = 0; v < kWarps; ++v) from[v] = smem + max(held_s[v], 0) * LY::kStageBytes;
+      for (int v = 0; v < kWarps; ++v) from[v] = ring + max(held_s[v], 0) * LY::kStageBytes;
 #pragma unroll 2
       for (int i = tid; i < G * kPart * 8; i += kConsumerThreads) {
         const int row = i / (kPart * 8), ls = i / 8 % kPart, sl = rd * kPart + ls, chunk = i & 7;
         const int off = ls * kSliceBytes + row * (kSlice * 4) + ((chunk ^ (row & 7)) << 4);
+        uint4 y[kWarps];
+#pragma unroll
+        for (int v = 0; v < kWarps; ++v) y[v] = v < nw ? lds128(from[v] + off) : make_uint4(0, 0, 0, 0);
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int v = 0; v < kWarps; ++v) {
-          if (v >= nw) break;
-          const float4 y = *reinterpret_cast<const float4*>(from[v] + off);
-          acc.x += y.x;
-          acc.y += y.y;
-          acc.z += y.z;
-          acc.w += y.w;
+          acc.x += __uint_as_float(y[v].x);
+          acc.y += __uint_as_float(y[v].y);
+          acc.z += __uint_as_float(y[v].z);
+          acc.w += __uint_as_float(y[v].w);
         }
         const int dim = F8 ? 128 * (sl >> 2) + 32 * (chunk >> 1) + 16 * ((sl >> 1) & 1) + 8 * (sl & 1) + 4 * (chunk & 1)
                            : kSlice * sl + 4 * chunk;
@@ -807,6 +807,7 @@ __device__ void consumers(const DenseArgs& a, uint8_t* smem, Walk w, const Share
           *reinterpret_cast<float4*>(a.part_o + at) = acc;
       }
     }
+    if (warp == kWarps - 1) put_lse(M[0] + log2f(L[0]), M[1] + log2f(L[1]));  // -inf when L = 0
     if (!next_piece<LY>(a, w, x1)) break;
     // every stage has been read: hand the held ones back to the copies, which come after
     // these ordinary writes
