@@ -927,6 +927,7 @@ struct JoinArgs {
   int64_t mass_ld;
   float decay;
   int32_t mass_blocks;  // CTAs per query for the weights
+  int32_t parts;        // CTAs per pair for the join, a share of its heads each
 };
 
 // The partial slot of CTA c's piece of a pair that spans several CTAs.
@@ -953,8 +954,8 @@ __device__ __forceinline__ float joined_lse2(const DenseArgs& a, int q, int h) {
   return M + log2f(L);
 }
 
-// Blocks 0 .. nq*hq-1: one (query, head) each; the pieces are spread over 4
-// groups of 64 threads (4 dims each) and summed in a fixed order.  The blocks
+// The first blocks: `parts` of them a (query, KV head) pair, for every parts-th head
+// each; the pieces of a head are spread over 4 groups of 64 threads (4 dims each) and summed in a fixed order.  The blocks
 // after them add up weights: 64 strips (256 micro-blocks) of one query's sequence
 // each, the heads spread over the 4 groups.
 __global__ void __launch_bounds__(kJoinThreads) dense_join_kernel(const __grid_constant__ JoinArgs ja) {
@@ -966,79 +967,83 @@ __global__ void __launch_bounds__(kJoinThreads) dense_join_kernel(const __grid_c
   __shared__ float lse_s[kMaxCtas];  // pieces' lse, then their weights (kMaxCtas <= kJoinThreads: one each)
   __shared__ float red_s[2][kJoinThreads / 32];
   static_assert(kMaxCtas <= kJoinThreads, "a thread per piece");
-  const int64_t n_join = (int64_t)a.nq * a.hq;
-  if (blockIdx.x < n_join) {
-    const int q = (int)(blockIdx.x / a.hq), h = (int)(blockIdx.x % a.hq), row = h % a.G;
-    const int2 p = a.span[q * a.hkv + h / a.G];
+  const int n_join = a.nq * a.hkv * ja.parts;
+  if ((int)blockIdx.x < n_join) {
+    const int pair = blockIdx.x / ja.parts;
+    const int2 p = a.span[pair];
     if (p.x == p.y) return;  // written by its CTA
-    const int grp = tid >> 6, c4 = tid & 63;
-    uint2 o = make_uint2(0, 0);
-    float lse = -INFINITY;
-    const int n = p.y - p.x + 1;
-    if (n > 1) {
-      // rows: requested before their weights are known
-      const float4* base = reinterpret_cast<const float4*>(a.part_o + (size_t)row * kHeadDim) + c4;
-      const size_t step = (size_t)a.G * (kHeadDim / 4);
-      constexpr int kAhead = 4;
-      float4 x[kAhead];
+    for (int row = blockIdx.x % ja.parts; row < a.G; row += ja.parts) {
+      const int64_t qh = (int64_t)pair * a.G + row;
+      __syncthreads();  // the last head's use of the shared arrays has ended
+      const int grp = tid >> 6, c4 = tid & 63;
+      uint2 o = make_uint2(0, 0);
+      float lse = -INFINITY;
+      const int n = p.y - p.x + 1;
+      if (n > 1) {
+        // rows: requested before their weights are known
+        const float4* base = reinterpret_cast<const float4*>(a.part_o + (size_t)row * kHeadDim) + c4;
+        const size_t step = (size_t)a.G * (kHeadDim / 4);
+        constexpr int kAhead = 4;
+        float4 x[kAhead];
 #pragma unroll
-      for (int k = 0; k < kAhead; ++k)
-        if (grp + 4 * k < n) x[k] = base[slot_of(p, p.x + grp + 4 * k) * step];
-      float v = tid < n ? a.part_lse[(size_t)slot_of(p, p.x + tid) * a.G + row] : -INFINITY;
-      float M = v;
+        for (int k = 0; k < kAhead; ++k)
+          if (grp + 4 * k < n) x[k] = base[slot_of(p, p.x + grp + 4 * k) * step];
+        float v = tid < n ? a.part_lse[(size_t)slot_of(p, p.x + tid) * a.G + row] : -INFINITY;
+        float M = v;
 #pragma unroll
-      for (int d = 16; d; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
-      if (lane == 0) red_s[0][warp] = M;
-      __syncthreads();
+        for (int d = 16; d; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+        if (lane == 0) red_s[0][warp] = M;
+        __syncthreads();
 #pragma unroll
-      for (int k = 0; k < kJoinThreads / 32; ++k) M = fmaxf(M, red_s[0][k]);
-      float e = M == -INFINITY ? 0.f : exp2f(v - M);  // 0 for an empty piece, whose row is zero
-      if (tid < n) lse_s[tid] = e;
+        for (int k = 0; k < kJoinThreads / 32; ++k) M = fmaxf(M, red_s[0][k]);
+        float e = M == -INFINITY ? 0.f : exp2f(v - M);  // 0 for an empty piece, whose row is zero
+        if (tid < n) lse_s[tid] = e;
 #pragma unroll
-      for (int d = 16; d; d >>= 1) e += __shfl_xor_sync(0xffffffffu, e, d);
-      if (lane == 0) red_s[1][warp] = e;
-      __syncthreads();
-      float L = 0.f;
+        for (int d = 16; d; d >>= 1) e += __shfl_xor_sync(0xffffffffu, e, d);
+        if (lane == 0) red_s[1][warp] = e;
+        __syncthreads();
+        float L = 0.f;
 #pragma unroll
-      for (int k = 0; k < kJoinThreads / 32; ++k) L += red_s[1][k];
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int i0 = grp; i0 < n; i0 += 4 * kAhead) {
+        for (int k = 0; k < kJoinThreads / 32; ++k) L += red_s[1][k];
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int i0 = grp; i0 < n; i0 += 4 * kAhead) {
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k) {
-          const int i = i0 + 4 * k;
-          if (i >= n) break;
-          const float f = lse_s[i];
-          acc.x += f * x[k].x;
-          acc.y += f * x[k].y;
-          acc.z += f * x[k].z;
-          acc.w += f * x[k].w;
+          for (int k = 0; k < kAhead; ++k) {
+            const int i = i0 + 4 * k;
+            if (i >= n) break;
+            const float f = lse_s[i];
+            acc.x += f * x[k].x;
+            acc.y += f * x[k].y;
+            acc.z += f * x[k].z;
+            acc.w += f * x[k].w;
+          }
+#pragma unroll
+          for (int k = 0; k < kAhead; ++k) {
+            const int i = i0 + 4 * kAhead + 4 * k;
+            if (i < n) x[k] = base[slot_of(p, p.x + i) * step];
+          }
         }
+        acc_s[grp][c4] = acc;
+        __syncthreads();
+        if (grp == 0 && M != -INFINITY) {
+          const float inv = 1.f / L;
+          float4 r = acc_s[0][c4];
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k) {
-          const int i = i0 + 4 * kAhead + 4 * k;
-          if (i < n) x[k] = base[slot_of(p, p.x + i) * step];
+          for (int k = 1; k < 4; ++k) {
+            r.x += acc_s[k][c4].x;
+            r.y += acc_s[k][c4].y;
+            r.z += acc_s[k][c4].z;
+            r.w += acc_s[k][c4].w;
+          }
+          o.x = pack_bf16(r.x * inv, r.y * inv);
+          o.y = pack_bf16(r.z * inv, r.w * inv);
+          lse = (M + log2f(L)) * 0.69314718055994530942f;
         }
       }
-      acc_s[grp][c4] = acc;
-      __syncthreads();
-      if (grp == 0 && M != -INFINITY) {
-        const float inv = 1.f / L;
-        float4 r = acc_s[0][c4];
-#pragma unroll
-        for (int k = 1; k < 4; ++k) {
-          r.x += acc_s[k][c4].x;
-          r.y += acc_s[k][c4].y;
-          r.z += acc_s[k][c4].z;
-          r.w += acc_s[k][c4].w;
-        }
-        o.x = pack_bf16(r.x * inv, r.y * inv);
-        o.y = pack_bf16(r.z * inv, r.w * inv);
-        lse = (M + log2f(L)) * 0.69314718055994530942f;
+      if (grp == 0) {
+        reinterpret_cast<uint2*>(a.out + (size_t)qh * kHeadDim)[c4] = o;
+        if (c4 == 0) a.lse[qh] = lse;
       }
-    }
-    if (grp == 0) {
-      reinterpret_cast<uint2*>(a.out + (size_t)blockIdx.x * kHeadDim)[c4] = o;
-      if (c4 == 0) a.lse[blockIdx.x] = lse;
     }
     return;
   }
@@ -1239,7 +1244,12 @@ extern "C" int qsa_dense_decode(const qsa_cache_t* cache, const void* q, int32_t
   j.decay = decay;
   const int64_t tiles = (int64_t)c.max_pages_per_seq * kStripsPerPage;
   j.mass_blocks = (int32_t)((tiles + 63) / 64);
-  const int64_t grid = (int64_t)nq * hq + (mass ? (int64_t)nq * j.mass_blocks : 0);
+  // About 8 CTAs per SM, a head each at most.  Of a large batch's pairs many need no join:
+  // a CTA per head, to find that out, took 2.2 us more for 161 queries of 24 heads, and one
+  // CTA for all 12 heads of a split pair 4.5 us more.
+  const int64_t pairs = (int64_t)nq * c.num_kv_heads, want = (8 * a.ctas + pairs - 1) / pairs;
+  j.parts = (int32_t)(want < a.G ? want : a.G);
+  const int64_t grid = pairs * j.parts + (mass ? (int64_t)nq * j.mass_blocks : 0);
   if (grid > 0x7fffffff) return QSA_ERR_UNSUPPORTED;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int r = c.kv_dtype == QSA_KV_FP8_E4M3 ? launch_dense<true>(a, s) : launch_dense<false>(a, s);

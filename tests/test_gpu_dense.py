@@ -354,6 +354,45 @@ def test_dense_decode_graph_streams_and_workspaces():
     assert o.shape[0] == 0
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+def test_dense_decode_more_queries_than_threads(fp8):
+    """Several rounds of the length scan; CTAs whose share spans more queries than they keep lengths of."""
+    rng = random.Random(3)
+    grp = Group([2000, 333, 64, 1], 1, fp8, seed=14)
+    q_seq, q_pos = [], []
+    for r in range(1000):
+        s = rng.choice([0, 1, 2, 3, -1, -1])
+        n = grp.lens[s] if s >= 0 else 10
+        q_seq.append(s)
+        q_pos.append(-1 if r % 97 > 20 else min(n - 1, rng.choice([0, 3, 16, 40, n - 1])))
+    mass0 = torch.rand((4, grp.cache.max_pages_per_seq * 16), generator=gen(1))
+    check_dense(grp, queries(1000, 3, 1), q_seq, q_pos, track=True, decay=0.5, mass0=mass0)
+    check_dense(grp, queries(1000, 3, 1), [0] * 1000, [15] * 1000)      # one tile each
+
+
+def test_dense_decode_e4m3_pages_past_four_gigabytes():
+    pages = 270000                                            # 16 KiB a page
+    grp = Group([700, 90], 1, True, seed=8, num_pages=pages, first_page=pages - 16)
+    assert int(grp.cache.block_table.max()) * 16384 > 1 << 32
+    check_dense(grp, queries(2, 12, 2), [0, 1], [699, 89])
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_dense_decode_agrees_with_the_sparse_step_that_selects_everything(fp8):
+    grp = Group([1999, 500, 3], 2, fp8, seed=15)
+    q, q_seq, q_pos = queries(3, 24, 4).cuda(), i32([0, 1, 2]), i32([1998, 499, 2])
+    sparse = qsa.Decoder(grp.cache, 24, 3, k=512)
+    so, sl = sparse.run(q, torch.ones((3, 8, 128), dtype=torch.bfloat16, device="cuda"),
+                        torch.ones((3, 8), device="cuda"), q_seq, q_pos)
+    do, dl = qsa.DenseDecoder(grp.cache, 24, 3).run(q, q_seq, q_pos)
+    for r in range(3):
+        n = int(q_pos[r]) + 1
+        k, v = grp.rows(r)
+        _, _, _, ob, lb, _ = D.dense(q[r].double().cpu().numpy(), k[:n], v[:n], 1 / 16, fp8)
+        within(do[r].double().cpu().numpy(), so[r].double().cpu().numpy(), 2 * ob, "out")   # each within its bound
+        within(dl[r].double().cpu().numpy(), sl[r].double().cpu().numpy(), 2 * lb, "lse")
+
+
 # ---------------------------------------------------------------- eviction
 
 
@@ -488,11 +527,29 @@ def test_evict_patterns_of_a_long_sequence_in_place(shape):
 
 
 @pytest.mark.parametrize("alias", [False, True])
-def test_evict_rows_too_long_for_registers(alias):
-    """More than 16,384 blocks: masses are read again and pass through the workspace."""
-    grp = Group([64 * 1100 + 3, 500], 1, seed=13)
-    mass = masses(random.Random(5), (2, 1101 * 16))
-    check_evict(grp, 9000, 3, 100, mass, alias=alias)
+def test_evict_rows_too_long_for_shared_memory(alias):
+    """More than 49,152 blocks: masses are read again and pass through the workspace."""
+    grp = Group([198403, 500], 1, True, seed=13)
+    mass = masses(random.Random(5), (2, grp.cache.max_pages_per_seq * 16))
+    check_evict(grp, 30000, 3, 100, mass, alias=alias)
+
+
+@pytest.mark.parametrize("values", ["one", "two", "close", "nan", "inf", "wide"])
+def test_evict_cuts_in_crowded_and_sparse_bins(values):
+    """Rows of one value, of two, of neighbouring floats, of NaN, of infinities, and over all exponents."""
+    g = gen(4)
+    n = 3000
+    m = {"one": torch.full((n,), 0.7), "two": torch.where(torch.rand(n, generator=g) < 0.5, 1.0, 2.0),
+         "close": (torch.randint(0, 700, (n,), generator=g) + 0x3f800000).int().view(torch.float32),
+         "nan": torch.where(torch.rand(n, generator=g) < 0.7, float("nan"), 1.0),
+         "inf": torch.where(torch.rand(n, generator=g) < 0.5, float("inf"), -float("inf")),
+         "wide": torch.exp2(torch.rand(n, generator=g) * 250 - 125)}[values]
+    grp = Group([4 * n], 1, True, seed=16)
+    mass = torch.zeros((1, grp.cache.max_pages_per_seq * 16))
+    mass[0, :n] = m
+    for budget in (1, 700, 1500, 2999):
+        check_evict(grp, budget, 0, 0, mass, lens=[4 * n])
+        grp = Group([4 * n], 1, True, seed=16)
 
 
 @pytest.mark.parametrize("seed", range(4))
