@@ -12,8 +12,8 @@
 // group fills; a tcgen05 tile would have 128 rows, K and V rows interleaved in
 // its operand, and an instruction floor that alone exceeds the copy time.
 //
-// Split.  A tile is 16 tokens (BF16) or 32 (e4m3) of one (query, KV head): 4 or 8
-// micro-blocks, one contiguous 16 KiB of the page.  The tiles of all pairs,
+// Split.  A tile is 16 tokens of one (query, KV head): 4 micro-blocks, one contiguous
+// run of the page (16 KiB BF16, 8 KiB e4m3).  The tiles of all pairs,
 // query-major, form one list that the CTAs (one per SM) share evenly, so ragged
 // lengths leave no SM idle; the lengths are read on the device (no host copy of
 // q_pos).  A pair inside one CTA is written to out / lse at once; of the others
@@ -21,13 +21,26 @@
 // 2 CTAs x 16 rows of workspace whatever the batch, and a second small kernel
 // joins them and adds up the weights.
 //
-// CTA = 6 consumer warps + 1 copy warp: with 8 warps or fewer a thread may hold
-// 255 registers, and the 16 x 256 accumulator takes 128.  The copy warp resolves
-// 32 tiles' pages at once, one batch ahead, and a lane each moves a tile (16
-// tokens BF16, 32 e4m3: 16 KiB) with bulk copies into a ring of 12; it also
-// brings the Q rows of the next pair.  Tile T goes to consumer warp T % 6, which
-// computes S = Q K^T, a running maximum and sum, and O += P V over all 256 dims,
-// with no exchange between warps until the pair's piece ends.
+// CTA = consumer warps + 1 copy warp, one CTA per SM.  A consumer warp takes whole
+// tiles (S = Q K^T, a running maximum and sum, O += P V over all 256 dims) with no
+// exchange until the pair's piece ends; its 16 x 256 accumulator takes 128
+// registers.  BF16: 6 consumers, 255 registers each (8 warps or fewer), and 12
+// tiles in flight.  e4m3: half the bytes a token, so the arithmetic counts: 8
+// consumers with 224 registers, which the copy warp's group gives up, and 24
+// tiles.  The copy warp resolves 32 tiles' pages at once, one batch ahead, a lane
+// each moves a tile, and it brings the Q rows of the next pairs.
+//
+// Measured on one B200 (time of the call, share of the 6.54 TB/s copy rate):
+//   BF16, 32 x 131,072 tokens, 24/2 heads     1,181 us   111%
+//   BF16, 8 x 32,768 tokens, 16/2 heads          85 us    97%
+//   e4m3, 64 x 16K-262K tokens, 12/1 heads      455 us    92%; power-capped at 1.7 GHz,
+//                                                         ALU 39%, tensor 34% of cycles
+//   BF16, 16 x 9K-16K tokens, 24/2, with totals   75 us    82%
+//   BF16, 1 x 4,096 tokens, 16/2                 12 us    of it 8 main kernel, 3 join
+//   BF16, 200 x 1-700 tokens, 3/1                15 us
+// What did not pay for e4m3: 6 or 7 consumers (512, 526 us then), 32-token tiles
+// (no change), one tile's products beside the last one's values (508 against 494),
+// e4m3 matrix instructions (25 to 38 cycles against 8 for FP16 ones of half the depth).
 #include "qsa_common.cuh"
 #include "tensor_map.cuh"
 
@@ -35,9 +48,11 @@ namespace {
 
 using namespace qsa;
 
-constexpr int kStrip = 16;                       // tokens of one matrix product: 4 micro-blocks
-constexpr int kStripRuns = kStrip / kRatio;
-constexpr int kStripsPerPage = kPage / kStrip;
+constexpr int kTile = 16;                        // tokens of one matrix product
+constexpr int kTileRuns = kTile / kRatio;        // 4 micro-blocks
+constexpr int kTilesPerPage = kPage / kTile;
+constexpr int kPieceCost = 8;                    // what a pair costs a CTA beside its tiles, in tiles
+constexpr int kMinPlaces = 8;                    // places a CTA takes at least
 constexpr int kMaxCtas = 256;                    // partial slots reserved: 2 per CTA
 constexpr int kQStride = kHeadDim * 2 + 16;      // Q rows 528 B apart: conflict-free 16-byte fragment reads
 constexpr int kSlice = 32;                       // dims of O that the warps join at once
@@ -67,14 +82,8 @@ struct Lay {
   static constexpr int kRegs = 168, kConsumerRegs = 224, kCopyRegs = 56;
   static_assert(256 * kConsumerRegs + 128 * kCopyRegs <= 384 * kRegs, "more registers than were launched");
   static constexpr int kRunBytes = 2 * kRatio * kHeadDim * (F8 ? 1 : 2);
-  static constexpr int kStrips = 1;  // of a tile
-  static constexpr int kTile = kStrips * kStrip;
-  static constexpr int kTileRuns = kStrips * kStripRuns;
-  static constexpr int kTilesPerPage = kPage / kTile;
   static constexpr int kStageBytes = kTileRuns * kRunBytes;
   static constexpr int kStages = F8 ? 24 : 12;
-  static constexpr int kPieceCost = 8;  // what a pair costs a CTA beside its tiles, in tiles
-  static constexpr int kMinPlaces = 8;            // places a CTA takes at least
   // Tile T and tile T + kStages, which reuses its stage, belong to one warp: it has
   // seen the stage's last phase end before it waits for the next.  A parity wait
   // cannot tell a phase from the one two before, so another warp could run ahead.
@@ -133,9 +142,8 @@ __device__ __forceinline__ int query_len(const DenseArgs& a, int q, bool report)
   return p + 1;
 }
 
-template <class LY>
 __device__ __forceinline__ int tiles_of(int len) {
-  return (len + LY::kTile - 1) / LY::kTile;
+  return (len + kTile - 1) / kTile;
 }
 
 // The list that the CTAs share out: every pair takes kPieceCost places (what
@@ -143,10 +151,9 @@ __device__ __forceinline__ int tiles_of(int len) {
 struct Shares {
   int n, base, rem;  // CTAs; the first `rem` take base + 1 places, the others base
 };
-template <class LY>
 __device__ __forceinline__ Shares make_shares(int total, int ctas) {
   Shares s;
-  s.n = min(ctas, max(1, (total + LY::kMinPlaces - 1) / LY::kMinPlaces));
+  s.n = min(ctas, max(1, (total + kMinPlaces - 1) / kMinPlaces));
   s.base = total / s.n;
   s.rem = total - s.base * s.n;
   return s;
@@ -157,13 +164,11 @@ __device__ __forceinline__ int share_of(const Shares& s, int x) {  // the CTA th
   return x < cut ? x / (s.base + 1) : s.rem + (x - cut) / s.base;
 }
 
-template <class LY>
 __device__ __forceinline__ int cost_of(int tiles) {  // a pair of one tile joins nothing
-  return tiles > 1 ? LY::kPieceCost : 1;
+  return tiles > 1 ? kPieceCost : 1;
 }
-template <class LY>
 __device__ __forceinline__ int places_of(int len) {
-  return len ? tiles_of<LY>(len) + cost_of<LY>(tiles_of<LY>(len)) : 0;
+  return len ? tiles_of(len) + cost_of(tiles_of(len)) : 0;
 }
 
 // A CTA's position in the list: a piece of pair (q, g).
@@ -176,18 +181,16 @@ struct Walk {
   const int2* tab;
 };
 
-template <class LY>
 __device__ __forceinline__ bool set_span(Walk& w, int x0, int x1) {
-  const int nt = tiles_of<LY>(w.len), lo = w.begin + cost_of<LY>(nt);
+  const int nt = tiles_of(w.len), lo = w.begin + cost_of(nt);
   w.t0 = max(0, x0 - lo);
   w.t1 = min(nt, x1 - lo);
   return w.t1 > 0;
 }
 
 // Step to the next pair with tiles in the share; false when there is none.
-template <class LY>
 __device__ __forceinline__ bool next_piece(const DenseArgs& a, Walk& w, int x1) {
-  const int begin = w.begin + places_of<LY>(w.len);
+  const int begin = w.begin + places_of(w.len);
   if (begin >= x1) return false;
   w.begin = begin;
   if (w.g + 1 < a.hkv) {
@@ -202,7 +205,7 @@ __device__ __forceinline__ bool next_piece(const DenseArgs& a, Walk& w, int x1) 
     } while (w.len == 0);
     w.g = 0;
   }
-  return set_span<LY>(w, 0, x1);
+  return set_span(w, 0, x1);
 }
 
 // Bounded wait; false (and the abort flag) when the limit passed.
@@ -248,7 +251,7 @@ __device__ void copy_warp(const DenseArgs& a, uint8_t* smem, Walk w, int x1) {
   const uint32_t q_full = empty + LY::kStages * 8, q_empty = q_full + kMaxQ * 8;
   auto lookup = [&](const Walk& at, int t) {
     int page = -1;
-    if (t < at.t1) page = __ldg(a.bt + (int64_t)at.seq * a.mpps + t / LY::kTilesPerPage);
+    if (t < at.t1) page = __ldg(a.bt + (int64_t)at.seq * a.mpps + t / kTilesPerPage);
     return page;
   };
   int page = lookup(w, w.t0 + lane);
@@ -275,17 +278,17 @@ __device__ void copy_warp(const DenseArgs& a, uint8_t* smem, Walk w, int x1) {
     // lane = tile: pages of 32 tiles at a time, the next batch's (of this pair or the
     // next one) requested before this batch's copies
     Walk after = w;
-    more = next_piece<LY>(a, after, x1);
+    more = next_piece(a, after, x1);
     const int page_after = more ? lookup(after, after.t0 + lane) : -1;
     for (int tb = w.t0; tb < w.t1 && !stop; tb += 32) {
       const int page_next = lookup(w, tb + 32 + lane);
       const int n = min(32, w.t1 - tb), t = tb + lane;
       const bool bad = page < 0 || page >= a.num_pages;
       if (lane < n && bad) flag(a.st, QSA_DEV_BAD_PAGE);
-      const int tok = min(LY::kTile, w.len - t * LY::kTile);
+      const int tok = min(kTile, w.len - t * kTile);
       const int runs = (tok + kRatio - 1) / kRatio;  // whole micro-blocks that hold a token
       const uint8_t* src = a.kv + (((size_t)page * a.hkv + w.g) * kBlocksPerPage +
-                                   (size_t)(t % LY::kTilesPerPage) * LY::kTileRuns) * LY::kRunBytes;
+                                   (size_t)(t % kTilesPerPage) * kTileRuns) * LY::kRunBytes;
       const uint32_t mine = T + lane;
       const int stage = (int)(mine % LY::kStages);
       const uint32_t bar = full + stage * 8, dst = ring + stage * LY::kStageBytes;
@@ -307,7 +310,7 @@ __device__ void copy_warp(const DenseArgs& a, uint8_t* smem, Walk w, int x1) {
             if constexpr (F8) {  // the whole tile: what lies behind the end is the page's own
               mbar_arrive_expect_tx(bar, LY::kStageBytes);
               tma2d(dst, &a.tm, 0,
-                    ((page * a.hkv + w.g) * kBlocksPerPage + t % LY::kTilesPerPage * LY::kTileRuns) * 2 * kRatio * 2, bar,
+                    ((page * a.hkv + w.g) * kBlocksPerPage + t % kTilesPerPage * kTileRuns) * 2 * kRatio * 2, bar,
                     policy);
             } else {
               mbar_arrive_expect_tx(bar, runs * LY::kRunBytes);
@@ -379,7 +382,7 @@ __device__ void consumers(const DenseArgs& a, uint8_t* smem, Walk w, const Share
   float* scales = reinterpret_cast<float*>(smem + LY::kOffScale);
   constexpr int kWarps = LY::kWarps, kConsumerThreads = LY::kConsumerThreads;
   const int G = a.G;
-  const int64_t max_strips = (int64_t)a.mpps * kStripsPerPage;
+  const int64_t max_tiles = (int64_t)a.mpps * kTilesPerPage;
 
   // K: column n = gq of n-tile j, V: this lane's tokens (j, e)
   const int ke = gq & 1, kr = tile_row<F8>(gq >> 1, ke);
@@ -417,7 +420,7 @@ __device__ void consumers(const DenseArgs& a, uint8_t* smem, Walk w, const Share
         ++lap;
       }
       ++T_base;
-      if (!next_piece<LY>(a, w, x1)) break;
+      if (!next_piece(a, w, x1)) break;
       continue;
     }
     float sc0 = a.scale_log2, sc1 = a.scale_log2;
@@ -458,23 +461,18 @@ __device__ void consumers(const DenseArgs& a, uint8_t* smem, Walk w, const Share
     for (int nt = 0; nt < 32; ++nt) o[nt][0] = o[nt][1] = o[nt][2] = o[nt][3] = 0.f;
 
     int held = -1;
-    for (int ti = rank; ti < n_tiles; ti += kWarps) {
+    // the tile of this warp's step ti has landed: its stage; -1 when the wait was given up
+    auto landed = [&](int ti) {
       const uint32_t T = T_base + ti;
       const int stage = (int)(T % LY::kStages);
       const bool got = !*abort_flag && wait_bar(a, full + stage * 8, (T / LY::kStages) & 1u, abort_flag);
       __syncwarp();
-      if (!__all_sync(0xffffffffu, got)) break;
-      const int nv = valid[stage];
-      const uint32_t kb = ring + stage * LY::kStageBytes;
-      constexpr int kS = LY::kStrips;
-      constexpr uint32_t kStripBytes = kStripRuns * LY::kRunBytes;
-
-      // ---- S = Q K^T, two n-tiles of 8 tokens per strip
-      float s[kS][2][4];
+      return __all_sync(0xffffffffu, got) ? stage : -1;
+    };
+    // ---- S = Q K^T of the tile at kb: two n-tiles of 8 tokens
+    auto products = [&](uint32_t kb, float(&s)[2][4]) {
 #pragma unroll
-      for (int b = 0; b < kS; ++b)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) s[b][j][0] = s[b][j][1] = s[b][j][2] = s[b][j][3] = 0.f;
+      for (int j = 0; j < 2; ++j) s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.f;
       if constexpr (F8) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {  // 64 dims: lane tq holds dims 64i + 16tq .. + 15
@@ -482,17 +480,15 @@ __device__ void consumers(const DenseArgs& a, uint8_t* smem, Walk w, const Share
           const uint4 qa0 = lds128(q_row0 + qo), qa1 = lds128(q_row0 + qo + 16);
           const uint4 qc0 = lds128(q_row1 + qo), qc1 = lds128(q_row1 + qo + 16);
 #pragma unroll
-          for (int b = 0; b < kS; ++b)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              const uint4 kk = lds128(kb + b * kStripBytes + k_off[j] + (i >> 1) * 128 +
-                                        (((4 * (i & 1) + tq) ^ (2 * kr + (i >> 1))) << 4));
-              const uint4 k0 = e4m3x8_to_f16x8(make_uint2(kk.x, kk.y)), k1 = e4m3x8_to_f16x8(make_uint2(kk.z, kk.w));
-              mma_f16_16816(s[b][j], qa0.x, qc0.x, qa0.y, qc0.y, k0.x, k0.y);
-              mma_f16_16816(s[b][j], qa0.z, qc0.z, qa0.w, qc0.w, k0.z, k0.w);
-              mma_f16_16816(s[b][j], qa1.x, qc1.x, qa1.y, qc1.y, k1.x, k1.y);
-              mma_f16_16816(s[b][j], qa1.z, qc1.z, qa1.w, qc1.w, k1.z, k1.w);
-            }
+          for (int j = 0; j < 2; ++j) {
+            const uint4 kk =
+                lds128(kb + k_off[j] + (i >> 1) * 128 + (((4 * (i & 1) + tq) ^ (2 * kr + (i >> 1))) << 4));
+            const uint4 k0 = e4m3x8_to_f16x8(make_uint2(kk.x, kk.y)), k1 = e4m3x8_to_f16x8(make_uint2(kk.z, kk.w));
+            mma_f16_16816(s[j], qa0.x, qc0.x, qa0.y, qc0.y, k0.x, k0.y);
+            mma_f16_16816(s[j], qa0.z, qc0.z, qa0.w, qc0.w, k0.z, k0.w);
+            mma_f16_16816(s[j], qa1.x, qc1.x, qa1.y, qc1.y, k1.x, k1.y);
+            mma_f16_16816(s[j], qa1.z, qc1.z, qa1.w, qc1.w, k1.z, k1.w);
+          }
         }
       } else {
         float s2[2][4];  // a second accumulator each: half the chain of dependent products
@@ -506,38 +502,31 @@ __device__ void consumers(const DenseArgs& a, uint8_t* smem, Walk w, const Share
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             const uint4 kk = lds128(kb + k_off[j] + (i >> 1) * 1024 + ((ch ^ kr) << 4));
-            mma_bf16_16816(s[0][j], qa.x, qc.x, qa.y, qc.y, kk.x, kk.y);
+            mma_bf16_16816(s[j], qa.x, qc.x, qa.y, qc.y, kk.x, kk.y);
             mma_bf16_16816(s2[j], qa.z, qc.z, qa.w, qc.w, kk.z, kk.w);
           }
         }
 #pragma unroll
         for (int j = 0; j < 2; ++j)
 #pragma unroll
-          for (int c = 0; c < 4; ++c) s[0][j][c] += s2[j][c];
+          for (int c = 0; c < 4; ++c) s[j][c] += s2[j][c];
       }
-      // ---- mask, running maximum and sum (base 2; the scale is positive, so the largest
-      // product is the largest logit)
-      const bool whole = nv == LY::kTile;
-      auto seen = [&](int b, int j, int e) {
-        return b * kStrip + tile_run(j, e) * kRatio + tile_row<F8>(tq, e) < nv;
-      };
-      if (!whole) {
+    };
+    // ---- S to weights: mask, running maximum and sum (base 2; the scale is positive, so the
+    // largest product is the largest logit).  BF16 V: the weights leave as a BF16 hi + lo
+    // pair (about 17 significant bits; 8 alone would show in short contexts).  e4m3 V: FP16
+    // weights (at most 2^8), 11 bits against the cache's 4.
+    auto weigh = [&](int ti, int nv, float(&p)[2][4], uint32_t(&pa)[4], uint32_t(&pl)[4]) {
+      auto seen = [&](int j, int e) { return tile_run(j, e) * kRatio + tile_row<F8>(tq, e) < nv; };
+      if (nv != kTile) {
 #pragma unroll
-        for (int b = 0; b < kS; ++b)
+        for (int j = 0; j < 2; ++j)
 #pragma unroll
-          for (int j = 0; j < 2; ++j)
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-              if (!seen(b, j, e)) s[b][j][e] = s[b][j][2 + e] = -INFINITY;
+          for (int e = 0; e < 2; ++e)
+            if (!seen(j, e)) p[j][e] = p[j][2 + e] = -INFINITY;
       }
-      float r0 = -INFINITY, r1 = -INFINITY;
-#pragma unroll
-      for (int b = 0; b < kS; ++b)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          r0 = fmaxf(r0, fmaxf(s[b][j][0], s[b][j][1]));
-          r1 = fmaxf(r1, fmaxf(s[b][j][2], s[b][j][3]));
-        }
+      float r0 = fmaxf(fmaxf(p[0][0], p[0][1]), fmaxf(p[1][0], p[1][1]));
+      float r1 = fmaxf(fmaxf(p[0][2], p[0][3]), fmaxf(p[1][2], p[1][3]));
       r0 = fmaxf(r0, __shfl_xor_sync(0xffffffffu, r0, 1));
       r1 = fmaxf(r1, __shfl_xor_sync(0xffffffffu, r1, 1));
       r0 = fmaxf(r0, __shfl_xor_sync(0xffffffffu, r0, 2)) * sc0;
@@ -561,107 +550,106 @@ __device__ void consumers(const DenseArgs& a, uint8_t* smem, Walk w, const Share
       // rows that have seen no token yet keep every weight at 0
       const float sub0 = m0 == -INFINITY ? 0.f : -m0, sub1 = m1 == -INFINITY ? 0.f : -m1;
 #pragma unroll
-      for (int b = 0; b < kS; ++b) {
-        float(&p)[2][4] = s[b];  // the weights take the products' place
+      for (int j = 0; j < 2; ++j) {
+        p[j][0] = exp2_fast(fmaf(p[j][0], sc0, sub0));
+        p[j][1] = exp2_fast(fmaf(p[j][1], sc0, sub0));
+        p[j][2] = exp2_fast(fmaf(p[j][2], sc1, sub1));
+        p[j][3] = exp2_fast(fmaf(p[j][3], sc1, sub1));
+      }
+      if (nv != kTile) {  // also where a scale has underflowed to 0
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          p[j][0] = exp2_fast(fmaf(p[j][0], sc0, sub0));
-          p[j][1] = exp2_fast(fmaf(p[j][1], sc0, sub0));
-          p[j][2] = exp2_fast(fmaf(p[j][2], sc1, sub1));
-          p[j][3] = exp2_fast(fmaf(p[j][3], sc1, sub1));
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            if (!seen(j, e)) p[j][e] = p[j][2 + e] = 0.f;
+      }
+      l0 += (p[0][0] + p[0][1]) + (p[1][0] + p[1][1]);
+      l1 += (p[0][2] + p[0][3]) + (p[1][2] + p[1][3]);
+      // weight of each micro-block: sums over its 4 tokens, one per quad lane (run 2j + e
+      // over the quad: halve the runs a lane carries twice)
+      if (a.bsum) {
+        const bool hi = tq & 2, odd = tq & 1;
+        const float a0 = (hi ? p[1][0] : p[0][0]) + __shfl_xor_sync(0xffffffffu, hi ? p[0][0] : p[1][0], 2);
+        const float a1 = (hi ? p[1][1] : p[0][1]) + __shfl_xor_sync(0xffffffffu, hi ? p[0][1] : p[1][1], 2);
+        const float c0 = (hi ? p[1][2] : p[0][2]) + __shfl_xor_sync(0xffffffffu, hi ? p[0][2] : p[1][2], 2);
+        const float c1 = (hi ? p[1][3] : p[0][3]) + __shfl_xor_sync(0xffffffffu, hi ? p[0][3] : p[1][3], 2);
+        const float b0 = (odd ? a1 : a0) + __shfl_xor_sync(0xffffffffu, odd ? a0 : a1, 1);
+        const float b1 = (odd ? c1 : c0) + __shfl_xor_sync(0xffffffffu, odd ? c0 : c1, 1);
+        const int64_t base = ((int64_t)w.q * a.hq + (int64_t)w.g * G) * max_tiles + w.t0 + ti;
+        if (gq < G) {
+          const int64_t at = base + gq * max_tiles;
+          a.bsum[at * 4 + tq] = b0;
+          if (tq == 0) a.bmax[at] = m0;
         }
-        if (!whole) {  // also where a scale has underflowed to 0
-#pragma unroll
-          for (int j = 0; j < 2; ++j)
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-              if (!seen(b, j, e)) p[j][e] = p[j][2 + e] = 0.f;
-        }
-        l0 += (p[0][0] + p[0][1]) + (p[1][0] + p[1][1]);
-        l1 += (p[0][2] + p[0][3]) + (p[1][2] + p[1][3]);
-
-        // ---- weight of each micro-block: sums over its 4 tokens, one per quad lane
-        if (a.bsum) {
-          // run 2j + e over the quad: halve the runs a lane carries twice
-          const bool hi = tq & 2, odd = tq & 1;
-          const float a0 = (hi ? p[1][0] : p[0][0]) + __shfl_xor_sync(0xffffffffu, hi ? p[0][0] : p[1][0], 2);
-          const float a1 = (hi ? p[1][1] : p[0][1]) + __shfl_xor_sync(0xffffffffu, hi ? p[0][1] : p[1][1], 2);
-          const float c0 = (hi ? p[1][2] : p[0][2]) + __shfl_xor_sync(0xffffffffu, hi ? p[0][2] : p[1][2], 2);
-          const float c1 = (hi ? p[1][3] : p[0][3]) + __shfl_xor_sync(0xffffffffu, hi ? p[0][3] : p[1][3], 2);
-          const float b0 = (odd ? a1 : a0) + __shfl_xor_sync(0xffffffffu, odd ? a0 : a1, 1);
-          const float b1 = (odd ? c1 : c0) + __shfl_xor_sync(0xffffffffu, odd ? c0 : c1, 1);
-          const int64_t base = ((int64_t)w.q * a.hq + (int64_t)w.g * G) * max_strips + (int64_t)(w.t0 + ti) * kS + b;
-          if (gq < G) {
-            const int64_t at = base + gq * max_strips;
-            a.bsum[at * 4 + tq] = b0;
-            if (tq == 0) a.bmax[at] = m0;
-          }
-          if (gq + 8 < G) {
-            const int64_t at = base + (gq + 8) * max_strips;
-            a.bsum[at * 4 + tq] = b1;
-            if (tq == 0) a.bmax[at] = m1;
-          }
+        if (gq + 8 < G) {
+          const int64_t at = base + (gq + 8) * max_tiles;
+          a.bsum[at * 4 + tq] = b1;
+          if (tq == 0) a.bmax[at] = m1;
         }
       }
-
-      // ---- O += P V.  BF16 V: the weights enter as a BF16 hi + lo pair (about 17
-      // significant bits; 8 alone would show in short contexts).  e4m3 V: FP16 weights
-      // (at most 2^8), 11 bits against the cache's 4.
-      uint32_t pa[kS][4], pl[4];
 #pragma unroll
-      for (int b = 0; b < kS; ++b)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float x = s[b][k >> 1][2 * (k & 1)], y = s[b][k >> 1][2 * (k & 1) + 1];
-          if constexpr (F8) {
-            const __half2 h = __floats2half2_rn(x, y);
-            pa[b][k] = *reinterpret_cast<const uint32_t*>(&h);
-          } else {
-            split_bf16(x, y, pa[b][k], pl[k]);
-          }
+      for (int k = 0; k < 4; ++k) {
+        const float x = p[k >> 1][2 * (k & 1)], y = p[k >> 1][2 * (k & 1) + 1];
+        if constexpr (F8) {
+          const __half2 h = __floats2half2_rn(x, y);
+          pa[k] = *reinterpret_cast<const uint32_t*>(&h);
+        } else {
+          split_bf16(x, y, pa[k], pl[k]);
         }
+      }
+    };
+    // ---- O += P V of the tile at kb
+    auto add_values = [&](uint32_t kb, int nv, const uint32_t(&pa)[4], const uint32_t(&pl)[4]) {
       constexpr int kParts = F8 ? 2 : 4;  // e4m3: 128 dims per 16-byte read of the 8 column groups; BF16: 64
 #pragma unroll
       for (int c = 0; c < kParts; ++c) {
+        uint32_t x[2][2][4];
 #pragma unroll
-        for (int b = 0; b < kS; ++b) {
-          uint32_t x[2][2][4];
+        for (int j = 0; j < 2; ++j)
 #pragma unroll
-          for (int j = 0; j < 2; ++j)
+          for (int e = 0; e < 2; ++e) {
+            uint4 v = lds128(kb + (F8 ? v_off[j][e] ^ (c * (128 + 16)) : v_off[j][e] + c * 1024));
+            if (nv != kTile && tile_run(j, e) * kRatio + tile_row<F8>(tq, e) >= nv)
+              v = make_uint4(0, 0, 0, 0);  // rows behind the end may hold anything
+            x[j][e][0] = v.x;
+            x[j][e][1] = v.y;
+            x[j][e][2] = v.z;
+            x[j][e][3] = v.w;
+          }
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              uint4 v = lds128(kb + b * kStripBytes + (F8 ? v_off[j][e] ^ (c * (128 + 16)) : v_off[j][e] + c * 1024));
-              if (!whole && !seen(b, j, e)) v = make_uint4(0, 0, 0, 0);  // rows behind the end may hold anything
-              x[j][e][0] = v.x;
-              x[j][e][1] = v.y;
-              x[j][e][2] = v.z;
-              x[j][e][3] = v.w;
-            }
-          const uint32_t(&pb)[4] = pa[b];
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            if constexpr (F8) {  // 4 dims: the two tokens' bytes are paired, then widened
-              const uint2 t0 = e4m3x4_to_f16x4(__byte_perm(x[0][0][r], x[0][1][r], 0x5140));
-              const uint2 t1 = e4m3x4_to_f16x4(__byte_perm(x[0][0][r], x[0][1][r], 0x7362));
-              const uint2 u0 = e4m3x4_to_f16x4(__byte_perm(x[1][0][r], x[1][1][r], 0x5140));
-              const uint2 u1 = e4m3x4_to_f16x4(__byte_perm(x[1][0][r], x[1][1][r], 0x7362));
-              mma_f16_16816(o[c * 16 + 4 * r + 0], pb[0], pb[1], pb[2], pb[3], t0.x, u0.x);
-              mma_f16_16816(o[c * 16 + 4 * r + 1], pb[0], pb[1], pb[2], pb[3], t0.y, u0.y);
-              mma_f16_16816(o[c * 16 + 4 * r + 2], pb[0], pb[1], pb[2], pb[3], t1.x, u1.x);
-              mma_f16_16816(o[c * 16 + 4 * r + 3], pb[0], pb[1], pb[2], pb[3], t1.y, u1.y);
-            } else {
-              const uint32_t lo0 = __byte_perm(x[0][0][r], x[0][1][r], 0x5410);
-              const uint32_t hi0 = __byte_perm(x[0][0][r], x[0][1][r], 0x7632);
-              const uint32_t lo1 = __byte_perm(x[1][0][r], x[1][1][r], 0x5410);
-              const uint32_t hi1 = __byte_perm(x[1][0][r], x[1][1][r], 0x7632);
-              mma_bf16_16816(o[c * 8 + 2 * r], pb[0], pb[1], pb[2], pb[3], lo0, lo1);
-              mma_bf16_16816(o[c * 8 + 2 * r + 1], pb[0], pb[1], pb[2], pb[3], hi0, hi1);
-              mma_bf16_16816(o[c * 8 + 2 * r], pl[0], pl[1], pl[2], pl[3], lo0, lo1);
-              mma_bf16_16816(o[c * 8 + 2 * r + 1], pl[0], pl[1], pl[2], pl[3], hi0, hi1);
-            }
+        for (int r = 0; r < 4; ++r) {
+          if constexpr (F8) {  // 4 dims: the two tokens' bytes are paired, then widened
+            const uint2 t0 = e4m3x4_to_f16x4(__byte_perm(x[0][0][r], x[0][1][r], 0x5140));
+            const uint2 t1 = e4m3x4_to_f16x4(__byte_perm(x[0][0][r], x[0][1][r], 0x7362));
+            const uint2 u0 = e4m3x4_to_f16x4(__byte_perm(x[1][0][r], x[1][1][r], 0x5140));
+            const uint2 u1 = e4m3x4_to_f16x4(__byte_perm(x[1][0][r], x[1][1][r], 0x7362));
+            mma_f16_16816(o[c * 16 + 4 * r + 0], pa[0], pa[1], pa[2], pa[3], t0.x, u0.x);
+            mma_f16_16816(o[c * 16 + 4 * r + 1], pa[0], pa[1], pa[2], pa[3], t0.y, u0.y);
+            mma_f16_16816(o[c * 16 + 4 * r + 2], pa[0], pa[1], pa[2], pa[3], t1.x, u1.x);
+            mma_f16_16816(o[c * 16 + 4 * r + 3], pa[0], pa[1], pa[2], pa[3], t1.y, u1.y);
+          } else {
+            const uint32_t lo0 = __byte_perm(x[0][0][r], x[0][1][r], 0x5410);
+            const uint32_t hi0 = __byte_perm(x[0][0][r], x[0][1][r], 0x7632);
+            const uint32_t lo1 = __byte_perm(x[1][0][r], x[1][1][r], 0x5410);
+            const uint32_t hi1 = __byte_perm(x[1][0][r], x[1][1][r], 0x7632);
+            mma_bf16_16816(o[c * 8 + 2 * r], pa[0], pa[1], pa[2], pa[3], lo0, lo1);
+            mma_bf16_16816(o[c * 8 + 2 * r + 1], pa[0], pa[1], pa[2], pa[3], hi0, hi1);
+            mma_bf16_16816(o[c * 8 + 2 * r], pl[0], pl[1], pl[2], pl[3], lo0, lo1);
+            mma_bf16_16816(o[c * 8 + 2 * r + 1], pl[0], pl[1], pl[2], pl[3], hi0, hi1);
           }
         }
       }
+    };
+    for (int ti = rank; ti < n_tiles; ti += kWarps) {
+      const int stage = landed(ti);
+      if (stage < 0) break;
+      const int nv = valid[stage];
+      const uint32_t kb = ring + stage * LY::kStageBytes;
+      float s[2][4];
+      uint32_t pa[4], pl[4];
+      products(kb, s);
+      weigh(ti, nv, s, pa, pl);
+      add_values(kb, nv, pa, pl);
       held = stage;
       if (ti + kWarps < n_tiles) {  // the last stage is kept for the join
         __syncwarp();
@@ -683,7 +671,7 @@ __device__ void consumers(const DenseArgs& a, uint8_t* smem, Walk w, const Share
     l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
     // whole pair here: straight to out; else to the partial slot of the pair that this
     // CTA took over (0) or leaves unfinished (1)
-    const int nt_pair = tiles_of<LY>(w.len);
+    const int nt_pair = tiles_of(w.len);
     const bool direct = w.t0 == 0 && w.t1 == nt_pair;
     const int slot = 2 * blockIdx.x + (w.t0 == 0 ? 1 : 0);
     const size_t out_row = direct ? (size_t)w.q * a.hq + (size_t)w.g * G : (size_t)slot * G;
@@ -697,7 +685,7 @@ __device__ void consumers(const DenseArgs& a, uint8_t* smem, Walk w, const Share
       if (w.t0 == 0 && lane == 0)
         a.span[w.q * a.hkv + w.g] =
             make_int2(blockIdx.x, direct ? blockIdx.x
-                                         : share_of(sh, w.begin + cost_of<LY>(nt_pair) + nt_pair - 1));
+                                         : share_of(sh, w.begin + cost_of(nt_pair) + nt_pair - 1));
     };
     // the columns and n-tiles of dim slice sl (see the join below)
     auto e_of = [](int sl) { return F8 ? (sl >> 1) & 1 : sl & 1; };
@@ -727,7 +715,7 @@ __device__ void consumers(const DenseArgs& a, uint8_t* smem, Walk w, const Share
           }
         }
       }
-      if (!next_piece<LY>(a, w, x1)) break;
+      if (!next_piece(a, w, x1)) break;
       continue;
     }
     if (lane == 0) held_s[rank] = held;
@@ -808,7 +796,7 @@ __device__ void consumers(const DenseArgs& a, uint8_t* smem, Walk w, const Share
       }
     }
     if (warp == kWarps - 1) put_lse(M[0] + log2f(L[0]), M[1] + log2f(L[1]));  // -inf when L = 0
-    if (!next_piece<LY>(a, w, x1)) break;
+    if (!next_piece(a, w, x1)) break;
     // every stage has been read: hand the held ones back to the copies, which come after
     // these ordinary writes
     fence_proxy_async();
@@ -845,7 +833,7 @@ __global__ void __launch_bounds__(Lay<F8>::kThreads, 1) dense_decode_kernel(cons
   auto scan_round = [&](int base, bool report) {  // places before query base + tid; total moves on
     const int q = base + tid;
     len = q < a.nq ? query_len(a, q, report) : 0;
-    const int n = places_of<LY>(len) * a.hkv;
+    const int n = places_of(len) * a.hkv;
     int inc = n;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -870,11 +858,11 @@ __global__ void __launch_bounds__(Lay<F8>::kThreads, 1) dense_decode_kernel(cons
       for (int g = 0; g < a.hkv; ++g) a.span[(b + tid) * a.hkv + g] = make_int2(0, -1);
   }
   if (total == 0) return;
-  const Shares sh = make_shares<LY>(total, a.ctas);
+  const Shares sh = make_shares(total, a.ctas);
   if ((int)blockIdx.x >= sh.n) return;
   const int x0 = share_begin(sh, blockIdx.x), x1 = share_begin(sh, blockIdx.x + 1);
   auto find_first = [&](int base) {  // the query that holds place x0
-    if (len > 0 && first <= x0 && x0 < first + places_of<LY>(len) * a.hkv) {
+    if (len > 0 && first <= x0 && x0 < first + places_of(len) * a.hkv) {
       plan[0] = base + tid;
       plan[1] = first;
     }
@@ -900,9 +888,9 @@ __global__ void __launch_bounds__(Lay<F8>::kThreads, 1) dense_decode_kernel(cons
   }
   w.len = tab[w.q - w.q_tab].x;
   w.seq = tab[w.q - w.q_tab].y;
-  w.g = (x0 - w.begin) / places_of<LY>(w.len);
-  w.begin += w.g * places_of<LY>(w.len);
-  if (!set_span<LY>(w, x0, x1)) return;  // the share ends before the pair's first tile
+  w.g = (x0 - w.begin) / places_of(w.len);
+  w.begin += w.g * places_of(w.len);
+  if (!set_span(w, x0, x1)) return;  // the share ends before the pair's first tile
   if constexpr (F8) {  // by whole warpgroups, and by every one that is left
     if (warp < kWarps)
       asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(LY::kConsumerRegs));
@@ -956,7 +944,7 @@ __device__ __forceinline__ float joined_lse2(const DenseArgs& a, int q, int h) {
 
 // The first blocks: `parts` of them a (query, KV head) pair, for every parts-th head
 // each; the pieces of a head are spread over 4 groups of 64 threads (4 dims each) and summed in a fixed order.  The blocks
-// after them add up weights: 64 strips (256 micro-blocks) of one query's sequence
+// after them add up weights: 64 tiles (256 micro-blocks) of one query's sequence
 // each, the heads spread over the 4 groups.
 __global__ void __launch_bounds__(kJoinThreads) dense_join_kernel(const __grid_constant__ JoinArgs ja) {
   const DenseArgs& a = ja.d;
@@ -1052,10 +1040,10 @@ __global__ void __launch_bounds__(kJoinThreads) dense_join_kernel(const __grid_c
   constexpr int kHeads = 8, kRound = 4 * kHeads;  // heads of a group and of the block at once
   const int64_t wb = blockIdx.x - n_join;
   const int q0 = (int)(wb / ja.mass_blocks);
-  const int strip = (int)(wb % ja.mass_blocks) * 64 + (tid & 63), grp = tid >> 6;
+  const int tile = (int)(wb % ja.mass_blocks) * 64 + (tid & 63), grp = tid >> 6;
   const int seq = a.q_seq[q0];
   if (query_len(a, q0, false) == 0) return;
-  const int64_t max_strips = (int64_t)a.mpps * kStripsPerPage;
+  const int64_t max_tiles = (int64_t)a.mpps * kTilesPerPage;
   __shared__ unsigned same_s[kJoinThreads / 32];  // queries of this sequence, 256 at a time
   float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
   int longest = 0;
@@ -1070,7 +1058,7 @@ __global__ void __launch_bounds__(kJoinThreads) dense_join_kernel(const __grid_c
         const int q = qb + v * 32 + __ffs(bits) - 1;
         if (q < q0) return;  // not the first: the same in every thread
         const int len = query_len(a, q, false);
-        const bool on = strip < (len + kStrip - 1) / kStrip;
+        const bool on = tile < (len + kTile - 1) / kTile;
         longest = max(longest, len);
         for (int h0 = 0; h0 < a.hq; h0 += kRound) {
           float bm[kHeads];
@@ -1081,7 +1069,7 @@ __global__ void __launch_bounds__(kJoinThreads) dense_join_kernel(const __grid_c
             bm[k] = -INFINITY;
             b[k] = make_float4(0.f, 0.f, 0.f, 0.f);
             if (on && h < a.hq) {
-              const int64_t at = ((int64_t)q * a.hq + h) * max_strips + strip;
+              const int64_t at = ((int64_t)q * a.hq + h) * max_tiles + tile;
               bm[k] = a.bmax[at];
               b[k] = reinterpret_cast<const float4*>(a.bsum)[at];
             }
@@ -1119,7 +1107,7 @@ __global__ void __launch_bounds__(kJoinThreads) dense_join_kernel(const __grid_c
   const int64_t row = (int64_t)seq * ja.mass_ld;
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    const int b = strip * kStripRuns + k;
+    const int b = tile * kTileRuns + k;
     if (b < blocks) ja.mass_out[row + b] = ja.decay * ja.mass_in[row + b] + v[k];
   }
 }
@@ -1137,7 +1125,7 @@ WorkspaceMap workspace_map(const qsa_cache_t& c, int32_t nq, int32_t hq, bool wi
   m.part_lse = align256((int64_t)nq * c.num_kv_heads * 8);
   m.part_o = m.part_lse + align256(2 * kMaxCtas * G * 4);
   m.bsum = m.part_o + align256(2 * kMaxCtas * G * kHeadDim * 4);
-  const int64_t tiles = with_mass ? (int64_t)nq * hq * c.max_pages_per_seq * kStripsPerPage : 0;
+  const int64_t tiles = with_mass ? (int64_t)nq * hq * c.max_pages_per_seq * kTilesPerPage : 0;
   m.bmax = m.bsum + align256(tiles * 16);
   m.total = m.bmax + align256(tiles * 4);
   return m;
@@ -1150,18 +1138,27 @@ int check_shape(const qsa_cache_t* cache, int32_t nq, int32_t hq) {
   if (hq % c.num_kv_heads != 0) return QSA_ERR_INVALID_ARG;
   if (hq / c.num_kv_heads > QSA_MAX_GROUP) return QSA_ERR_UNSUPPORTED;
   if (c.max_pages_per_seq > 0x7fffffff / kPage) return QSA_ERR_UNSUPPORTED;  // positions are int32
-  if (((int64_t)c.max_pages_per_seq * kStripsPerPage + 8) * c.num_kv_heads > 0x7fffffff / (nq > 0 ? nq : 1))
+  if (((int64_t)c.max_pages_per_seq * kTilesPerPage + 8) * c.num_kv_heads > 0x7fffffff / (nq > 0 ? nq : 1))
     return QSA_ERR_UNSUPPORTED;  // places are int32
   return QSA_OK;
 }
 
 template <bool F8>
 int launch_dense(const DenseArgs& a, cudaStream_t s) {
-  // per device, once: the attribute belongs to the device's copy of the kernel
+  // the attribute belongs to the device's copy of the kernel
   if (cudaFuncSetAttribute(dense_decode_kernel<F8>, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<F8>::kSmem) !=
       cudaSuccess) {
     (void)cudaGetLastError();
     return QSA_ERR_CUDA;
+  }
+  if constexpr (F8) {  // a kernel built with fewer registers would wait for its share forever
+    static const bool enough = [] {
+      cudaFuncAttributes f;
+      const bool ok = cudaFuncGetAttributes(&f, dense_decode_kernel<F8>) == cudaSuccess;
+      if (!ok) (void)cudaGetLastError();
+      return ok && f.numRegs >= Lay<F8>::kRegs;
+    }();
+    if (!enough) return QSA_ERR_CUDA;
   }
   return qsa_host::launch(dense_decode_kernel<F8>, dim3((unsigned)a.ctas), dim3(Lay<F8>::kThreads), (size_t)Lay<F8>::kSmem, s,
                           a);
@@ -1242,7 +1239,7 @@ extern "C" int qsa_dense_decode(const qsa_cache_t* cache, const void* q, int32_t
   j.mass_out = mass_out;
   j.mass_ld = mass_ld;
   j.decay = decay;
-  const int64_t tiles = (int64_t)c.max_pages_per_seq * kStripsPerPage;
+  const int64_t tiles = (int64_t)c.max_pages_per_seq * kTilesPerPage;
   j.mass_blocks = (int32_t)((tiles + 63) / 64);
   // About 8 CTAs per SM, a head each at most.  Of a large batch's pairs many need no join:
   // a CTA per head, to find that out, took 2.2 us more for 161 queries of 24 heads, and one
