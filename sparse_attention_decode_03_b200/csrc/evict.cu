@@ -9,9 +9,9 @@
 // the side cache describes: its K/V run of every KV head and its kc row move
 // together.
 //
-// evict_select_kernel, one CTA per sequence: radix select of the cut (11 + 11 +
-// 10 bits of the order-preserving key) over masses held in shared memory, then one
-// ordered pass that writes the kept indices, the number kept before every page,
+// evict_select_kernel, a CTA per sequence or a cluster of up to 8: radix select of the
+// cut (11 + 11 + 10 bits of the order-preserving key) over masses held in shared
+// memory, histograms summed over the cluster's shared memory, then one ordered pass that writes the kept indices, the number kept before every page,
 // and the moved mass row.
 //
 // evict_move_kernel: units of one destination page and KV head (16 runs, 64 KiB
@@ -35,6 +35,7 @@ constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kBins0 = 2048, kBins1 = 2048, kBins2 = 1024;  // 11 + 11 + 10 bits of a key
 constexpr int kFew = 256;  // keys that are ranked by comparing each with all
+constexpr int kMaxCluster = 8;
 constexpr int kOnePerSm = 116 * 1024;
 constexpr int kMaxRoom = 48 * 1024;  // masses the selection keeps in shared memory: 192 KiB, 196,608 tokens
 constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s
@@ -76,29 +77,69 @@ __device__ __forceinline__ int entry_seq(const EvictArgs& a, int i, bool report)
   return bad ? -1 : seq;
 }
 
-__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictArgs a, int room) {
+// All threads of the cluster's CTAs; orders shared and global memory among them.
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
+// The shared-memory word at `p` of CTA `rank` of this cluster.
+__device__ __forceinline__ uint32_t remote_addr(const void* p, int rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ uint32_t ld_remote(const void* p, int rank) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(remote_addr(p, rank)) : "memory");
+  return v;
+}
+__device__ __forceinline__ void st_remote(void* p, int rank, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(remote_addr(p, rank)), "r"(v) : "memory");
+}
+__device__ __forceinline__ uint32_t add_remote(void* p, int rank, uint32_t v) {
+  uint32_t old;
+  asm volatile("atom.shared::cluster.add.u32 %0, [%1], %2;" : "=r"(old) : "r"(remote_addr(p, rank)), "r"(v) : "memory");
+  return old;
+}
+
+// kCluster: an entry is shared by a cluster of `cluster` CTAs, else one CTA takes it.
+template <bool kCluster>
+__global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(EvictArgs a, int cluster, int room) {
+  const int ctas = kCluster ? cluster : 1;
   extern __shared__ float mass_s[];
   pdl_launch_dependents();
   pdl_wait_previous();
-  const int i = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int i = blockIdx.x / ctas, part = blockIdx.x % ctas;  // entry, and CTA of its cluster
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int gtid = part * kSelThreads + tid, gthreads = ctas * kSelThreads;
   __shared__ uint32_t hist[kBins0 + kBins1 + kBins2];
   __shared__ int warp_sum[2][kSelWarps];
-  __shared__ uint32_t s_prefix, s_need, s_in_bin, s_few;
+  __shared__ uint32_t s_prefix, s_need, s_in_bin, s_few, total_s[2], slice_s[kMaxCluster];
+  auto sync_all = [&] {
+    if constexpr (!kCluster) {
+      __syncthreads();
+    } else {
+      __syncwarp();
+      cluster_arrive();
+      cluster_wait();
+    }
+  };
   const int hkv = a.c.num_kv_heads;
-  if (i == 0 && tid == 0) *a.ticket = 0;
-  for (int k = tid; k < hkv * a.pages; k += kSelThreads) a.read_done[(int64_t)i * hkv * a.pages + k] = 0;
+  if (blockIdx.x == 0 && tid == 0) *a.ticket = 0;
+  for (int k = gtid; k < hkv * a.pages; k += gthreads) a.read_done[(int64_t)i * hkv * a.pages + k] = 0;
   int32_t* keep = a.keep + (int64_t)i * a.budget;
-  int seq = entry_seq(a, i, true);
+  int seq = entry_seq(a, i, part == 0);
   const int len = a.seq_len[i];
   if (seq >= 0 && (len < 0 || (int64_t)len > (int64_t)a.c.max_pages_per_seq * kPage)) {
-    if (tid == 0) flag(a.st, QSA_DEV_BAD_POS);
+    if (gtid == 0) flag(a.st, QSA_DEV_BAD_POS);
     seq = -1;
   }
   int32_t* rank = a.rank + (int64_t)i * (a.c.max_pages_per_seq + 2);
-  if (tid == 0) rank[a.c.max_pages_per_seq + 1] = seq < 0 ? 0 : len;
-  if (seq < 0) {  // nothing of this entry moves
-    for (int k = tid; k < a.budget; k += kSelThreads) keep[k] = -1;
-    if (tid == 0) {
+  if (gtid == 0) rank[a.c.max_pages_per_seq + 1] = seq < 0 ? 0 : len;
+  if (seq < 0) {  // nothing of this entry moves; the whole cluster leaves before its first barrier
+    for (int k = gtid; k < a.budget; k += gthreads) keep[k] = -1;
+    if (gtid == 0) {
       a.keep_count[i] = 0;
       a.new_len[i] = len;
     }
@@ -110,25 +151,28 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictArgs a, 
   const int lo = cut ? a.sink : nb, hi = cut ? nb - a.recent : nb;  // blocks that compete
   const int want = cut ? a.budget - a.sink - a.recent : 0;
   const int count = cut ? a.budget : nb, left = count + (tail ? 1 : 0), blocks = nb + (tail ? 1 : 0);
-  // Each warp owns a run of blocks, a lane every 32nd of it.  The masses of the first
-  // `room` blocks stay in shared memory, later ones are read again.
-  const int steps = (nb + kSelThreads - 1) / kSelThreads;
-  const int b0 = warp * steps * 32 + lane;
-  const bool held = nb <= room;
+  // Each CTA owns a run of blocks, each of its warps a run of those, a lane every 32nd.
+  // The masses of a CTA's first `room` blocks stay in shared memory, later ones are
+  // read again.
+  const int steps = (nb + gthreads - 1) / gthreads;
+  const int c0 = part * steps * kSelThreads, c1 = min(nb, c0 + steps * kSelThreads);
+  const int b0 = c0 + warp * steps * 32 + lane;
+  const bool held = steps * kSelThreads <= room;  // the same in every CTA
 #pragma unroll 4
-  for (int b = tid; b < min(nb, room); b += kSelThreads) mass_s[b] = mass[b];
-  const float m_open = tail && tid == 0 ? mass[nb] : 0.f;
+  for (int b = c0 + tid; b < min(c1, c0 + room); b += kSelThreads) mass_s[b - c0] = mass[b];
+  const float m_open = tail && gtid == 0 ? mass[nb] : 0.f;
   auto each = [&](auto f) {  // every block of this lane: f(block, mass)
 #pragma unroll 2
     for (int k = 0; k < steps; ++k) {
       const int b = b0 + 32 * k;
-      f(b, b < nb ? (b < room ? mass_s[b] : mass[b]) : 0.f);
+      f(b, b < nb ? (b - c0 < room ? mass_s[b - c0] : mass[b]) : 0.f);
     }
   };
   for (int k = tid; k < kBins0 + kBins1 + kBins2; k += kSelThreads) hist[k] = 0;
   if (tid == 0) s_few = 0;
-  __syncthreads();
-  // ---- the cut: the want-th largest key of [lo, hi), and how many equal to it are kept
+  sync_all();  // also: every CTA of the cluster runs before its shared memory is touched
+  // ---- the cut: the want-th largest key of [lo, hi), and how many equal to it are kept.
+  // Every CTA of a cluster works it out for itself from the sum of all histograms.
   uint32_t T = 0xffffffffu;
   int need = 0;
   if (want > 0) {
@@ -143,14 +187,31 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictArgs a, 
         const uint32_t key = mass_key(x);
         if (b >= lo && b < hi && (key & mask) == prefix) atomicAdd(&h[(key >> sh) & (bins - 1)], 1u);
       });
-      __syncthreads();
-      // counts from the top: thread t owns 2 bins (or 1) from there, warp w the t of its lanes
-      const int per = bins / kSelThreads, top = bins - 1 - tid * per;
-      const uint32_t first = h[top], own = first + (per == 2 ? h[top - 1] : 0u);
+      sync_all();
+      // counts from the top: CTA c of the cluster sums slice c of the bins, its thread t
+      // bin t of them (2t and 2t + 1 of 2,048 in one CTA), warp w the t of its lanes
+      const int slice = bins / ctas, per = slice > kSelThreads ? 2 : 1;
+      const int top = bins - 1 - part * slice - tid * per;
+      uint32_t first = 0, second = 0;
+      if constexpr (!kCluster) {
+        first = h[top];
+        second = per == 2 ? h[top - 1] : 0u;
+      } else if (tid < slice) {
+#pragma unroll
+        for (int c = 0; c < kMaxCluster; ++c)
+          if (c < ctas) first += ld_remote(&h[top], c);
+      }
+      const uint32_t own = first + second;
       const uint32_t sum = __reduce_add_sync(0xffffffffu, own);
       if (lane == 0) warp_sum[0][warp] = (int)sum;
       __syncthreads();
-      const uint32_t before_warp = __reduce_add_sync(0xffffffffu, lane < warp ? (uint32_t)warp_sum[0][lane] : 0u);
+      uint32_t before_warp = __reduce_add_sync(0xffffffffu, lane < warp ? (uint32_t)warp_sum[0][lane] : 0u);
+      if constexpr (kCluster) {  // the slices above
+        const uint32_t total = __reduce_add_sync(0xffffffffu, (uint32_t)warp_sum[0][lane]);
+        if (tid < ctas) st_remote(&slice_s[part], tid, total);
+        sync_all();
+        before_warp += __reduce_add_sync(0xffffffffu, lane < part ? slice_s[lane] : 0u);
+      }
       if (before_warp < (uint32_t)rest && before_warp + sum >= (uint32_t)rest) {  // the cut is in this warp's bins
         uint32_t inc = own;
 #pragma unroll
@@ -160,23 +221,43 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictArgs a, 
         }
         const uint32_t before = before_warp + inc - own;
         if (before < (uint32_t)rest && before + own >= (uint32_t)rest) {
-          const bool second = before + first < (uint32_t)rest;
-          s_prefix = prefix | ((uint32_t)(top - second) << sh);
-          s_need = (uint32_t)rest - before - (second ? first : 0u);
-          s_in_bin = second ? own - first : first;
+          const bool low = before + first < (uint32_t)rest;
+          const uint32_t to = prefix | ((uint32_t)(top - low) << sh), nd = (uint32_t)rest - before - (low ? first : 0u);
+          const uint32_t in = low ? second : first;
+          if constexpr (!kCluster) {
+            s_prefix = to;
+            s_need = nd;
+            s_in_bin = in;
+          } else {
+            for (int c = 0; c < ctas; ++c) {
+              st_remote(&s_prefix, c, to);
+              st_remote(&s_need, c, nd);
+              st_remote(&s_in_bin, c, in);
+            }
+          }
         }
       }
-      __syncthreads();
+      sync_all();
       prefix = s_prefix;
       rest = (int)s_need;
       h += bins;
       const int n = (int)s_in_bin;
-      if (pass < 2 && n <= kFew) {  // few keys left: each counts those above it (h is free now)
+      if (pass < 2 && n <= kFew) {  // few keys left: listed in the first CTA (h is free now), each
+                                    // counts those above it
         each([&](int b, float x) {
           const uint32_t key = mass_key(x);
-          if (b >= lo && b < hi && (key & ~0u << sh) == prefix) h[atomicAdd(&s_few, 1u)] = key;
+          if (b >= lo && b < hi && (key & ~0u << sh) == prefix) {
+            if constexpr (!kCluster)
+              h[atomicAdd(&s_few, 1u)] = key;
+            else
+              st_remote(&h[add_remote(&s_few, 0, 1u)], 0, key);
+          }
         });
-        __syncthreads();
+        sync_all();
+        if (kCluster && part > 0) {
+          if (tid < n) h[tid] = ld_remote(&h[tid], 0);
+          __syncthreads();
+        }
         if (tid < n) {
           const uint32_t key = h[tid];
           int above = 0, equal = 0;
@@ -219,9 +300,20 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictArgs a, 
     warp_sum[0][warp] = gt;
     warp_sum[1][warp] = eq;
   }
-  __syncthreads();  // every mass that is held has been read: its row may be overwritten
+  __syncthreads();
   int gt0 = __reduce_add_sync(0xffffffffu, lane < warp ? warp_sum[0][lane] : 0);
   int eq0 = __reduce_add_sync(0xffffffffu, lane < warp ? warp_sum[1][lane] : 0);
+  if constexpr (kCluster) {
+    if (warp == kSelWarps - 1 && lane == 0) {
+      total_s[0] = (uint32_t)(gt0 + gt);
+      total_s[1] = (uint32_t)(eq0 + eq);
+    }
+    sync_all();  // every held mass of the row has been read: it may be overwritten
+    gt0 += __reduce_add_sync(0xffffffffu, lane < part ? (int)ld_remote(&total_s[0], lane) : 0);
+    eq0 += __reduce_add_sync(0xffffffffu, lane < part ? (int)ld_remote(&total_s[1], lane) : 0);
+    __syncwarp();
+    cluster_arrive();  // done with the other CTAs' shared memory; waited for before leaving
+  }
   // ---- in order: kept indices, blocks kept before each page, and the moved masses
   // (rows too long to be held pass through the workspace)
   float* out = a.mass_out + (int64_t)seq * a.mass_ld;
@@ -243,19 +335,23 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictArgs a, 
     gt0 += __popc(gm);
     eq0 += __popc(em);
   });
-  for (int k = count + tid; k < a.budget; k += kSelThreads) keep[k] = -1;
-  for (int P = (nb + kBlocksPerPage - 1) / kBlocksPerPage + tid; P <= a.c.max_pages_per_seq; P += kSelThreads)
+  for (int k = count + gtid; k < a.budget; k += gthreads) keep[k] = -1;
+  for (int P = (nb + kBlocksPerPage - 1) / kBlocksPerPage + gtid; P <= a.c.max_pages_per_seq; P += gthreads)
     rank[P] = count;
-  if (tid == 0) {
+  if (gtid == 0) {
     if (tail) tmp[count] = m_open;
     a.keep_count[i] = count;
     a.new_len[i] = count * kRatio + tail;
   }
-  if (!held) {
-    __syncthreads();  // the whole row has been read
-    for (int b = tid; b < left; b += kSelThreads) out[b] = tmp[b];
+  if constexpr (kCluster) {
+    __syncwarp();
+    cluster_wait();
   }
-  for (int b = left + tid; b < blocks; b += kSelThreads) out[b] = 0.f;
+  if (!held) {
+    sync_all();  // the whole row has been read
+    for (int b = gtid; b < left; b += gthreads) out[b] = tmp[b];
+  }
+  for (int b = left + gtid; b < blocks; b += gthreads) out[b] = 0.f;
 }
 
 __device__ __forceinline__ int ld_acquire(const int* p) {
@@ -450,6 +546,33 @@ int check_evict(const qsa_cache_t* cache, int32_t n, int32_t budget) {
   return QSA_OK;
 }
 
+template <bool kCluster>
+int launch_select(const EvictArgs& a, int ctas, int room, size_t smem, cudaStream_t s) {
+  if (cudaFuncSetAttribute(evict_select_kernel<kCluster>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxRoom * 4) !=
+      cudaSuccess) {
+    (void)cudaGetLastError();
+    return QSA_ERR_CUDA;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(a.n * ctas));
+  cfg.blockDim = dim3(kSelThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)ctas;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = kCluster ? 2 : 1;
+  if (cudaLaunchKernelEx(&cfg, evict_select_kernel<kCluster>, a, ctas, room) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return QSA_ERR_CUDA;
+  }
+  return QSA_OK;
+}
+
 template <int kRunBytes, int kWorkers>
 int launch_move(const EvictArgs& a, int units, int sms, cudaStream_t s) {
   constexpr int smem = MoveLay<kRunBytes, kWorkers>::kSmem;
@@ -523,18 +646,20 @@ extern "C" int qsa_evict(const qsa_cache_t* cache, const int32_t* dst_table, con
     return QSA_ERR_CUDA;
   }
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  // CTAs per entry: a cluster when its row may be long, as many as keep the call on
+  // about the card's SMs (the call on one row of 65,500 blocks: 54 us with 8, 168 with 1;
+  // on 8 of 10K blocks: 191, 198; on one of 1,040 blocks 14, 16)
   const int64_t blocks = (int64_t)c.max_pages_per_seq * kBlocksPerPage;
-  const int room = blocks < kMaxRoom ? (int)blocks : kMaxRoom;
-  if (cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxRoom * 4) !=
-      cudaSuccess) {
-    (void)cudaGetLastError();
-    return QSA_ERR_CUDA;
-  }
+  int ctas = 1;
+  while (blocks > 4096 && ctas < kMaxCluster && (int64_t)n * ctas * 2 <= 128) ctas *= 2;
+  const int64_t own = (blocks + (int64_t)ctas * kSelThreads - 1) / ((int64_t)ctas * kSelThreads) * kSelThreads;
+  const int room = own < kMaxRoom ? (int)own : kMaxRoom;
+  if ((int64_t)n * ctas > 0x7fffffff) return QSA_ERR_UNSUPPORTED;
   // More than half an SM's shared memory: one CTA per SM.  Launched early, behind a
   // kernel that fills the GPU, the CTAs would otherwise pile up on the first SMs to
   // come free (8 rows of 10K blocks, selection alone: 38 us instead of 24).
   const size_t smem = (size_t)(room * 4 > kOnePerSm ? room * 4 : kOnePerSm);
-  const int r = qsa_host::launch(evict_select_kernel, dim3((unsigned)n), dim3(kSelThreads), smem, s, a, room);
+  const int r = ctas > 1 ? launch_select<true>(a, ctas, room, smem, s) : launch_select<false>(a, 1, room, smem, s);
   if (r != QSA_OK) return r;
   return c.kv_dtype == QSA_KV_FP8_E4M3 ? launch_move<2048, 6>(a, (int)units, sms, s)
                                        : launch_move<4096, 3>(a, (int)units, sms, s);

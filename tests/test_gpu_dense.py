@@ -528,10 +528,27 @@ def test_evict_patterns_of_a_long_sequence_in_place(shape):
 
 @pytest.mark.parametrize("alias", [False, True])
 def test_evict_rows_too_long_for_shared_memory(alias):
-    """More than 49,152 blocks: masses are read again and pass through the workspace."""
-    grp = Group([198403, 500], 1, True, seed=13)
-    mass = masses(random.Random(5), (2, grp.cache.max_pages_per_seq * 16))
+    """More than 49,152 blocks a CTA: masses are read again and pass through the workspace (128 entries take a CTA each)."""
+    lens = [198403, 500] + [1] * 126
+    grp = Group(lens, 1, True, seed=13)
+    mass = masses(random.Random(5), (128, grp.cache.max_pages_per_seq * 16))
     check_evict(grp, 30000, 3, 100, mass, alias=alias)
+    grp = Group(lens[:2], 1, True, seed=13)          # and the same rows shared by clusters
+    check_evict(grp, 30000, 3, 100, mass[:2].clone(), alias=alias)
+
+
+@pytest.mark.parametrize("n", [1, 12, 20, 40, 70])
+def test_evict_clusters_of_each_size(n):
+    """Rows of a table that may be long: 8, 4, 2 CTAs share a row, or one takes it; short, empty and refused ones among them."""
+    rng = random.Random(n)
+    lens = [rng.choice([0, 3, 64, 900, 4097, 4 * rng.randint(1, 5000) + rng.randint(0, 3)]) for _ in range(n)]
+    lens[0] = 20003
+    grp = Group(lens, 1, True, seed=n, mpps=320)
+    mass = masses(rng, (n, 320 * 16))
+    ids = list(range(n)) + ([0, -1] if n > 1 else [])
+    refused = {n} if n > 1 else set()
+    check_evict(grp, 800, 5, 90, mass, ids=ids, lens=lens + ([4, 0] if n > 1 else []), refused=refused,
+                status=2 if n > 1 else 0, alias=bool(n % 8))
 
 
 @pytest.mark.parametrize("values", ["one", "two", "close", "nan", "inf", "wide"])
