@@ -1035,80 +1035,82 @@ __global__ void __launch_bounds__(kJoinThreads) dense_join_kernel(const __grid_c
     }
     return;
   }
-  // ---- weights.  The first query of a sequence adds up all of the sequence's
-  // queries in order, so the total does not depend on which block runs first.
+  // ---- weights.  The longest query of a sequence (the first of several) adds up all of
+  // the sequence's queries in order, so the total does not depend on which block runs
+  // first.  Its blocks take every mass_blocks-th 64 tiles.
   constexpr int kHeads = 8, kRound = 4 * kHeads;  // heads of a group and of the block at once
   const int64_t wb = blockIdx.x - n_join;
-  const int q0 = (int)(wb / ja.mass_blocks);
-  const int tile = (int)(wb % ja.mass_blocks) * 64 + (tid & 63), grp = tid >> 6;
-  const int seq = a.q_seq[q0];
-  if (query_len(a, q0, false) == 0) return;
+  const int q0 = (int)(wb / ja.mass_blocks), grp = tid >> 6;
+  const int seq = a.q_seq[q0], longest = query_len(a, q0, false);
   const int64_t max_tiles = (int64_t)a.mpps * kTilesPerPage;
   __shared__ unsigned same_s[kJoinThreads / 32];  // queries of this sequence, 256 at a time
-  float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-  int longest = 0;
-  for (int qb = 0; qb < a.nq; qb += kJoinThreads) {
-    const int qt = qb + tid;
-    const unsigned same = __ballot_sync(0xffffffffu, qt < a.nq && a.q_seq[qt] == seq && query_len(a, qt, false) > 0);
-    __syncthreads();
-    if (lane == 0) same_s[warp] = same;
-    __syncthreads();
-    for (int v = 0; v < kJoinThreads / 32; ++v)
-      for (unsigned bits = same_s[v]; bits; bits &= bits - 1) {
-        const int q = qb + v * 32 + __ffs(bits) - 1;
-        if (q < q0) return;  // not the first: the same in every thread
-        const int len = query_len(a, q, false);
-        const bool on = tile < (len + kTile - 1) / kTile;
-        longest = max(longest, len);
-        for (int h0 = 0; h0 < a.hq; h0 += kRound) {
-          float bm[kHeads];
-          float4 b[kHeads];
+  for (int t0 = (int)(wb % ja.mass_blocks) * 64; t0 < tiles_of(longest); t0 += ja.mass_blocks * 64) {
+    const int tile = t0 + (tid & 63);
+    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int qb = 0; qb < a.nq; qb += kJoinThreads) {
+      const int qt = qb + tid;
+      const unsigned same = __ballot_sync(0xffffffffu, qt < a.nq && a.q_seq[qt] == seq && query_len(a, qt, false) > 0);
+      __syncthreads();
+      if (lane == 0) same_s[warp] = same;
+      __syncthreads();
+      for (int v = 0; v < kJoinThreads / 32; ++v)
+        for (unsigned bits = same_s[v]; bits; bits &= bits - 1) {
+          const int q = qb + v * 32 + __ffs(bits) - 1;
+          const int len = query_len(a, q, false);
+          if (len > longest || (len == longest && q < q0)) return;  // the same in every thread
+          const bool on = tile < (len + kTile - 1) / kTile;
+          for (int h0 = 0; h0 < a.hq; h0 += kRound) {
+            float bm[kHeads];
+            float4 b[kHeads];
 #pragma unroll
-          for (int k = 0; k < kHeads; ++k) {  // head h0 + 4k + grp, requested before its lse is known
-            const int h = h0 + 4 * k + grp;
-            bm[k] = -INFINITY;
-            b[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (on && h < a.hq) {
-              const int64_t at = ((int64_t)q * a.hq + h) * max_tiles + tile;
-              bm[k] = a.bmax[at];
-              b[k] = reinterpret_cast<const float4*>(a.bsum)[at];
+            for (int k = 0; k < kHeads; ++k) {  // head h0 + 4k + grp, requested before its lse is known
+              const int h = h0 + 4 * k + grp;
+              bm[k] = -INFINITY;
+              b[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+              if (on && h < a.hq) {
+                const int64_t at = ((int64_t)q * a.hq + h) * max_tiles + tile;
+                bm[k] = a.bmax[at];
+                b[k] = reinterpret_cast<const float4*>(a.bsum)[at];
+              }
+            }
+            const int hl = h0 + (tid >> 3);
+            const float v2 = hl < a.hq ? joined_lse2(a, q, hl) : -INFINITY;
+            __syncthreads();
+            if ((tid & 7) == 0) lse_s[tid >> 3] = v2;
+            __syncthreads();
+#pragma unroll
+            for (int k = 0; k < kHeads; ++k) {
+              const float l2 = lse_s[4 * k + grp];
+              const float f = l2 == -INFINITY || bm[k] == -INFINITY ? 0.f : exp2f(bm[k] - l2);  // 0: no token seen
+              sum.x += f * b[k].x;
+              sum.y += f * b[k].y;
+              sum.z += f * b[k].z;
+              sum.w += f * b[k].w;
             }
           }
-          const int hl = h0 + (tid >> 3);
-          const float v2 = hl < a.hq ? joined_lse2(a, q, hl) : -INFINITY;
-          __syncthreads();
-          if ((tid & 7) == 0) lse_s[tid >> 3] = v2;
-          __syncthreads();
-#pragma unroll
-          for (int k = 0; k < kHeads; ++k) {
-            const float l2 = lse_s[4 * k + grp];
-            const float f = l2 == -INFINITY || bm[k] == -INFINITY ? 0.f : exp2f(bm[k] - l2);  // 0: no token seen
-            sum.x += f * b[k].x;
-            sum.y += f * b[k].y;
-            sum.z += f * b[k].z;
-            sum.w += f * b[k].w;
-          }
         }
+    }
+    acc_s[grp][tid & 63] = sum;
+    __syncthreads();
+    if (grp == 0) {
+#pragma unroll
+      for (int k = 1; k < 4; ++k) {
+        const float4 y = acc_s[k][tid];
+        sum.x += y.x;
+        sum.y += y.y;
+        sum.z += y.z;
+        sum.w += y.w;
       }
-  }
-  acc_s[grp][tid & 63] = sum;
-  __syncthreads();
-  if (grp) return;
+      const int blocks = (longest + kRatio - 1) / kRatio;
+      const float v[4] = {sum.x, sum.y, sum.z, sum.w};
+      const int64_t row = (int64_t)seq * ja.mass_ld;
 #pragma unroll
-  for (int k = 1; k < 4; ++k) {
-    const float4 y = acc_s[k][tid];
-    sum.x += y.x;
-    sum.y += y.y;
-    sum.z += y.z;
-    sum.w += y.w;
-  }
-  const int blocks = (longest + kRatio - 1) / kRatio;
-  const float v[4] = {sum.x, sum.y, sum.z, sum.w};
-  const int64_t row = (int64_t)seq * ja.mass_ld;
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const int b = tile * kTileRuns + k;
-    if (b < blocks) ja.mass_out[row + b] = ja.decay * ja.mass_in[row + b] + v[k];
+      for (int k = 0; k < 4; ++k) {
+        const int b = tile * kTileRuns + k;
+        if (b < blocks) ja.mass_out[row + b] = ja.decay * ja.mass_in[row + b] + v[k];
+      }
+    }
+    __syncthreads();  // acc_s is used again
   }
 }
 
@@ -1240,7 +1242,10 @@ extern "C" int qsa_dense_decode(const qsa_cache_t* cache, const void* q, int32_t
   j.mass_ld = mass_ld;
   j.decay = decay;
   const int64_t tiles = (int64_t)c.max_pages_per_seq * kTilesPerPage;
-  j.mass_blocks = (int32_t)((tiles + 63) / 64);
+  // 64 tiles a block while that makes no more than about 8 blocks per SM; the lengths may
+  // be far below the table's capacity, and a block that finds nothing costs about 1 us
+  const int64_t most = (tiles + 63) / 64, fit = (8 * (int64_t)a.ctas + nq - 1) / nq;
+  j.mass_blocks = (int32_t)(most < fit ? most : fit);
   // About 8 CTAs per SM, a head each at most.  Of a large batch's pairs many need no join:
   // a CTA per head, to find that out, took 2.2 us more for 161 queries of 24 heads, and one
   // CTA for all 12 heads of a split pair 4.5 us more.
