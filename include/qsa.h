@@ -476,8 +476,9 @@ QSA_API int qsa_rope(const qsa_rope_plan_t* plan, const qsa_rope_tensor_t* tenso
  *   mass_in, mass_out fp32 [max_seqs][mass_ld] (both or neither), mass_ld >=
  *   max_pages_per_seq * 16
  *   workspace  256-byte aligned, at least qsa_dense_decode_workspace_bytes (its
- *              contents need no preparation); calls that share one must not
- *              overlap on the GPU, captured graphs included
+ *              contents need no preparation): at most 8.5 MB, and with totals
+ *              nq * hq * max_pages_per_seq * 80 bytes more; calls that share
+ *              one must not overlap on the GPU, captured graphs included
  * A query with q_seq < 0 (padding) or q_pos == -1 (no tokens) gets out = 0 and
  * lse = -inf; so does, flagged, one whose sequence or position is out of range.
  * The 64 tokens of a page-table miss are left out and flagged; a query left
@@ -522,8 +523,8 @@ QSA_API int qsa_dense_decode(const qsa_cache_t* cache, const void* q, int32_t nq
  * (QSA_DEV_BAD_SEQ) or with a length out of range (QSA_DEV_BAD_POS) is refused:
  * nothing of it moves, keep_count = 0, new_len = seq_len.  A block whose page
  * is a table miss is lost (QSA_DEV_BAD_PAGE).  Requirements: 1 <= budget <=
- * max_pages_per_seq * 16, sink + recent <= budget, mass_ld >=
- * max_pages_per_seq * 16.
+ * 2^30 (one beyond the table's blocks keeps all), sink + recent <= budget,
+ * mass_ld >= max_pages_per_seq * 16.
  */
 QSA_API int64_t qsa_evict_workspace_bytes(const qsa_cache_t* cache, int32_t n, int32_t budget);
 QSA_API int qsa_evict(const qsa_cache_t* cache, const int32_t* dst_table, const int32_t* seq_ids, const int32_t* seq_len,

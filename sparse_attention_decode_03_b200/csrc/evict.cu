@@ -433,6 +433,8 @@ __global__ void __launch_bounds__(kWorkers * 32) evict_move_kernel(EvictArgs a, 
     const int total = count + (len % kRatio ? 1 : 0);
     u.in_place = dp == own;
     u.any = u.page * kBlocksPerPage < total;
+    // pages behind the last kept block: the entry's other tickets hold nothing either
+    if (!u.any && lane == 0) atomicMax(a.ticket, (i + 1) * hkv * a.pages);
     u.p0 = k0 / kBlocksPerPage;
     u.p1 = k1 > k0 && dp == own ? min(u.page - 1, (k1 - 1) / kBlocksPerPage) : -1;
     if (lane < kBlocksPerPage && k < total) {
@@ -542,7 +544,7 @@ int check_evict(const qsa_cache_t* cache, int32_t n, int32_t budget) {
   if (c.num_pages < 1 || c.max_seqs < 1 || c.max_pages_per_seq < 1 || c.num_kv_heads < 1) return QSA_ERR_INVALID_ARG;
   if (c.max_pages_per_seq > 0x7fffffff / kPage || c.num_pages > 0x7fffffff / kBlocksPerPage)
     return QSA_ERR_UNSUPPORTED;  // positions and page * 16 + slot are int32
-  if ((int64_t)budget > (int64_t)c.max_pages_per_seq * kBlocksPerPage) return QSA_ERR_INVALID_ARG;
+  if (budget > 1 << 30) return QSA_ERR_UNSUPPORTED;
   return QSA_OK;
 }
 

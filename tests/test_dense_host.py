@@ -73,7 +73,7 @@ def test_evict_refuses_bad_arguments_before_any_cuda_call():
 
     assert call(n=0) == 0
     assert call(cache=None) == -1 and call(n=-1) == -1
-    assert call(budget=0) == -1 and call(budget=65) == -1               # the table holds 64 blocks
+    assert call(budget=0) == -1 and call(budget=(1 << 30) + 1) == -2
     assert call(sink=-1) == -1 and call(recent=-1) == -1
     assert call(sink=10, recent=7) == -1
     assert call(sink=0x7fffffff, recent=0x7fffffff) == -1

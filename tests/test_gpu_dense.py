@@ -511,6 +511,7 @@ def test_evict_whole_budget_and_full_table():
     grp = Group([256, 255, 130], 1, seed=1, mpps=4)
     mass = masses(random.Random(1), (3, 64))
     check_evict(grp, 64, 10, 10, mass)           # the budget is the table: everything stays
+    check_evict(grp, 100, 10, 10, mass)          # or beyond it
     check_evict(grp, 63, 0, 0, mass)
 
 
