@@ -52,7 +52,10 @@ constexpr int kTile = 16;                        // tokens of one matrix product
 constexpr int kTileRuns = kTile / kRatio;        // 4 micro-blocks
 constexpr int kTilesPerPage = kPage / kTile;
 constexpr int kPieceCost = 8;                    // what a pair costs a CTA beside its tiles, in tiles
-constexpr int kMinPlaces = 8;                    // places a CTA takes at least
+// Places a CTA takes at least, so that one short sequence is not cut into pieces whose
+// join costs more than they save; with more pairs than that a CTA may hold one pair alone
+// (167 queries of 1 to 4 tokens, 12/1 heads, e4m3: 15.4 us at 8 places a CTA, 10.7 so).
+constexpr int kMinPlaces = 8;
 constexpr int kMaxCtas = 256;                    // partial slots reserved: 2 per CTA
 constexpr int kQStride = kHeadDim * 2 + 16;      // Q rows 528 B apart: conflict-free 16-byte fragment reads
 constexpr int kSlice = 32;                       // dims of O that the warps join at once
@@ -151,9 +154,9 @@ __device__ __forceinline__ int tiles_of(int len) {
 struct Shares {
   int n, base, rem;  // CTAs; the first `rem` take base + 1 places, the others base
 };
-__device__ __forceinline__ Shares make_shares(int total, int ctas) {
+__device__ __forceinline__ Shares make_shares(int total, int pairs, int ctas) {
   Shares s;
-  s.n = min(ctas, max(1, (total + kMinPlaces - 1) / kMinPlaces));
+  s.n = min(ctas, max(pairs, (total + kMinPlaces - 1) / kMinPlaces));
   s.base = total / s.n;
   s.rem = total - s.base * s.n;
   return s;
@@ -829,7 +832,7 @@ __global__ void __launch_bounds__(Lay<F8>::kThreads, 1) dense_decode_kernel(cons
   // one round (the usual batch) the lengths are loaded once and kept.
   const bool one_round = a.nq <= kThreads;
   const bool whole_tab = a.nq <= kTab;
-  int total = 0, first = 0, len = 0;
+  int total = 0, first = 0, len = 0, filled = 0;  // filled: queries that see tokens
   auto scan_round = [&](int base, bool report) {  // places before query base + tid; total moves on
     const int q = base + tid;
     len = q < a.nq ? query_len(a, q, report) : 0;
@@ -842,7 +845,7 @@ __global__ void __launch_bounds__(Lay<F8>::kThreads, 1) dense_decode_kernel(cons
     }
     if (lane == 31) plan[4 + warp] = inc;
     if (whole_tab && q < a.nq) tab[q] = make_int2(len, a.q_seq[q]);
-    __syncthreads();
+    filled += __syncthreads_count(len > 0);
     first = total + inc - n;
 #pragma unroll
     for (int v = 0; v < kThreads / 32; ++v) {
@@ -858,7 +861,7 @@ __global__ void __launch_bounds__(Lay<F8>::kThreads, 1) dense_decode_kernel(cons
       for (int g = 0; g < a.hkv; ++g) a.span[(b + tid) * a.hkv + g] = make_int2(0, -1);
   }
   if (total == 0) return;
-  const Shares sh = make_shares(total, a.ctas);
+  const Shares sh = make_shares(total, filled * a.hkv, a.ctas);
   if ((int)blockIdx.x >= sh.n) return;
   const int x0 = share_begin(sh, blockIdx.x), x1 = share_begin(sh, blockIdx.x + 1);
   auto find_first = [&](int base) {  // the query that holds place x0
@@ -943,9 +946,13 @@ __device__ __forceinline__ float joined_lse2(const DenseArgs& a, int q, int h) {
 }
 
 // The first blocks: `parts` of them a (query, KV head) pair, for every parts-th head
-// each; the pieces of a head are spread over 4 groups of 64 threads (4 dims each) and summed in a fixed order.  The blocks
-// after them add up weights: 64 tiles (256 micro-blocks) of one query's sequence
-// each, the heads spread over the 4 groups.
+// each; the pieces of a head are spread over 4 groups of 64 threads (4 dims each) and
+// summed in a fixed order.  The blocks after them add up weights: 64 tiles (256
+// micro-blocks) of one query's sequence each, the heads spread over the 4 groups.
+// Its time is the latency of three dependent loads (span, pieces' lse, rows), so a
+// block takes few heads and the rows are requested first: 3 us of the 12 us at 1 x 4,096
+// tokens.  512 threads a block gained 1.4 us at 2 sequences of 2K and 44K tokens and lost
+// 4 us at 125 of 300 to 900.
 __global__ void __launch_bounds__(kJoinThreads) dense_join_kernel(const __grid_constant__ JoinArgs ja) {
   const DenseArgs& a = ja.d;
   pdl_launch_dependents();

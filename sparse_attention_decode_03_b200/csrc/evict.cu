@@ -11,13 +11,16 @@
 //
 // evict_select_kernel, a CTA per sequence or a cluster of up to 8: radix select of the
 // cut (11 + 11 + 10 bits of the order-preserving key) over masses held in shared
-// memory, histograms summed over the cluster's shared memory, then one ordered pass that writes the kept indices, the number kept before every page,
-// and the moved mass row.
+// memory, histograms summed over the cluster's shared memory, then one ordered pass
+// that writes the kept indices, the number kept before every page, and the moved mass
+// row.  Bound by the latency of its passes: 6 us for 4K tokens; a call that cuts one
+// sequence of 262,144 tokens to 1,024 blocks took 168 us with one CTA, 53 with a cluster.
 //
 // evict_move_kernel: units of one destination page and KV head (16 runs, 64 KiB
-// BF16) are claimed by warps, three to a CTA and one CTA per SM, each with a
-// buffer of its own in shared memory; lane b moves block b with bulk copies.
-// What bounds it is the traffic: each kept run is read once and written once.
+// BF16) are claimed by warps, one CTA per SM, each warp with a buffer of its own in
+// shared memory: 3 of them BF16, 6 e4m3 (as many as fit; one alone left its SM idle while
+// it wrote), 2 where there are too few units for more; lane b moves block b with bulk
+// copies.  What bounds it is the traffic: each kept run is read once and written once.
 // The move is in place (or into other pages), so a page may be written only when
 // the blocks it held have been read.  Kept blocks move towards lower indices
 // only; hence page c's old blocks go to pages <= c, and a warp that has read its
@@ -25,6 +28,11 @@
 // blocks out of page c have been read as well.  Units are claimed by ticket,
 // lower pages first, and read before they wait, so the lowest unit at work
 // never waits and every wait ends.
+//
+// Measured on one B200 (time of the call, share of the 6.54 TB/s copy rate):
+//   8 x 33K-50K tokens to 8,192 blocks, 2 heads      191 us   89%; in place 12 to 22% more
+//   48 x 4.3K-4.9K tokens to 1,024 blocks, 1 head     86 us   76%; 10 us of it selection
+//   1 x 4,163 tokens to 1,024 blocks, 2 heads         13 us   of it 6 selection, 6 moves
 #include "qsa_common.cuh"
 
 namespace {

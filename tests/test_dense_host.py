@@ -171,8 +171,8 @@ def test_rope_plan():
 PIECE_COST, MIN_PLACES = 8, 8
 
 
-def shares(T, ctas):
-    n = min(ctas, max(1, -(-T // MIN_PLACES)))
+def shares(T, pairs, ctas):
+    n = min(ctas, max(pairs, -(-T // MIN_PLACES)))
     base, rem = divmod(T, n)
     return n, [c * base + min(c, rem) for c in range(n + 1)], base, rem
 
@@ -198,7 +198,7 @@ def test_shares_cover_every_tile_once_and_partials_have_slots_of_their_own(seed)
     if T == 0:
         return
     ctas = rng.choice([1, 3, 148, 256])
-    n, start, base, rem = shares(T, ctas)
+    n, start, base, rem = shares(T, len(pairs), ctas)
     assert start[0] == 0 and start[n] == T and all(a < b for a, b in zip(start, start[1:]))
     for x in range(0, T, max(1, T // 500)):
         c = share_of(base, rem, x)
