@@ -36,7 +36,7 @@
 //   e4m3, 64 x 16K-262K tokens, 12/1 heads      455 us    92%; power-capped at 1.7 GHz,
 //                                                         ALU 39%, tensor 34% of cycles
 //   BF16, 16 x 9K-16K tokens, 24/2, with totals   75 us    82%
-//   BF16, 1 x 4,096 tokens, 16/2                 12 us    of it 8 main kernel, 3 join
+//   BF16, 1 x 4,096 tokens, 16/2                 10 us    of it 7 main kernel, 3 join
 //   BF16, 200 x 1-700 tokens, 3/1                15 us
 // What did not pay for e4m3: 6 or 7 consumers (512, 526 us then), 32-token tiles
 // (no change), one tile's products beside the last one's values (508 against 494),
@@ -53,9 +53,10 @@ constexpr int kTileRuns = kTile / kRatio;        // 4 micro-blocks
 constexpr int kTilesPerPage = kPage / kTile;
 constexpr int kPieceCost = 8;                    // what a pair costs a CTA beside its tiles, in tiles
 // Places a CTA takes at least, so that one short sequence is not cut into pieces whose
-// join costs more than they save; with more pairs than that a CTA may hold one pair alone
-// (167 queries of 1 to 4 tokens, 12/1 heads, e4m3: 15.4 us at 8 places a CTA, 10.7 so).
-constexpr int kMinPlaces = 8;
+// join costs more than they save (1 x 4,096 tokens, 16/2 heads: 10.1 us with 4, 10.2 with
+// 6, 11.3 with 8); with more pairs than that a CTA may hold one pair alone (167 queries
+// of 1 to 4 tokens, 12/1 heads, e4m3: 10.3 us, 15.4 without this).
+constexpr int kMinPlaces = 4;
 constexpr int kMaxCtas = 256;                    // partial slots reserved: 2 per CTA
 constexpr int kQStride = kHeadDim * 2 + 16;      // Q rows 528 B apart: conflict-free 16-byte fragment reads
 constexpr int kSlice = 32;                       // dims of O that the warps join at once
@@ -910,6 +911,7 @@ __global__ void __launch_bounds__(Lay<F8>::kThreads, 1) dense_decode_kernel(cons
 // ------------------------------------------------------------------ join + weights
 
 constexpr int kJoinThreads = 256;
+constexpr int kFewPieces = 8;  // pieces of a head that 64 threads join alone
 
 struct JoinArgs {
   DenseArgs d;
@@ -918,7 +920,8 @@ struct JoinArgs {
   int64_t mass_ld;
   float decay;
   int32_t mass_blocks;  // CTAs per query for the weights
-  int32_t parts;        // CTAs per pair for the join, a share of its heads each
+  int32_t parts;        // CTAs per pair for the join
+  int32_t slice_bits;   // the dims of a head of many pieces are shared by 1, 2 or 4 blocks
 };
 
 // The partial slot of CTA c's piece of a pair that spans several CTAs.
@@ -945,99 +948,133 @@ __device__ __forceinline__ float joined_lse2(const DenseArgs& a, int q, int h) {
   return M + log2f(L);
 }
 
-// The first blocks: `parts` of them a (query, KV head) pair, for every parts-th head
-// each; the pieces of a head are spread over 4 groups of 64 threads (4 dims each) and
-// summed in a fixed order.  The blocks after them add up weights: 64 tiles (256
-// micro-blocks) of one query's sequence each, the heads spread over the 4 groups.
-// Its time is the latency of three dependent loads (span, pieces' lse, rows), so a
-// block takes few heads and the rows are requested first: 3 us of the 12 us at 1 x 4,096
-// tokens.  512 threads a block gained 1.4 us at 2 sequences of 2K and 44K tokens and lost
-// 4 us at 125 of 300 to 900.
+// The first blocks: `parts` of them a (query, KV head) pair.  The blocks after them add
+// up weights: 64 tiles (256 micro-blocks) of one query's sequence each, the heads spread
+// over 4 groups of 64 threads.
+// The join's time is the latency of two dependent loads (span; pieces' lse and rows
+// together), so it asks for all rows at once and waits as seldom as it can: up to 8
+// pieces a head, 64 threads join one with no exchange (the call on 125 pairs of 12 heads, 2
+// pieces each: 24.4 us with a block a head, 22.7 so); more pieces are spread over the block,
+// and few heads over 2 or 4 blocks each, by their dims (the call on 2 sequences of 2K and
+// 44K tokens, 12/1 heads: 22.0 us unsplit, 18.6 so).  Sums run in a fixed order.
 __global__ void __launch_bounds__(kJoinThreads) dense_join_kernel(const __grid_constant__ JoinArgs ja) {
   const DenseArgs& a = ja.d;
   pdl_launch_dependents();
   pdl_wait_previous();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  __shared__ float4 acc_s[4][64];
+  __shared__ float4 acc_s[kJoinThreads];
   __shared__ float lse_s[kMaxCtas];  // pieces' lse, then their weights (kMaxCtas <= kJoinThreads: one each)
   __shared__ float red_s[2][kJoinThreads / 32];
   static_assert(kMaxCtas <= kJoinThreads, "a thread per piece");
   const int n_join = a.nq * a.hkv * ja.parts;
   if ((int)blockIdx.x < n_join) {
-    const int pair = blockIdx.x / ja.parts;
+    const int pair = blockIdx.x / ja.parts, part = blockIdx.x % ja.parts;
     const int2 p = a.span[pair];
     if (p.x == p.y) return;  // written by its CTA
-    for (int row = blockIdx.x % ja.parts; row < a.G; row += ja.parts) {
-      const int64_t qh = (int64_t)pair * a.G + row;
-      __syncthreads();  // the last head's use of the shared arrays has ended
-      const int grp = tid >> 6, c4 = tid & 63;
-      uint2 o = make_uint2(0, 0);
-      float lse = -INFINITY;
-      const int n = p.y - p.x + 1;
-      if (n > 1) {
-        // rows: requested before their weights are known
-        const float4* base = reinterpret_cast<const float4*>(a.part_o + (size_t)row * kHeadDim) + c4;
-        const size_t step = (size_t)a.G * (kHeadDim / 4);
-        constexpr int kAhead = 4;
-        float4 x[kAhead];
+    const int n = max(0, p.y - p.x + 1);
+    const float4* rows = reinterpret_cast<const float4*>(a.part_o);
+    // of a head: weights relative to 2^M, their sum, the rows they weigh
+    auto put = [&](int row, int c4, float M, float L, float4 r) {
+      const size_t qh = (size_t)pair * a.G + row;
+      const float inv = L == 0.f ? 0.f : 1.f / L;  // 0: no token; a NaN stays one
+      reinterpret_cast<uint2*>(a.out + qh * kHeadDim)[c4] =
+          make_uint2(pack_bf16(r.x * inv, r.y * inv), pack_bf16(r.z * inv, r.w * inv));
+      if (c4 == 0) a.lse[qh] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994530942f;
+    };
+    auto weight = [](float v, float M) { return v == -INFINITY ? 0.f : exp2f(v - M); };  // 0: an empty piece
+    if (n <= kFewPieces) {  // 64 threads a head, nothing shared
+      const int c4 = tid & 63;
+      for (int row = (tid >> 6) * ja.parts + part; row < a.G; row += ja.parts * 4) {
+        float4 x[kFewPieces];
+        float v[kFewPieces];
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k)
-          if (grp + 4 * k < n) x[k] = base[slot_of(p, p.x + grp + 4 * k) * step];
-        float v = tid < n ? a.part_lse[(size_t)slot_of(p, p.x + tid) * a.G + row] : -INFINITY;
-        float M = v;
-#pragma unroll
-        for (int d = 16; d; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
-        if (lane == 0) red_s[0][warp] = M;
-        __syncthreads();
-#pragma unroll
-        for (int k = 0; k < kJoinThreads / 32; ++k) M = fmaxf(M, red_s[0][k]);
-        float e = M == -INFINITY ? 0.f : exp2f(v - M);  // 0 for an empty piece, whose row is zero
-        if (tid < n) lse_s[tid] = e;
-#pragma unroll
-        for (int d = 16; d; d >>= 1) e += __shfl_xor_sync(0xffffffffu, e, d);
-        if (lane == 0) red_s[1][warp] = e;
-        __syncthreads();
-        float L = 0.f;
-#pragma unroll
-        for (int k = 0; k < kJoinThreads / 32; ++k) L += red_s[1][k];
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int i0 = grp; i0 < n; i0 += 4 * kAhead) {
-#pragma unroll
-          for (int k = 0; k < kAhead; ++k) {
-            const int i = i0 + 4 * k;
-            if (i >= n) break;
-            const float f = lse_s[i];
-            acc.x += f * x[k].x;
-            acc.y += f * x[k].y;
-            acc.z += f * x[k].z;
-            acc.w += f * x[k].w;
-          }
-#pragma unroll
-          for (int k = 0; k < kAhead; ++k) {
-            const int i = i0 + 4 * kAhead + 4 * k;
-            if (i < n) x[k] = base[slot_of(p, p.x + i) * step];
+        for (int k = 0; k < kFewPieces; ++k) {
+          v[k] = -INFINITY;
+          x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (k < n) {
+            const size_t at = (size_t)slot_of(p, p.x + k) * a.G + row;
+            v[k] = a.part_lse[at];
+            x[k] = rows[at * (kHeadDim / 4) + c4];
           }
         }
-        acc_s[grp][c4] = acc;
-        __syncthreads();
-        if (grp == 0 && M != -INFINITY) {
-          const float inv = 1.f / L;
-          float4 r = acc_s[0][c4];
+        float M = v[0], L = 0.f;
 #pragma unroll
-          for (int k = 1; k < 4; ++k) {
-            r.x += acc_s[k][c4].x;
-            r.y += acc_s[k][c4].y;
-            r.z += acc_s[k][c4].z;
-            r.w += acc_s[k][c4].w;
-          }
-          o.x = pack_bf16(r.x * inv, r.y * inv);
-          o.y = pack_bf16(r.z * inv, r.w * inv);
-          lse = (M + log2f(L)) * 0.69314718055994530942f;
+        for (int k = 1; k < kFewPieces; ++k) M = fmaxf(M, v[k]);
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int k = 0; k < kFewPieces; ++k) {
+          const float f = weight(v[k], M);
+          L += f;
+          acc.x += f * x[k].x;
+          acc.y += f * x[k].y;
+          acc.z += f * x[k].z;
+          acc.w += f * x[k].w;
+        }
+        put(row, c4, M, L, acc);
+      }
+      return;
+    }
+    // many pieces: the block takes a slice of a head's dims, groups of threads share the pieces
+    const int bits = ja.slice_bits, cols = 64 >> bits, groups = 4 << bits;
+    const int grp = tid >> (6 - bits), col = tid & (cols - 1);
+    for (int item = part; item < a.G << bits; item += ja.parts) {
+      const int row = item >> bits, c4 = (item & ((1 << bits) - 1)) * cols + col;
+      __syncthreads();  // the last item's use of the shared arrays has ended
+      // rows: requested before their weights are known
+      const float4* base = rows + (size_t)row * (kHeadDim / 4) + c4;
+      const size_t step = (size_t)a.G * (kHeadDim / 4);
+      constexpr int kAhead = 4;
+      float4 x[kAhead];
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k)
+        if (grp + groups * k < n) x[k] = base[slot_of(p, p.x + grp + groups * k) * step];
+      const float v = tid < n ? a.part_lse[(size_t)slot_of(p, p.x + tid) * a.G + row] : -INFINITY;
+      float M = v;
+#pragma unroll
+      for (int d = 16; d; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+      if (lane == 0) red_s[0][warp] = M;
+      __syncthreads();
+#pragma unroll
+      for (int k = 0; k < kJoinThreads / 32; ++k) M = fmaxf(M, red_s[0][k]);
+      float e = weight(v, M);
+      if (tid < n) lse_s[tid] = e;
+#pragma unroll
+      for (int d = 16; d; d >>= 1) e += __shfl_xor_sync(0xffffffffu, e, d);
+      if (lane == 0) red_s[1][warp] = e;
+      __syncthreads();
+      float L = 0.f;
+#pragma unroll
+      for (int k = 0; k < kJoinThreads / 32; ++k) L += red_s[1][k];
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int i0 = grp; i0 < n; i0 += groups * kAhead) {
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+          const int i = i0 + groups * k;
+          if (i >= n) break;
+          const float f = lse_s[i];
+          acc.x += f * x[k].x;
+          acc.y += f * x[k].y;
+          acc.z += f * x[k].z;
+          acc.w += f * x[k].w;
+        }
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+          const int i = i0 + groups * (kAhead + k);
+          if (i < n) x[k] = base[slot_of(p, p.x + i) * step];
         }
       }
+      acc_s[tid] = acc;
+      __syncthreads();
       if (grp == 0) {
-        reinterpret_cast<uint2*>(a.out + (size_t)qh * kHeadDim)[c4] = o;
-        if (c4 == 0) a.lse[qh] = lse;
+#pragma unroll 4
+        for (int k = 1; k < groups; ++k) {
+          const float4 y = acc_s[k * cols + col];
+          acc.x += y.x;
+          acc.y += y.y;
+          acc.z += y.z;
+          acc.w += y.w;
+        }
+        put(row, c4, M, L, acc);
       }
     }
     return;
@@ -1048,12 +1085,21 @@ __global__ void __launch_bounds__(kJoinThreads) dense_join_kernel(const __grid_c
   constexpr int kHeads = 8, kRound = 4 * kHeads;  // heads of a group and of the block at once
   const int64_t wb = blockIdx.x - n_join;
   const int q0 = (int)(wb / ja.mass_blocks), grp = tid >> 6;
+  float4(*sum_s)[64] = reinterpret_cast<float4(*)[64]>(&acc_s[0]);
   const int seq = a.q_seq[q0], longest = query_len(a, q0, false);
   const int64_t max_tiles = (int64_t)a.mpps * kTilesPerPage;
   __shared__ unsigned same_s[kJoinThreads / 32];  // queries of this sequence, 256 at a time
   for (int t0 = (int)(wb % ja.mass_blocks) * 64; t0 < tiles_of(longest); t0 += ja.mass_blocks * 64) {
     const int tile = t0 + (tid & 63);
     float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+    const int blocks = (longest + kRatio - 1) / kRatio;
+    const int64_t row = (int64_t)seq * ja.mass_ld;
+    float old[4] = {};  // requested before anything else is waited for
+    if (grp == 0) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (tile * kTileRuns + k < blocks) old[k] = ja.mass_in[row + tile * kTileRuns + k];
+    }
     for (int qb = 0; qb < a.nq; qb += kJoinThreads) {
       const int qt = qb + tid;
       const unsigned same = __ballot_sync(0xffffffffu, qt < a.nq && a.q_seq[qt] == seq && query_len(a, qt, false) > 0);
@@ -1097,27 +1143,25 @@ __global__ void __launch_bounds__(kJoinThreads) dense_join_kernel(const __grid_c
           }
         }
     }
-    acc_s[grp][tid & 63] = sum;
+    sum_s[grp][tid & 63] = sum;
     __syncthreads();
     if (grp == 0) {
 #pragma unroll
       for (int k = 1; k < 4; ++k) {
-        const float4 y = acc_s[k][tid];
+        const float4 y = sum_s[k][tid];
         sum.x += y.x;
         sum.y += y.y;
         sum.z += y.z;
         sum.w += y.w;
       }
-      const int blocks = (longest + kRatio - 1) / kRatio;
       const float v[4] = {sum.x, sum.y, sum.z, sum.w};
-      const int64_t row = (int64_t)seq * ja.mass_ld;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const int b = tile * kTileRuns + k;
-        if (b < blocks) ja.mass_out[row + b] = ja.decay * ja.mass_in[row + b] + v[k];
+        if (b < blocks) ja.mass_out[row + b] = ja.decay * old[k] + v[k];
       }
     }
-    __syncthreads();  // acc_s is used again
+    __syncthreads();  // sum_s is used again
   }
 }
 
@@ -1253,11 +1297,13 @@ extern "C" int qsa_dense_decode(const qsa_cache_t* cache, const void* q, int32_t
   // be far below the table's capacity, and a block that finds nothing costs about 1 us
   const int64_t most = (tiles + 63) / 64, fit = (8 * (int64_t)a.ctas + nq - 1) / nq;
   j.mass_blocks = (int32_t)(most < fit ? most : fit);
-  // About 8 CTAs per SM, a head each at most.  Of a large batch's pairs many need no join:
-  // a CTA per head, to find that out, took 2.2 us more for 161 queries of 24 heads, and one
-  // CTA for all 12 heads of a split pair 4.5 us more.
-  const int64_t pairs = (int64_t)nq * c.num_kv_heads, want = (8 * a.ctas + pairs - 1) / pairs;
-  j.parts = (int32_t)(want < a.G ? want : a.G);
+  // About 4 CTAs per SM, as many as are resident at once (8: 125 queries with totals 26.1
+  // us instead of 25.0); the dims split only while that leaves 2 per SM (8 x 32,768 tokens,
+  // 128 heads: 85.0 us split in two, 86.0 in four)
+  const int64_t pairs = (int64_t)nq * c.num_kv_heads, want = (4 * a.ctas + pairs - 1) / pairs;
+  j.slice_bits = pairs * a.G * 4 <= 2 * a.ctas ? 2 : pairs * a.G * 2 <= 2 * a.ctas ? 1 : 0;
+  const int64_t items = (int64_t)a.G << j.slice_bits;
+  j.parts = (int32_t)(want < items ? want : items);
   const int64_t grid = pairs * j.parts + (mass ? (int64_t)nq * j.mass_blocks : 0);
   if (grid > 0x7fffffff) return QSA_ERR_UNSUPPORTED;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);

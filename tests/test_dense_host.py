@@ -168,7 +168,7 @@ def test_rope_plan():
 # ---------------------------------------------------------------- index arithmetic, restated
 
 
-PIECE_COST, MIN_PLACES = 8, 8
+PIECE_COST, MIN_PLACES = 8, 4
 
 
 def shares(T, pairs, ctas):
