@@ -14,7 +14,7 @@
 // The chunks that turn (R / 8 of a row) and those that are only copied go to
 // different warps: with R = 64 of 256 dims a warp turns 4 rows at once instead of
 // one with three quarters of its lanes idle, which took 139 instructions a row
-// and 55 us for 8,192 tokens of 24 + 2 heads and an indexer's (now 48 us, 5.3 TB/s).  A half-split pair's partner chunk comes by
+// and 55 us for 8,192 tokens of 24 + 2 heads and an indexer's (now 45 us, 5.7 TB/s).  A half-split pair's partner chunk comes by
 // shuffle.  The chunks of all its tokens are requested together, before the angles
 // are computed: each CTA computes its tokens' R/2 sines and cosines once, for all
 // heads.  Few tokens spread their rows over more CTAs instead.
@@ -24,8 +24,8 @@ namespace {
 
 using namespace qsa;
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
+constexpr int kWarps = 8;      // of a CTA; kWideWarps for long calls
+constexpr int kWideWarps = 16;
 constexpr int kTokens = 4;  // tokens of a CTA at most; a warp requests its chunks of all of them together
 constexpr int kMaxPairs = QSA_ROPE_MAX_PAIRS;
 
@@ -103,17 +103,17 @@ __device__ __forceinline__ Piece find_piece(const RopeArgs& a, int item, int lan
   return p;
 }
 
-template <bool kAdjacent>
-__global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeArgs a) {
+template <bool kAdjacent, int kW>
+__global__ void __launch_bounds__(kW * 32) rope_kernel(const __grid_constant__ RopeArgs a) {
   __shared__ __align__(16) float2 cs[kTokens][kMaxPairs];  // cos, sin
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int half = a.plan.rot_dim / 2;
   const int64_t tok0 = (int64_t)blockIdx.x * a.tokens;
   const int ntok = (int)min((int64_t)a.tokens, a.n - tok0);
-  const int step = gridDim.y * kWarps;
+  const int step = gridDim.y * kW;
   pdl_wait_previous();
   bool angles = false;
-  for (int item = blockIdx.y * kWarps + warp; item < a.items || !angles; item += step) {
+  for (int item = blockIdx.y * kW + warp; item < a.items || !angles; item += step) {
     const bool has = item < a.items;
     Piece p = {};
     if (has) p = find_piece(a, item, lane);
@@ -125,7 +125,7 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
       if (p.live && u < ntok) v[u] = ld_row(src + u * p.in_stride);
     }
     if (!angles) {  // every warp once, with its first rows on their way
-      for (int k = tid; k < ntok * half; k += kThreads) {
+      for (int k = tid; k < ntok * half; k += kW * 32) {
         const int i = k % half, t = k / half;
         double turn = (double)a.pos[a.plan.axis[i] * a.pos_stride + tok0 + t] * a.plan.freq[i] *
                       0.15915494309189533577;  // 1 / 2 pi
@@ -242,15 +242,23 @@ extern "C" int qsa_rope(const qsa_rope_plan_t* plan, const qsa_rope_tensor_t* te
   }
   // 4 tokens a CTA when that still fills the GPU (148 SMs x 5 CTAs), else fewer; then rows
   // spread over grid.y until there are about as many CTAs, a piece per warp at least
-  // (8,192 tokens: 4 of them 48 us, 2: 50, 8: 50; 57 tokens: 2.5 us, unspread 3.8)
+  // (8,192 tokens: 4 of them 45 us, 2: 56, 8: 47; 57 tokens: 2.5 us, unspread 3.8)
   constexpr int kFill = 1024;
   a.tokens = n >= 4 * kFill ? 4 : n >= 2 * kFill ? 2 : 1;
   const int64_t gx = ((int64_t)n + a.tokens - 1) / a.tokens;
-  const int rounds = (a.items + kWarps - 1) / kWarps;
+  // 16 warps a CTA where a token has work for them (8,192 tokens of 24 + 2 heads and an
+  // indexer's: 45.1 us, with 8 warps 48.0, with 24 51.4; one token: 2.45 us, with 8 2.28).
+  // Streaming stores gain 0.9 us more, but the rows are read again by the next kernels.
+  const bool wide = a.tokens == kTokens && a.items > kWarps;
+  const int warps = wide ? kWideWarps : kWarps;
+  const int rounds = (a.items + warps - 1) / warps;
   int gy = (int)(kFill / gx);
   gy = gy < 1 ? 1 : gy > rounds ? rounds : gy;
-  const dim3 grid((unsigned)gx, (unsigned)gy);
+  const dim3 grid((unsigned)gx, (unsigned)gy), block((unsigned)warps * 32);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return plan->adjacent ? qsa_host::launch(rope_kernel<true>, grid, dim3(kThreads), 0, s, a)
-                        : qsa_host::launch(rope_kernel<false>, grid, dim3(kThreads), 0, s, a);
+  if (wide)
+    return plan->adjacent ? qsa_host::launch(rope_kernel<true, kWideWarps>, grid, block, 0, s, a)
+                          : qsa_host::launch(rope_kernel<false, kWideWarps>, grid, block, 0, s, a);
+  return plan->adjacent ? qsa_host::launch(rope_kernel<true, kWarps>, grid, block, 0, s, a)
+                        : qsa_host::launch(rope_kernel<false, kWarps>, grid, block, 0, s, a);
 }
