@@ -35,7 +35,7 @@
 //   BF16, 8 x 32,768 tokens, 16/2 heads          85 us    97%
 //   e4m3, 64 x 16K-262K tokens, 12/1 heads      455 us    92%; power-capped at 1.7 GHz,
 //                                                         ALU 39%, tensor 34% of cycles
-//   BF16, 16 x 9K-16K tokens, 24/2, with totals   75 us    82%
+//   BF16, 16 x 9K-16K tokens, 24/2, with totals   73 us    84%
 //   BF16, 1 x 4,096 tokens, 16/2                 10 us    of it 7 main kernel, 3 join
 //   BF16, 200 x 1-700 tokens, 3/1                15 us
 // What did not pay for e4m3: 6 or 7 consumers (512, 526 us then), 32-token tiles
@@ -920,6 +920,7 @@ struct JoinArgs {
   int64_t mass_ld;
   float decay;
   int32_t mass_blocks;  // CTAs per query for the weights
+  int32_t n_mass;       // all of them, the first of the grid
   int32_t parts;        // CTAs per pair for the join
   int32_t slice_bits;   // the dims of a head of many pieces are shared by 1, 2 or 4 blocks
 };
@@ -948,9 +949,9 @@ __device__ __forceinline__ float joined_lse2(const DenseArgs& a, int q, int h) {
   return M + log2f(L);
 }
 
-// The first blocks: `parts` of them a (query, KV head) pair.  The blocks after them add
-// up weights: 64 tiles (256 micro-blocks) of one query's sequence each, the heads spread
-// over 4 groups of 64 threads.
+// The first blocks add up weights, which takes longest: 64 tiles (256 micro-blocks) of one
+// query's sequence each, the heads spread over 4 groups of 64 threads.  The others join:
+// `parts` of them a (query, KV head) pair.
 // The join's time is the latency of two dependent loads (span; pieces' lse and rows
 // together), so it asks for all rows at once and waits as seldom as it can: up to 8
 // pieces a head, 64 threads join one with no exchange (the call on 125 pairs of 12 heads, 2
@@ -966,9 +967,8 @@ __global__ void __launch_bounds__(kJoinThreads) dense_join_kernel(const __grid_c
   __shared__ float lse_s[kMaxCtas];  // pieces' lse, then their weights (kMaxCtas <= kJoinThreads: one each)
   __shared__ float red_s[2][kJoinThreads / 32];
   static_assert(kMaxCtas <= kJoinThreads, "a thread per piece");
-  const int n_join = a.nq * a.hkv * ja.parts;
-  if ((int)blockIdx.x < n_join) {
-    const int pair = blockIdx.x / ja.parts, part = blockIdx.x % ja.parts;
+  if ((int)blockIdx.x >= ja.n_mass) {
+    const int pair = (blockIdx.x - ja.n_mass) / ja.parts, part = (blockIdx.x - ja.n_mass) % ja.parts;
     const int2 p = a.span[pair];
     if (p.x == p.y) return;  // written by its CTA
     const int n = max(0, p.y - p.x + 1);
@@ -1083,13 +1083,12 @@ __global__ void __launch_bounds__(kJoinThreads) dense_join_kernel(const __grid_c
   // the sequence's queries in order, so the total does not depend on which block runs
   // first.  Its blocks take every mass_blocks-th 64 tiles.
   constexpr int kHeads = 8, kRound = 4 * kHeads;  // heads of a group and of the block at once
-  const int64_t wb = blockIdx.x - n_join;
-  const int q0 = (int)(wb / ja.mass_blocks), grp = tid >> 6;
+  const int q0 = blockIdx.x / ja.mass_blocks, grp = tid >> 6;
   float4(*sum_s)[64] = reinterpret_cast<float4(*)[64]>(&acc_s[0]);
   const int seq = a.q_seq[q0], longest = query_len(a, q0, false);
   const int64_t max_tiles = (int64_t)a.mpps * kTilesPerPage;
   __shared__ unsigned same_s[kJoinThreads / 32];  // queries of this sequence, 256 at a time
-  for (int t0 = (int)(wb % ja.mass_blocks) * 64; t0 < tiles_of(longest); t0 += ja.mass_blocks * 64) {
+  for (int t0 = (int)(blockIdx.x % ja.mass_blocks) * 64; t0 < tiles_of(longest); t0 += ja.mass_blocks * 64) {
     const int tile = t0 + (tid & 63);
     float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
     const int blocks = (longest + kRatio - 1) / kRatio;
@@ -1304,8 +1303,9 @@ extern "C" int qsa_dense_decode(const qsa_cache_t* cache, const void* q, int32_t
   j.slice_bits = pairs * a.G * 4 <= 2 * a.ctas ? 2 : pairs * a.G * 2 <= 2 * a.ctas ? 1 : 0;
   const int64_t items = (int64_t)a.G << j.slice_bits;
   j.parts = (int32_t)(want < items ? want : items);
-  const int64_t grid = pairs * j.parts + (mass ? (int64_t)nq * j.mass_blocks : 0);
+  const int64_t n_mass = mass ? (int64_t)nq * j.mass_blocks : 0, grid = n_mass + pairs * j.parts;
   if (grid > 0x7fffffff) return QSA_ERR_UNSUPPORTED;
+  j.n_mass = (int32_t)n_mass;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int r = c.kv_dtype == QSA_KV_FP8_E4M3 ? launch_dense<true>(a, s) : launch_dense<false>(a, s);
   if (r != QSA_OK) return r;
