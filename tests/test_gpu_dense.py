@@ -277,6 +277,30 @@ def test_dense_decode_long_shares(lens, fp8):
 
 
 @pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("lens,hq,hkv", [([30000], 16, 1), ([9000] + [100] * 7, 16, 1), ([20000] + [40] * 30, 24, 2),
+                                         ([20000] + [40] * 150, 32, 2), ([2000 + 7 * i for i in range(60)], 12, 1)])
+def test_dense_decode_joins_few_and_many_pieces(lens, hq, hkv, fp8):
+    """Pairs of 1 to 148 pieces, heads joined whole or by slices, one or several a block."""
+    grp = Group(lens, hkv, fp8, seed=hq)
+    mass0 = torch.rand((len(lens), grp.cache.max_pages_per_seq * 16), generator=gen(hq))
+    check_dense(grp, queries(len(lens), hq, 3, 2.0), list(range(len(lens))), [n - 1 for n in lens], track=True,
+                mass0=mass0)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("n", [30000, 1500])
+def test_dense_decode_pieces_without_a_token(n, fp8):
+    """Runs of missed pages that empty whole CTAs' pieces, the first and the last too."""
+    grp = Group([n, 64 * 7], 1, fp8, seed=5)
+    pages = -(-n // 64)
+    missed = [P for P in range(pages) if P < pages // 5 or pages // 2 <= P < pages // 2 + pages // 6 or P > pages - pages // 8]
+    grp.cache.block_table[0, missed] = -1
+    mass0 = torch.rand((2, grp.cache.max_pages_per_seq * 16), generator=gen(n))
+    check_dense(grp, queries(2, 12, 4, 2.0), [0, 1], [n - 1, 64 * 7 - 1], track=True, mass0=mass0, status=1,
+                lost={(0, P) for P in missed})
+
+
+@pytest.mark.parametrize("fp8", [False, True])
 @pytest.mark.parametrize("gain", [2.0 ** -30, 2.0 ** -14, 30.0, 2.0 ** 18])
 def test_dense_decode_small_and_large_queries(gain, fp8):
     """Logits from all but equal to one token taking everything; FP8 operands beyond FP16's range."""
