@@ -12,26 +12,28 @@
 // evict_select_kernel, a CTA per sequence or a cluster of up to 8: radix select of the
 // cut (11 + 11 + 10 bits of the order-preserving key) over masses held in shared
 // memory, histograms summed over the cluster's shared memory, then one ordered pass
-// that writes the kept indices, the number kept before every page, and the moved mass
+// that writes the kept indices, the number kept before every unit, and the moved mass
 // row.  Bound by the latency of its passes: 6 us for 4K tokens; a call that cuts one
 // sequence of 262,144 tokens to 1,024 blocks took 168 us with one CTA, 53 with a cluster.
 //
-// evict_move_kernel: units of one destination page and KV head (16 runs, 64 KiB
+// evict_move_kernel: units of 8 destination blocks and one KV head (8 runs, 32 KiB
 // BF16) are claimed by warps, one CTA per SM, each warp with a buffer of its own in
-// shared memory: 3 of them BF16, 6 e4m3 (as many as fit; one alone left its SM idle while
-// it wrote), 2 where there are too few units for more; lane b moves block b with bulk
+// shared memory: 6 of them BF16, 12 e4m3, as many as fit; lane b moves block b with bulk
 // copies.  What bounds it is the traffic: each kept run is read once and written once.
-// The move is in place (or into other pages), so a page may be written only when
+// Units of a page (3 buffers an SM) left the SMs idle at the end: 86 us instead of 81 at
+// 48 x 4.3K-4.9K tokens; of 4 blocks, 82, and 195 instead of 192 at 8 x 33K-50K.
+// The move is in place (or into other pages), so a unit's place may be written only when
 // the blocks it held have been read.  Kept blocks move towards lower indices
-// only; hence page c's old blocks go to pages <= c, and a warp that has read its
-// own 16 blocks has only to wait until the one or two lower pages that took
-// blocks out of page c have been read as well.  Units are claimed by ticket,
-// lower pages first, and read before they wait, so the lowest unit at work
+// only; hence unit c's old blocks go to units <= c, and a warp that has read its
+// own blocks has only to wait until the one or two lower units that took
+// blocks out of unit c's place have been read as well.  Units are claimed by ticket,
+// lower ones first, and read before they wait, so the lowest unit at work
 // never waits and every wait ends.
 //
 // Measured on one B200 (time of the call, share of the 6.54 TB/s copy rate):
-//   8 x 33K-50K tokens to 8,192 blocks, 2 heads      191 us   89%; in place 12 to 22% more
-//   48 x 4.3K-4.9K tokens to 1,024 blocks, 1 head     86 us   76%; 10 us of it selection
+//   8 x 33K-50K tokens to 8,192 blocks, 2 heads      192 us   88%; in place 15% more
+//   48 x 4.3K-4.9K tokens to 1,024 blocks, 1 head     81 us   81%; 10 us of it selection;
+//                                                             in place 30% more
 //   1 x 4,163 tokens to 1,024 blocks, 2 heads         13 us   of it 6 selection, 6 moves
 #include "qsa_common.cuh"
 
@@ -43,6 +45,8 @@ constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kBins0 = 2048, kBins1 = 2048, kBins2 = 1024;  // 11 + 11 + 10 bits of a key
 constexpr int kFew = 256;  // keys that are ranked by comparing each with all
+constexpr int kUnit = 8;  // destination blocks that a warp moves at a time
+constexpr int kUnitsPerPage = kBlocksPerPage / kUnit;
 constexpr int kMaxCluster = 8;
 constexpr int kOnePerSm = 116 * 1024;
 constexpr int kMaxRoom = 48 * 1024;  // masses the selection keeps in shared memory: 192 KiB, 196,608 tokens
@@ -63,11 +67,12 @@ struct EvictArgs {
   int32_t* new_len;
   // workspace
   int32_t* ticket;
-  int32_t* read_done;  // [n][hkv][pages of the budget]
-  int32_t* rank;       // [n][max_pages_per_seq + 2] kept blocks before each page, then the entry's
+  int32_t* read_done;  // [n][hkv][units]
+  int32_t* rank;       // [n][table_units + 2] kept blocks before each unit, then the entry's
                        // old length (0: refused), so that new_len may be seq_len itself
   float* mass_tmp;     // [n][budget + 1]
-  int32_t pages;       // destination pages a sequence can fill
+  int32_t units;       // destination units a sequence can fill
+  int32_t table_units; // units of a sequence's row of the table
   int32_t* st;
 };
 
@@ -135,7 +140,7 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(EvictArgs 
   };
   const int hkv = a.c.num_kv_heads;
   if (blockIdx.x == 0 && tid == 0) *a.ticket = 0;
-  for (int k = gtid; k < hkv * a.pages; k += gthreads) a.read_done[(int64_t)i * hkv * a.pages + k] = 0;
+  for (int k = gtid; k < hkv * a.units; k += gthreads) a.read_done[(int64_t)i * hkv * a.units + k] = 0;
   int32_t* keep = a.keep + (int64_t)i * a.budget;
   int seq = entry_seq(a, i, part == 0);
   const int len = a.seq_len[i];
@@ -143,8 +148,8 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(EvictArgs 
     if (gtid == 0) flag(a.st, QSA_DEV_BAD_POS);
     seq = -1;
   }
-  int32_t* rank = a.rank + (int64_t)i * (a.c.max_pages_per_seq + 2);
-  if (gtid == 0) rank[a.c.max_pages_per_seq + 1] = seq < 0 ? 0 : len;
+  int32_t* rank = a.rank + (int64_t)i * (a.table_units + 2);
+  if (gtid == 0) rank[a.table_units + 1] = seq < 0 ? 0 : len;
   if (seq < 0) {  // nothing of this entry moves; the whole cluster leaves before its first barrier
     for (int k = gtid; k < a.budget; k += gthreads) keep[k] = -1;
     if (gtid == 0) {
@@ -322,7 +327,7 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(EvictArgs 
     __syncwarp();
     cluster_arrive();  // done with the other CTAs' shared memory; waited for before leaving
   }
-  // ---- in order: kept indices, blocks kept before each page, and the moved masses
+  // ---- in order: kept indices, blocks kept before each unit, and the moved masses
   // (rows too long to be held pass through the workspace)
   float* out = a.mass_out + (int64_t)seq * a.mass_ld;
   float* tmp = held ? out : a.mass_tmp + (int64_t)i * (a.budget + 1);
@@ -334,7 +339,7 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(EvictArgs 
     const int eb = eq0 + __popc(em & below);
     const int at = gt0 + __popc(gm & below) + min(eb, need);
     if (b < nb) {
-      if (b % kBlocksPerPage == 0) rank[b / kBlocksPerPage] = at;
+      if (b % kUnit == 0) rank[b / kUnit] = at;
       if (g || (e && eb < need)) {
         keep[at] = b;
         tmp[at] = x;
@@ -344,8 +349,7 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(EvictArgs 
     eq0 += __popc(em);
   });
   for (int k = count + gtid; k < a.budget; k += gthreads) keep[k] = -1;
-  for (int P = (nb + kBlocksPerPage - 1) / kBlocksPerPage + gtid; P <= a.c.max_pages_per_seq; P += gthreads)
-    rank[P] = count;
+  for (int U = (nb + kUnit - 1) / kUnit + gtid; U <= a.table_units; U += gthreads) rank[U] = count;
   if (gtid == 0) {
     if (tail) tmp[count] = m_open;
     a.keep_count[i] = count;
@@ -381,21 +385,21 @@ __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.comm
 __device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 __device__ __forceinline__ void fence_proxy_async_all() { asm volatile("fence.proxy.async;" ::: "memory"); }
 
-// A unit of the move, as lane b of a warp sees it: block b of the destination page.
+// A unit of the move, as lane b of a warp sees it: the unit's block b.
 struct Unit {
-  int page, g;           // destination page of the sequence, KV head
+  int unit, g;           // kUnit destination blocks of the sequence, KV head
   int32_t* done;         // read flags of the sequence and head
   int src, dst;          // physical page * 16 + slot; src -1: nothing to move
-  int p0, p1;            // lower pages that take blocks out of this one (none: p1 < p0); only a page
+  int p0, p1;            // lower units that take blocks out of this one (none: p1 < p0); only a page
                          // of the sequence's own, written in place, still holds them
-  bool any, in_place;    // the page receives blocks; it is the sequence's own
+  bool any, in_place;    // the unit receives blocks; its page is the sequence's own
 };
 
 // kRunBytes: 4096 (BF16) or 2048 (e4m3); kWorkers warps, each with a buffer of one unit.
 template <int kRunBytes, int kWorkers>
 struct MoveLay {
   static constexpr int kKcBytes = kIdxDim * 2;
-  static constexpr int kBuf = kBlocksPerPage * (kRunBytes + kKcBytes);
+  static constexpr int kBuf = kUnit * (kRunBytes + kKcBytes);
   static constexpr int kSmem = kWorkers * kBuf + kWorkers * 8;
   static_assert(kSmem <= 232448, "shared memory budget");
 };
@@ -421,38 +425,38 @@ __global__ void __launch_bounds__(kWorkers * 32) evict_move_kernel(EvictArgs a, 
     if (lane == 0) t = atomicAdd(a.ticket, 1);
     return __shfl_sync(0xffffffffu, t, 0);
   };
-  // head fastest, then page, then sequence: lower pages of a sequence and head come first
+  // head fastest, then unit, then sequence: lower units of a sequence and head come first
   auto look_up = [&](int t) {
     Unit u;
-    const int i = t / (hkv * a.pages);
+    const int i = t / (hkv * a.units);
     u.g = t % hkv;
-    u.page = t / hkv % a.pages;
-    const int32_t* rank = a.rank + (int64_t)i * (a.c.max_pages_per_seq + 2);
-    u.done = a.read_done + ((int64_t)i * hkv + u.g) * a.pages;
+    u.unit = t / hkv % a.units;
+    const int32_t* rank = a.rank + (int64_t)i * (a.table_units + 2);
+    u.done = a.read_done + ((int64_t)i * hkv + u.g) * a.units;
     u.src = -1;
     u.dst = 0;
-    const int k = u.page * kBlocksPerPage + lane;
+    const int k = u.unit * kUnit + lane;
     // independent loads first; keep may hold nothing meaningful at k, then it is not used
-    const int count = a.keep_count[i], len = rank[a.c.max_pages_per_seq + 1], seq = a.seq_ids[i];
-    const int k0 = rank[u.page], k1 = rank[u.page + 1];
+    const int count = a.keep_count[i], len = rank[a.table_units + 1], seq = a.seq_ids[i];
+    const int k0 = rank[u.unit], k1 = rank[u.unit + 1];
     const int64_t row = (int64_t)max(0, min(seq, a.c.max_seqs - 1)) * a.c.max_pages_per_seq;
-    const int dp = a.dst_table[row + u.page], own = a.c.block_table[row + u.page];
-    const int kept = lane < kBlocksPerPage && k < a.budget ? a.keep[(int64_t)i * a.budget + k] : 0;
+    const int dp = a.dst_table[row + u.unit / kUnitsPerPage], own = a.c.block_table[row + u.unit / kUnitsPerPage];
+    const int kept = lane < kUnit && k < a.budget ? a.keep[(int64_t)i * a.budget + k] : 0;
     const int total = count + (len % kRatio ? 1 : 0);
     u.in_place = dp == own;
-    u.any = u.page * kBlocksPerPage < total;
-    // pages behind the last kept block: the entry's other tickets hold nothing either
-    if (!u.any && lane == 0) atomicMax(a.ticket, (i + 1) * hkv * a.pages);
-    u.p0 = k0 / kBlocksPerPage;
-    u.p1 = k1 > k0 && dp == own ? min(u.page - 1, (k1 - 1) / kBlocksPerPage) : -1;
-    if (lane < kBlocksPerPage && k < total) {
+    u.any = u.unit * kUnit < total;
+    // units behind the last kept block: the entry's other tickets hold nothing either
+    if (!u.any && lane == 0) atomicMax(a.ticket, (i + 1) * hkv * a.units);
+    u.p0 = k0 / kUnit;
+    u.p1 = k1 > k0 && dp == own ? min(u.unit - 1, (k1 - 1) / kUnit) : -1;
+    if (lane < kUnit && k < total) {
       const int b = k < count ? kept : len / kRatio;
       const int sp = a.c.block_table[row + b / kBlocksPerPage];
       if (sp < 0 || sp >= a.c.num_pages || dp < 0 || dp >= a.c.num_pages) {
         flag(a.st, QSA_DEV_BAD_PAGE);
       } else {
         u.src = sp * kBlocksPerPage + b % kBlocksPerPage;
-        u.dst = dp * kBlocksPerPage + lane;
+        u.dst = dp * kBlocksPerPage + k % kBlocksPerPage;
         if (u.src == u.dst) u.src = -1;  // stays where it is
       }
     }
@@ -462,7 +466,7 @@ __global__ void __launch_bounds__(kWorkers * 32) evict_move_kernel(EvictArgs a, 
     return kv + (((int64_t)(unit / kBlocksPerPage) * hkv + g) * kBlocksPerPage + unit % kBlocksPerPage) * kRunBytes;
   };
   const uint64_t policy = l2_policy_evict_first();
-  const uint32_t my_run = buf + lane * kRunBytes, my_kc = buf + kBlocksPerPage * kRunBytes + lane * LY::kKcBytes;
+  const uint32_t my_run = buf + lane * kRunBytes, my_kc = buf + kUnit * kRunBytes + lane * LY::kKcBytes;
   uint32_t parity = 0;
   bool sound = true;
   int t = claim();
@@ -487,8 +491,8 @@ __global__ void __launch_bounds__(kWorkers * 32) evict_move_kernel(EvictArgs a, 
     const Unit now = u;
     const int t_next = claim();
     if (t_next < units) u = look_up(t_next);
-    // ---- the lower pages that take blocks out of this one: usually read by now (at most
-    // 16 kept blocks came from here, so they went to two pages)
+    // ---- the lower units that take blocks out of this one: usually read by now (at most
+    // kUnit kept blocks came from here, so they went to two units)
     const int dep = now.p0 + lane;
     const bool has_dep = movers && dep <= now.p1;
     bool clear = !has_dep || ld_acquire(now.done + dep);
@@ -498,7 +502,7 @@ __global__ void __launch_bounds__(kWorkers * 32) evict_move_kernel(EvictArgs a, 
     }
     const bool wait = !__all_sync(0xffffffffu, clear);
     const bool early = now.in_place || !movers;  // its neighbours wait; else the flag keeps out of the stores' way
-    if (early && now.any && lane == 0) st_release(now.done + now.page, 1);
+    if (early && now.any && lane == 0) st_release(now.done + now.unit, 1);
     if (movers) {
       if (wait && !clear) {
         const uint64_t t0 = global_timer_ns();
@@ -521,7 +525,7 @@ __global__ void __launch_bounds__(kWorkers * 32) evict_move_kernel(EvictArgs a, 
         if (with_kc) bulk_s2g(kc + (int64_t)now.dst * LY::kKcBytes, my_kc, LY::kKcBytes);
       }
       bulk_commit();
-      if (!early && lane == 0) st_release(now.done + now.page, 1);
+      if (!early && lane == 0) st_release(now.done + now.unit, 1);
     }
     t = t_next;
   }
@@ -534,14 +538,18 @@ struct WorkspaceMap {
 
 int64_t align256(int64_t n) { return (n + 255) / 256 * 256; }
 
-int32_t pages_of_budget(int32_t budget) { return (int32_t)(((int64_t)budget + 1 + kBlocksPerPage - 1) / kBlocksPerPage); }
+// destination units that a sequence can fill
+int32_t units_of(const qsa_cache_t& c, int32_t budget) {
+  const int32_t u = (budget + kUnit) / kUnit;  // and the open block
+  return u < c.max_pages_per_seq * kUnitsPerPage ? u : c.max_pages_per_seq * kUnitsPerPage;
+}
 
 WorkspaceMap workspace_map(const qsa_cache_t& c, int32_t n, int32_t budget) {
   WorkspaceMap m;
   m.ticket = 0;
   m.read_done = 256;
-  m.rank = m.read_done + align256((int64_t)n * c.num_kv_heads * pages_of_budget(budget) * 4);
-  m.mass_tmp = m.rank + align256((int64_t)n * ((int64_t)c.max_pages_per_seq + 2) * 4);
+  m.rank = m.read_done + align256((int64_t)n * c.num_kv_heads * units_of(c, budget) * 4);
+  m.mass_tmp = m.rank + align256((int64_t)n * ((int64_t)c.max_pages_per_seq * kUnitsPerPage + 2) * 4);
   m.total = m.mass_tmp + align256((int64_t)n * ((int64_t)budget + 1) * 4);
   return m;
 }
@@ -644,10 +652,10 @@ extern "C" int qsa_evict(const qsa_cache_t* cache, const int32_t* dst_table, con
   a.read_done = reinterpret_cast<int32_t*>(ws + m.read_done);
   a.rank = reinterpret_cast<int32_t*>(ws + m.rank);
   a.mass_tmp = reinterpret_cast<float*>(ws + m.mass_tmp);
-  a.pages = pages_of_budget(budget);
-  if (a.pages > c.max_pages_per_seq) a.pages = c.max_pages_per_seq;
+  a.units = units_of(c, budget);
+  a.table_units = c.max_pages_per_seq * kUnitsPerPage;
   a.st = dev_status;
-  const int64_t units = (int64_t)n * c.num_kv_heads * a.pages;
+  const int64_t units = (int64_t)n * c.num_kv_heads * a.units;
   if (units > 0x3fffffff) return QSA_ERR_UNSUPPORTED;
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
@@ -671,11 +679,11 @@ extern "C" int qsa_evict(const qsa_cache_t* cache, const int32_t* dst_table, con
   const size_t smem = (size_t)(room * 4 > kOnePerSm ? room * 4 : kOnePerSm);
   const int r = ctas > 1 ? launch_select<true>(a, ctas, room, smem, s) : launch_select<false>(a, 1, room, smem, s);
   if (r != QSA_OK) return r;
-  // Buffers per SM: 3 (BF16) or 6 keep the memory busy.  A call of at most a unit per SM
-  // ends sooner with 2: the CTAs that start first then take all units (one sequence of
-  // 4,163 tokens, 130 units: 12.3 us with 2, 13.4 with 1 or 3; 48 of them: 92 us, 84 with 3)
-  const bool few = units <= sms;
+  // Buffers per SM: 6 (BF16) or 12 keep the memory busy.  A call of at most two units per
+  // SM ends sooner with 2: the CTAs that start first then take all units (one sequence of
+  // 4,163 tokens, 260 units: 12.7 us with 2, 12.8 with 3, 13.2 with 6)
+  const bool few = units <= 2 * sms;
   if (c.kv_dtype == QSA_KV_FP8_E4M3)
-    return few ? launch_move<2048, 2>(a, (int)units, sms, s) : launch_move<2048, 6>(a, (int)units, sms, s);
-  return few ? launch_move<4096, 2>(a, (int)units, sms, s) : launch_move<4096, 3>(a, (int)units, sms, s);
+    return few ? launch_move<2048, 2>(a, (int)units, sms, s) : launch_move<2048, 12>(a, (int)units, sms, s);
+  return few ? launch_move<4096, 2>(a, (int)units, sms, s) : launch_move<4096, 6>(a, (int)units, sms, s);
 }
