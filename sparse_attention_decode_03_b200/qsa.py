@@ -998,7 +998,8 @@ class DenseDecoder:
     """Outputs and workspace of qsa_dense_decode for up to `max_nq` queries.  With
     ``track=True`` it also holds `mass`, the running attention weight of every
     micro-block (``decay`` of the old total is kept at each step), and
-    :meth:`evict` cuts sequences to a budget by it."""
+    :meth:`evict` cuts sequences to a budget by it.  A row of `mass` belongs to
+    the sequence in its slot: zero it when the slot goes to another."""
 
     def __init__(self, cache: PagedCache, hq: int, max_nq: int, scale: float = 1.0 / 16.0, track: bool = False,
                  decay: float = 1.0):
