@@ -31,9 +31,9 @@
 // never waits and every wait ends.
 //
 // Measured on one B200 (time of the call, share of the 6.54 TB/s copy rate):
-//   8 x 33K-50K tokens to 8,192 blocks, 2 heads      192 us   88%; in place 15% more
+//   8 x 33K-50K tokens to 8,192 blocks, 2 heads      192 us   88%; in place 2% more
 //   48 x 4.3K-4.9K tokens to 1,024 blocks, 1 head     81 us   81%; 10 us of it selection;
-//                                                             in place 30% more
+//                                                             in place 7% more
 //   1 x 4,163 tokens to 1,024 blocks, 2 heads         13 us   of it 6 selection, 6 moves
 #include "qsa_common.cuh"
 
@@ -395,7 +395,8 @@ struct Unit {
   bool any, in_place;    // the unit receives blocks; its page is the sequence's own
 };
 
-// kRunBytes: 4096 (BF16) or 2048 (e4m3); kWorkers warps, each with a buffer of one unit.
+// kRunBytes: 4096 (BF16) or 2048 (e4m3); kWorkers warps, each with a buffer of one unit;
+// kInPlace: dst_table is block_table.
 template <int kRunBytes, int kWorkers>
 struct MoveLay {
   static constexpr int kKcBytes = kIdxDim * 2;
@@ -404,7 +405,7 @@ struct MoveLay {
   static_assert(kSmem <= 232448, "shared memory budget");
 };
 
-template <int kRunBytes, int kWorkers>
+template <int kRunBytes, int kWorkers, bool kInPlace>
 __global__ void __launch_bounds__(kWorkers * 32) evict_move_kernel(EvictArgs a, int units) {
   using LY = MoveLay<kRunBytes, kWorkers>;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -425,28 +426,52 @@ __global__ void __launch_bounds__(kWorkers * 32) evict_move_kernel(EvictArgs a, 
     if (lane == 0) t = atomicAdd(a.ticket, 1);
     return __shfl_sync(0xffffffffu, t, 0);
   };
-  // head fastest, then unit, then sequence: lower units of a sequence and head come first
+  // blocks that an entry has moved, from those it keeps and its old length
+  auto total_of = [&](int count, int len) {
+    if (kInPlace && count == len / kRatio) return 0;  // nothing was cut
+    return count + (len % kRatio ? 1 : 0);
+  };
+  auto old_len = [&](int i) { return a.rank[(int64_t)i * (a.table_units + 2) + a.table_units + 1]; };
+  // In place: head fastest, then entry, then unit, since a unit waits for lower ones of its
+  // own sequence, which then were claimed a round of all entries ago at least (48 x
+  // 4.3K-4.9K tokens, cold: 90 us, unit before entry 111).  Into other pages nothing waits,
+  // and sequences in turn are read faster (8 x 33K-50K tokens: 191.7 us, in place's order 195).
   auto look_up = [&](int t) {
     Unit u;
-    const int i = t / (hkv * a.units);
+    const int i = kInPlace ? t / hkv % a.n : t / (hkv * a.units);
     u.g = t % hkv;
-    u.unit = t / hkv % a.units;
+    u.unit = kInPlace ? t / hkv / a.n : t / hkv % a.units;
     const int32_t* rank = a.rank + (int64_t)i * (a.table_units + 2);
     u.done = a.read_done + ((int64_t)i * hkv + u.g) * a.units;
     u.src = -1;
     u.dst = 0;
     const int k = u.unit * kUnit + lane;
     // independent loads first; keep may hold nothing meaningful at k, then it is not used
-    const int count = a.keep_count[i], len = rank[a.table_units + 1], seq = a.seq_ids[i];
+    const int count = a.keep_count[i], len = old_len(i), seq = a.seq_ids[i];
     const int k0 = rank[u.unit], k1 = rank[u.unit + 1];
     const int64_t row = (int64_t)max(0, min(seq, a.c.max_seqs - 1)) * a.c.max_pages_per_seq;
     const int dp = a.dst_table[row + u.unit / kUnitsPerPage], own = a.c.block_table[row + u.unit / kUnitsPerPage];
     const int kept = lane < kUnit && k < a.budget ? a.keep[(int64_t)i * a.budget + k] : 0;
-    const int total = count + (len % kRatio ? 1 : 0);
+    const int total = total_of(count, len);
     u.in_place = dp == own;
     u.any = u.unit * kUnit < total;
-    // units behind the last kept block: the entry's other tickets hold nothing either
-    if (!u.any && lane == 0) atomicMax(a.ticket, (i + 1) * hkv * a.units);
+    if (!u.any && !kInPlace) {  // the entry's other units hold nothing either
+      if (lane == 0) atomicMax(a.ticket, (i + 1) * hkv * a.units);
+    } else if (!u.any) {  // on to the next unit in order that receives blocks
+      constexpr int kLook = 4;  // x 32 entries, this unit's and then the next one's
+      unsigned has[kLook];
+#pragma unroll
+      for (int k = 0; k < kLook; ++k) {
+        const int e = i + 1 + k * 32 + lane, j = e % a.n;
+        has[k] = __ballot_sync(0xffffffffu, total_of(a.keep_count[j], old_len(j)) > (u.unit + e / a.n) * kUnit);
+      }
+      int skip = kLook * 32;
+#pragma unroll
+      for (int k = kLook - 1; k >= 0; --k)
+        if (has[k]) skip = k * 32 + __ffs(has[k]) - 1;
+      const bool over = skip == kLook * 32 && a.n <= kLook * 32;  // no entry has blocks in later units
+      if (lane == 0) atomicMax(a.ticket, over ? units : (u.unit * a.n + i + 1 + skip) * hkv);
+    }
     u.p0 = k0 / kUnit;
     u.p1 = k1 > k0 && dp == own ? min(u.unit - 1, (k1 - 1) / kUnit) : -1;
     if (lane < kUnit && k < total) {
@@ -594,13 +619,14 @@ int launch_select(const EvictArgs& a, int ctas, int room, size_t smem, cudaStrea
 template <int kRunBytes, int kWorkers>
 int launch_move(const EvictArgs& a, int units, int sms, cudaStream_t s) {
   constexpr int smem = MoveLay<kRunBytes, kWorkers>::kSmem;
-  if (cudaFuncSetAttribute(evict_move_kernel<kRunBytes, kWorkers>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           smem) != cudaSuccess) {
+  const auto kernel = a.dst_table == a.c.block_table ? evict_move_kernel<kRunBytes, kWorkers, true>
+                                                     : evict_move_kernel<kRunBytes, kWorkers, false>;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) {
     (void)cudaGetLastError();
     return QSA_ERR_CUDA;
   }
   const int grid = units < sms ? units : sms;  // at least a unit per CTA: few units spread over the SMs
-  return qsa_host::launch(evict_move_kernel<kRunBytes, kWorkers>, dim3((unsigned)grid), dim3(kWorkers * 32),
+  return qsa_host::launch(kernel, dim3((unsigned)grid), dim3(kWorkers * 32),
                           (size_t)smem, s, a, units);
 }
 
