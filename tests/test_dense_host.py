@@ -283,6 +283,38 @@ def test_in_place_moves_never_overwrite_an_unread_block(seed):
     assert slots[:len(moved)] == moved
 
 
+@pytest.mark.parametrize("seed", range(40))
+def test_in_place_tickets_reach_every_unit_that_receives_blocks(seed):
+    """Tickets run head, entry, unit; one that finds nothing moves the counter on to
+    the next unit that receives blocks, as far as it looks.  Every such unit is
+    claimed once, lower units of a sequence first, whatever the warps' order."""
+    rng = random.Random(seed)
+    n, hkv, look = rng.choice([1, 2, 5, 127, 128, 129, 300]), rng.choice([1, 2, 3]), 128
+    units = rng.randint(1, 40)
+    totals = [rng.choice([0, 0, 0, 1, rng.randint(0, UNIT * units)]) for _ in range(n)]
+    ticket, claimed, pending = 0, [], []
+    while True:
+        if pending and (len(pending) > rng.randint(0, 8) or ticket >= n * hkv * units):
+            t = pending.pop(rng.randrange(len(pending)))       # some warp looks its ticket up
+            g, i, unit = t % hkv, t // hkv % n, t // hkv // n
+            if unit * UNIT < totals[i]:
+                claimed.append((t, i, g, unit))
+                continue
+            skip = next((s for s in range(look) if totals[(i + 1 + s) % n] > (unit + (i + 1 + s) // n) * UNIT), look)
+            over = skip == look and n <= look
+            ticket = max(ticket, n * hkv * units if over else (unit * n + i + 1 + skip) * hkv)
+        elif ticket < n * hkv * units:
+            pending.append(ticket)
+            ticket += 1
+        else:
+            break
+    assert sorted(c[1:] for c in claimed) == [(i, g, u) for i in range(n) for g in range(hkv)
+                                              for u in range(-(-totals[i] // UNIT))]
+    by_ticket = sorted(claimed)
+    for i in range(n):
+        assert [c[3] for c in by_ticket if c[1] == i] == sorted(c[3] for c in claimed if c[1] == i)
+
+
 # ---------------------------------------------------------------- the references themselves
 
 

@@ -605,6 +605,21 @@ def test_evict_in_place_random(seed):
                 ids=rng.sample(range(7), 5), alias=True)
 
 
+@pytest.mark.parametrize("n", [2, 40, 128, 129, 300])
+@pytest.mark.parametrize("to_free", [False, True])
+def test_evict_many_entries_cut_uncut_and_empty(n, to_free):
+    """Most entries have nothing to move, in runs longer and shorter than the search for the next."""
+    rng = random.Random(n)
+    lens = [rng.choice([0, 3, 40, 90, rng.randint(100, 900)]) if rng.random() < 0.3 or i == n // 2 else rng.choice([0, 5, 70])
+            for i in range(n)]
+    lens[n // 3] = 2000
+    grp = Group(lens, 2, n == 40, seed=n, spare=sum(-(-x // 64) for x in lens) if to_free else 0)
+    mass = masses(rng, (n, grp.cache.max_pages_per_seq * 16))
+    ids = rng.sample(range(n), n - n // 8) + [-1] * 3
+    rng.shuffle(ids)
+    check_evict(grp, 30, 2, 5, mass, ids=ids, to_free=to_free, alias=True)
+
+
 def test_evict_refuses_entries_and_flags_them():
     grp = Group([300, 301, 302, 303], 2, seed=4)
     mass = masses(random.Random(4), (4, grp.cache.max_pages_per_seq * 16))
