@@ -20,7 +20,7 @@
 // BF16) are claimed by warps, one CTA per SM, each warp with a buffer of its own in
 // shared memory: 6 of them BF16, 12 e4m3, as many as fit; lane b moves block b with bulk
 // copies.  What bounds it is the traffic: each kept run is read once and written once.
-// Units of a page (3 buffers an SM) left the SMs idle at the end: 86 us instead of 81 at
+// Small calls use units half that size.  Units of a page (3 buffers an SM) left the SMs idle at the end: 86 us instead of 81 at
 // 48 x 4.3K-4.9K tokens; of 4 blocks, 82, and 195 instead of 192 at 8 x 33K-50K.
 // The move is in place (or into other pages), so a unit's place may be written only when
 // the blocks it held have been read.  Kept blocks move towards lower indices
@@ -45,8 +45,9 @@ constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kBins0 = 2048, kBins1 = 2048, kBins2 = 1024;  // 11 + 11 + 10 bits of a key
 constexpr int kFew = 256;  // keys that are ranked by comparing each with all
-constexpr int kUnit = 8;  // destination blocks that a warp moves at a time
-constexpr int kUnitsPerPage = kBlocksPerPage / kUnit;
+// Destination blocks that a warp moves at a time, many or few; ranks are kept for the smaller
+constexpr int kUnitBlocks = 8, kSmallUnit = 4;
+constexpr int kRanksPerPage = kBlocksPerPage / kSmallUnit;
 constexpr int kMaxCluster = 8;
 constexpr int kOnePerSm = 116 * 1024;
 constexpr int kMaxRoom = 48 * 1024;  // masses the selection keeps in shared memory: 192 KiB, 196,608 tokens
@@ -68,11 +69,11 @@ struct EvictArgs {
   // workspace
   int32_t* ticket;
   int32_t* read_done;  // [n][hkv][units]
-  int32_t* rank;       // [n][table_units + 2] kept blocks before each unit, then the entry's
+  int32_t* rank;       // [n][table_ranks + 2] kept blocks before each kSmallUnit, then the entry's
                        // old length (0: refused), so that new_len may be seq_len itself
   float* mass_tmp;     // [n][budget + 1]
   int32_t units;       // destination units a sequence can fill
-  int32_t table_units; // units of a sequence's row of the table
+  int32_t table_ranks; // ranks of a sequence's row of the table
   int32_t* st;
 };
 
@@ -148,8 +149,8 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(EvictArgs 
     if (gtid == 0) flag(a.st, QSA_DEV_BAD_POS);
     seq = -1;
   }
-  int32_t* rank = a.rank + (int64_t)i * (a.table_units + 2);
-  if (gtid == 0) rank[a.table_units + 1] = seq < 0 ? 0 : len;
+  int32_t* rank = a.rank + (int64_t)i * (a.table_ranks + 2);
+  if (gtid == 0) rank[a.table_ranks + 1] = seq < 0 ? 0 : len;
   if (seq < 0) {  // nothing of this entry moves; the whole cluster leaves before its first barrier
     for (int k = gtid; k < a.budget; k += gthreads) keep[k] = -1;
     if (gtid == 0) {
@@ -327,7 +328,7 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(EvictArgs 
     __syncwarp();
     cluster_arrive();  // done with the other CTAs' shared memory; waited for before leaving
   }
-  // ---- in order: kept indices, blocks kept before each unit, and the moved masses
+  // ---- in order: kept indices, blocks kept before each place, and the moved masses
   // (rows too long to be held pass through the workspace)
   float* out = a.mass_out + (int64_t)seq * a.mass_ld;
   float* tmp = held ? out : a.mass_tmp + (int64_t)i * (a.budget + 1);
@@ -339,7 +340,7 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(EvictArgs 
     const int eb = eq0 + __popc(em & below);
     const int at = gt0 + __popc(gm & below) + min(eb, need);
     if (b < nb) {
-      if (b % kUnit == 0) rank[b / kUnit] = at;
+      if (b % kSmallUnit == 0) rank[b / kSmallUnit] = at;
       if (g || (e && eb < need)) {
         keep[at] = b;
         tmp[at] = x;
@@ -349,7 +350,7 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(EvictArgs 
     eq0 += __popc(em);
   });
   for (int k = count + gtid; k < a.budget; k += gthreads) keep[k] = -1;
-  for (int U = (nb + kUnit - 1) / kUnit + gtid; U <= a.table_units; U += gthreads) rank[U] = count;
+  for (int k = (nb + kSmallUnit - 1) / kSmallUnit + gtid; k <= a.table_ranks; k += gthreads) rank[k] = count;
   if (gtid == 0) {
     if (tail) tmp[count] = m_open;
     a.keep_count[i] = count;
@@ -395,9 +396,9 @@ struct Unit {
   bool any, in_place;    // the unit receives blocks; its page is the sequence's own
 };
 
-// kRunBytes: 4096 (BF16) or 2048 (e4m3); kWorkers warps, each with a buffer of one unit;
+// kRunBytes: 4096 (BF16) or 2048 (e4m3); kUnit blocks of a unit; kWorkers warps, each with a buffer of one unit;
 // kInPlace: dst_table is block_table.
-template <int kRunBytes, int kWorkers>
+template <int kRunBytes, int kUnit, int kWorkers>
 struct MoveLay {
   static constexpr int kKcBytes = kIdxDim * 2;
   static constexpr int kBuf = kUnit * (kRunBytes + kKcBytes);
@@ -405,9 +406,10 @@ struct MoveLay {
   static_assert(kSmem <= 232448, "shared memory budget");
 };
 
-template <int kRunBytes, int kWorkers, bool kInPlace>
+template <int kRunBytes, int kUnit, int kWorkers, bool kInPlace>
 __global__ void __launch_bounds__(kWorkers * 32) evict_move_kernel(EvictArgs a, int units) {
-  using LY = MoveLay<kRunBytes, kWorkers>;
+  using LY = MoveLay<kRunBytes, kUnit, kWorkers>;
+  constexpr int kRanks = kUnit / kSmallUnit, kUnitsPerPage = kBlocksPerPage / kUnit;
   extern __shared__ __align__(128) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t buf = smem_u32(smem) + warp * LY::kBuf, bar = smem_u32(smem) + kWorkers * LY::kBuf + warp * 8;
@@ -431,7 +433,7 @@ __global__ void __launch_bounds__(kWorkers * 32) evict_move_kernel(EvictArgs a, 
     if (kInPlace && count == len / kRatio) return 0;  // nothing was cut
     return count + (len % kRatio ? 1 : 0);
   };
-  auto old_len = [&](int i) { return a.rank[(int64_t)i * (a.table_units + 2) + a.table_units + 1]; };
+  auto old_len = [&](int i) { return a.rank[(int64_t)i * (a.table_ranks + 2) + a.table_ranks + 1]; };
   // In place: head fastest, then entry, then unit, since a unit waits for lower ones of its
   // own sequence, which then were claimed a round of all entries ago at least (48 x
   // 4.3K-4.9K tokens, cold: 90 us, unit before entry 111).  Into other pages nothing waits,
@@ -441,14 +443,14 @@ __global__ void __launch_bounds__(kWorkers * 32) evict_move_kernel(EvictArgs a, 
     const int i = kInPlace ? t / hkv % a.n : t / (hkv * a.units);
     u.g = t % hkv;
     u.unit = kInPlace ? t / hkv / a.n : t / hkv % a.units;
-    const int32_t* rank = a.rank + (int64_t)i * (a.table_units + 2);
+    const int32_t* rank = a.rank + (int64_t)i * (a.table_ranks + 2);
     u.done = a.read_done + ((int64_t)i * hkv + u.g) * a.units;
     u.src = -1;
     u.dst = 0;
     const int k = u.unit * kUnit + lane;
     // independent loads first; keep may hold nothing meaningful at k, then it is not used
     const int count = a.keep_count[i], len = old_len(i), seq = a.seq_ids[i];
-    const int k0 = rank[u.unit], k1 = rank[u.unit + 1];
+    const int k0 = rank[u.unit * kRanks], k1 = rank[(u.unit + 1) * kRanks];
     const int64_t row = (int64_t)max(0, min(seq, a.c.max_seqs - 1)) * a.c.max_pages_per_seq;
     const int dp = a.dst_table[row + u.unit / kUnitsPerPage], own = a.c.block_table[row + u.unit / kUnitsPerPage];
     const int kept = lane < kUnit && k < a.budget ? a.keep[(int64_t)i * a.budget + k] : 0;
@@ -564,17 +566,17 @@ struct WorkspaceMap {
 int64_t align256(int64_t n) { return (n + 255) / 256 * 256; }
 
 // destination units that a sequence can fill
-int32_t units_of(const qsa_cache_t& c, int32_t budget) {
-  const int32_t u = (budget + kUnit) / kUnit;  // and the open block
-  return u < c.max_pages_per_seq * kUnitsPerPage ? u : c.max_pages_per_seq * kUnitsPerPage;
+int32_t units_of(const qsa_cache_t& c, int32_t budget, int32_t unit) {
+  const int32_t u = (budget + unit) / unit, most = c.max_pages_per_seq * (kBlocksPerPage / unit);  // and the open block
+  return u < most ? u : most;
 }
 
 WorkspaceMap workspace_map(const qsa_cache_t& c, int32_t n, int32_t budget) {
   WorkspaceMap m;
   m.ticket = 0;
   m.read_done = 256;
-  m.rank = m.read_done + align256((int64_t)n * c.num_kv_heads * units_of(c, budget) * 4);
-  m.mass_tmp = m.rank + align256((int64_t)n * ((int64_t)c.max_pages_per_seq * kUnitsPerPage + 2) * 4);
+  m.rank = m.read_done + align256((int64_t)n * c.num_kv_heads * units_of(c, budget, kSmallUnit) * 4);
+  m.mass_tmp = m.rank + align256((int64_t)n * ((int64_t)c.max_pages_per_seq * kRanksPerPage + 2) * 4);
   m.total = m.mass_tmp + align256((int64_t)n * ((int64_t)budget + 1) * 4);
   return m;
 }
@@ -616,11 +618,11 @@ int launch_select(const EvictArgs& a, int ctas, int room, size_t smem, cudaStrea
   return QSA_OK;
 }
 
-template <int kRunBytes, int kWorkers>
+template <int kRunBytes, int kUnit, int kWorkers>
 int launch_move(const EvictArgs& a, int units, int sms, cudaStream_t s) {
-  constexpr int smem = MoveLay<kRunBytes, kWorkers>::kSmem;
-  const auto kernel = a.dst_table == a.c.block_table ? evict_move_kernel<kRunBytes, kWorkers, true>
-                                                     : evict_move_kernel<kRunBytes, kWorkers, false>;
+  constexpr int smem = MoveLay<kRunBytes, kUnit, kWorkers>::kSmem;
+  const auto kernel = a.dst_table == a.c.block_table ? evict_move_kernel<kRunBytes, kUnit, kWorkers, true>
+                                                     : evict_move_kernel<kRunBytes, kUnit, kWorkers, false>;
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) {
     (void)cudaGetLastError();
     return QSA_ERR_CUDA;
@@ -678,17 +680,23 @@ extern "C" int qsa_evict(const qsa_cache_t* cache, const int32_t* dst_table, con
   a.read_done = reinterpret_cast<int32_t*>(ws + m.read_done);
   a.rank = reinterpret_cast<int32_t*>(ws + m.rank);
   a.mass_tmp = reinterpret_cast<float*>(ws + m.mass_tmp);
-  a.units = units_of(c, budget);
-  a.table_units = c.max_pages_per_seq * kUnitsPerPage;
+  a.table_ranks = c.max_pages_per_seq * kRanksPerPage;
   a.st = dev_status;
-  const int64_t units = (int64_t)n * c.num_kv_heads * a.units;
-  if (units > 0x3fffffff) return QSA_ERR_UNSUPPORTED;
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
     (void)cudaGetLastError();
     return QSA_ERR_CUDA;
   }
+  // Buffers per SM: 6 units of 8 blocks (BF16) or 12 keep the memory busy.  A call of at
+  // most two such units per SM ends sooner with 4 of half the size: they spread more
+  // evenly, and the first stores start earlier (one sequence of 4,163 tokens in a
+  // graph: 11.4 us, 12.7 with 2 of full size, 12.9 with 3 of half)
+  a.units = units_of(c, budget, kUnitBlocks);
+  const bool few = (int64_t)n * c.num_kv_heads * a.units <= 2 * sms;
+  if (few) a.units = units_of(c, budget, kSmallUnit);
+  const int64_t units = (int64_t)n * c.num_kv_heads * a.units;
+  if (units > 0x3fffffff) return QSA_ERR_UNSUPPORTED;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   // CTAs per entry: a cluster when its row may be long, as many as keep the call on
   // about the card's SMs (the call on one row of 65,500 blocks: 54 us with 8, 168 with 1;
@@ -705,11 +713,9 @@ extern "C" int qsa_evict(const qsa_cache_t* cache, const int32_t* dst_table, con
   const size_t smem = (size_t)(room * 4 > kOnePerSm ? room * 4 : kOnePerSm);
   const int r = ctas > 1 ? launch_select<true>(a, ctas, room, smem, s) : launch_select<false>(a, 1, room, smem, s);
   if (r != QSA_OK) return r;
-  // Buffers per SM: 6 (BF16) or 12 keep the memory busy.  A call of at most two units per
-  // SM ends sooner with 2: the CTAs that start first then take all units (one sequence of
-  // 4,163 tokens, 260 units: 12.7 us with 2, 12.8 with 3, 13.2 with 6)
-  const bool few = units <= 2 * sms;
   if (c.kv_dtype == QSA_KV_FP8_E4M3)
-    return few ? launch_move<2048, 2>(a, (int)units, sms, s) : launch_move<2048, 12>(a, (int)units, sms, s);
-  return few ? launch_move<4096, 2>(a, (int)units, sms, s) : launch_move<4096, 6>(a, (int)units, sms, s);
+    return few ? launch_move<2048, kSmallUnit, 4>(a, (int)units, sms, s)
+               : launch_move<2048, kUnitBlocks, 12>(a, (int)units, sms, s);
+  return few ? launch_move<4096, kSmallUnit, 4>(a, (int)units, sms, s)
+             : launch_move<4096, kUnitBlocks, 6>(a, (int)units, sms, s);
 }

@@ -232,12 +232,10 @@ def test_shares_cover_every_tile_once_and_partials_have_slots_of_their_own(seed)
             assert v["slots"] == {2 * c + (1 if c == first else 0): c for c in range(first, last + 1)}
 
 
-UNIT = 8
-
-
+@pytest.mark.parametrize("unit", [4, 8])
 @pytest.mark.parametrize("seed", range(60))
-def test_in_place_moves_never_overwrite_an_unread_block(seed):
-    """The eviction's ordering rule: units (UNIT destination blocks) are claimed in
+def test_in_place_moves_never_overwrite_an_unread_block(seed, unit):
+    """The eviction's ordering rule: units (unit destination blocks) are claimed in
     order, each reads its blocks, then waits only for the lower units that took
     blocks out of its place, then writes.  Any interleaving of the claimed units
     leaves every kept block in its place, and every wait is for a lower unit."""
@@ -250,8 +248,8 @@ def test_in_place_moves_never_overwrite_an_unread_block(seed):
     moved = keep + ([nb] if tail else [])
     if not moved:
         return
-    pages = -(-len(moved) // UNIT)
-    rank = [sum(1 for b in keep if b < UNIT * p) for p in range(nb // UNIT + 3)]
+    pages = -(-len(moved) // unit)
+    rank = [sum(1 for b in keep if b < unit * p) for p in range(nb // unit + 3)]
     state, data, resident = {}, {}, rng.randint(1, 6)
     claimed, done_read, finished = 0, set(), set()
     while len(finished) < pages:
@@ -264,13 +262,13 @@ def test_in_place_moves_never_overwrite_an_unread_block(seed):
                 moves.append(("read", p))
             else:
                 k0, k1 = rank[p], rank[p + 1]
-                waits = range(k0 // UNIT, min(p - 1, (k1 - 1) // UNIT) + 1) if k1 > k0 else []
+                waits = range(k0 // unit, min(p - 1, (k1 - 1) // unit) + 1) if k1 > k0 else []
                 assert all(w < p for w in waits)
                 if all(w in done_read for w in waits):
                     moves.append(("write", p))
         assert moves, "a wait that never ends"
         what, p = rng.choice(moves)
-        span = range(UNIT * p, min(UNIT * p + UNIT, len(moved)))
+        span = range(unit * p, min(unit * p + unit, len(moved)))
         if what == "claim":
             claimed += 1
         elif what == "read":
@@ -281,6 +279,9 @@ def test_in_place_moves_never_overwrite_an_unread_block(seed):
                 slots[k] = x
             finished.add(p)
     assert slots[:len(moved)] == moved
+
+
+UNIT = 8
 
 
 @pytest.mark.parametrize("seed", range(40))
