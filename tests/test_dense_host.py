@@ -235,8 +235,8 @@ def test_shares_cover_every_tile_once_and_partials_have_slots_of_their_own(seed)
 @pytest.mark.parametrize("unit", [4, 8])
 @pytest.mark.parametrize("seed", range(60))
 def test_in_place_moves_never_overwrite_an_unread_block(seed, unit):
-    """The eviction's ordering rule: units (unit destination blocks) are claimed in
-    order, each reads its blocks, then waits only for the lower units that took
+    """The eviction's ordering rule: units (of 4 or 8 destination blocks) are
+    claimed in order, each reads its blocks, then waits only for the lower units that took
     blocks out of its place, then writes.  Any interleaving of the claimed units
     leaves every kept block in its place, and every wait is for a lower unit."""
     rng = random.Random(seed)

@@ -605,6 +605,14 @@ def test_evict_in_place_random(seed):
                 ids=rng.sample(range(7), 5), alias=True)
 
 
+@pytest.mark.parametrize("to_free", [False, True])
+def test_evict_pages_past_four_gigabytes(to_free):
+    pages = 140000                                            # 32 KiB a page
+    grp = Group([700, 90], 1, seed=8, num_pages=pages, first_page=pages - 26, spare=13)
+    mass = masses(random.Random(3), (2, grp.cache.max_pages_per_seq * 16))
+    check_evict(grp, 60, 2, 8, mass, to_free=to_free, alias=True)
+
+
 @pytest.mark.parametrize("n", [2, 40, 128, 129, 300])
 @pytest.mark.parametrize("to_free", [False, True])
 def test_evict_many_entries_cut_uncut_and_empty(n, to_free):
