@@ -34,7 +34,7 @@
 //   8 x 33K-50K tokens to 8,192 blocks, 2 heads      192 us   88%; in place 2% more
 //   48 x 4.3K-4.9K tokens to 1,024 blocks, 1 head     81 us   81%; 10 us of it selection;
 //                                                             in place 7% more
-//   1 x 4,163 tokens to 1,024 blocks, 2 heads         13 us   of it 6 selection, 6 moves
+//   1 x 4,163 tokens to 1,024 blocks, 2 heads         12 us   of it 6 selection, 5 moves
 #include "qsa_common.cuh"
 
 namespace {
@@ -620,7 +620,9 @@ int launch_select(const EvictArgs& a, int ctas, int room, size_t smem, cudaStrea
 
 template <int kRunBytes, int kUnit, int kWorkers>
 int launch_move(const EvictArgs& a, int units, int sms, cudaStream_t s) {
-  constexpr int smem = MoveLay<kRunBytes, kUnit, kWorkers>::kSmem;
+  // never two CTAs on an SM: launched early, those of a small call would pile up (one
+  // sequence of 4,163 tokens: 13.5 us so, 11.8 with one each)
+  constexpr int need = MoveLay<kRunBytes, kUnit, kWorkers>::kSmem, smem = need > kOnePerSm ? need : kOnePerSm;
   const auto kernel = a.dst_table == a.c.block_table ? evict_move_kernel<kRunBytes, kUnit, kWorkers, true>
                                                      : evict_move_kernel<kRunBytes, kUnit, kWorkers, false>;
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) {
@@ -690,8 +692,8 @@ extern "C" int qsa_evict(const qsa_cache_t* cache, const int32_t* dst_table, con
   }
   // Buffers per SM: 6 units of 8 blocks (BF16) or 12 keep the memory busy.  A call of at
   // most two such units per SM ends sooner with 4 of half the size: they spread more
-  // evenly, and the first stores start earlier (one sequence of 4,163 tokens in a
-  // graph: 11.4 us, 12.7 with 2 of full size, 12.9 with 3 of half)
+  // evenly, and the first stores start earlier (one sequence of 4,163 tokens, two
+  // CTAs an SM allowed, in a graph: 11.4 us, 12.7 with 2 of full size, 12.9 with 3 of half)
   a.units = units_of(c, budget, kUnitBlocks);
   const bool few = (int64_t)n * c.num_kv_heads * a.units <= 2 * sms;
   if (few) a.units = units_of(c, budget, kSmallUnit);
