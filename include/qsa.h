@@ -472,7 +472,8 @@ QSA_API int qsa_rope(const qsa_rope_plan_t* plan, const qsa_rope_tensor_t* tenso
  *                  + sum_{queries q of s} sum_h sum_{t in block b} exp(z_t - lse)
  * for every block b that a query of s sees (the open block too); the rest of
  * mass_out is left as it was.  mass_out may be mass_in.
- *   q bf16 [nq][hq][256]; out bf16 [nq][hq][256]; lse fp32 [nq][hq]
+ *   q bf16 [nq][hq][256] (16-byte aligned); out bf16 [nq][hq][256] (8-byte
+ *   aligned); lse fp32 [nq][hq]
  *   mass_in, mass_out fp32 [max_seqs][mass_ld] (both or neither), mass_ld >=
  *   max_pages_per_seq * 16
  *   workspace  256-byte aligned, at least qsa_dense_decode_workspace_bytes (its

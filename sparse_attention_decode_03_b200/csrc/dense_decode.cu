@@ -710,9 +710,9 @@ __device__ void consumers(const DenseArgs& a, uint8_t* smem, Walk w, const Share
 #pragma unroll
           for (int k = 0; k < 8; ++k) y[k] = o[i0 + k][2 * hr + e] * f;
           const size_t at = (out_row + gq + 8 * hr) * kHeadDim + dim;
-          if (direct) {
-            *reinterpret_cast<uint4*>(a.out + at) = make_uint4(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]),
-                                                               pack_bf16(y[4], y[5]), pack_bf16(y[6], y[7]));
+          if (direct) {  // out is 8-byte aligned
+            *reinterpret_cast<uint2*>(a.out + at) = make_uint2(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]));
+            *reinterpret_cast<uint2*>(a.out + at + 4) = make_uint2(pack_bf16(y[4], y[5]), pack_bf16(y[6], y[7]));
           } else {
             *reinterpret_cast<float4*>(a.part_o + at) = make_float4(y[0], y[1], y[2], y[3]);
             *reinterpret_cast<float4*>(a.part_o + at + 4) = make_float4(y[4], y[5], y[6], y[7]);
