@@ -70,8 +70,13 @@ constexpr int kQRows = 32, kMaxQ = 6;
 constexpr int kBarConsumers = 1;
 // The running maximum a warp subtracts may lag the true one by this much (base
 // 2), so that O is seldom rescaled: exp2 stays below 2^8, harmless in fp32 sums
-// and in the BF16 / FP16 weights, whose precision is relative.
+// and in the BF16 weights, whose precision is relative.
 constexpr float kLag = 8.f;
+// e4m3 V takes FP16 weights, whose precision is relative from 2^-14 up only.  What is
+// subtracted lies 7 below the running maximum there, so the largest weights are between
+// 2^7 and 2^15 and a tile may hold weights down to 2^-21 of theirs; one with a smaller
+// weight takes the wide form (see weigh).
+constexpr float kLeastF16 = 0x1p-14f;
 
 // BF16: runs lie in shared memory as in the cache (128-byte swizzled rows), a
 // plain bulk copy each tile.  e4m3: the cache's rows are plain; a tensor-map copy
@@ -88,6 +93,7 @@ struct Lay {
   static constexpr int kRunBytes = 2 * kRatio * kHeadDim * (F8 ? 1 : 2);
   static constexpr int kStageBytes = kTileRuns * kRunBytes;
   static constexpr int kStages = F8 ? 24 : 12;
+  static constexpr float kBias = F8 ? 7.f : 0.f;  // weights are relative to 2^(maximum - kBias): see kLeastF16
   // Tile T and tile T + kStages, which reuses its stage, belong to one warp: it has
   // seen the stage's last phase end before it waits for the next.  A parity wait
   // cannot tell a phase from the one two before, so another warp could run ahead.
@@ -101,7 +107,8 @@ struct Lay {
   static constexpr int kOffTab = kOffPlan + 16 * 8;             // (len, seq) of queries q0 ..
   static constexpr int kOffBar = kOffTab + kTab * 8;            // full, empty, Q full, Q empty
   static constexpr int kOffAbort = kOffBar + 2 * (kStages + kMaxQ) * 8;
-  static constexpr int kSmem = kOffAbort + 16;
+  static constexpr int kOffWide = kOffAbort + 16;               // e4m3: each warp's wide weights, hi and lo
+  static constexpr int kSmem = kOffWide + (F8 ? kWarps * 1024 : 0);
   static constexpr int kIssue = F8 ? 8 : 3;  // copy-warp lanes that wait and issue together, a tile each
   static_assert(kSmem <= 232448, "shared memory budget");
   static constexpr int kRounds = F8 ? 2 : 1;  // the join puts O into a held stage in so many parts
@@ -360,6 +367,12 @@ __device__ __forceinline__ float exp2_fast(float x) {
   return y;
 }
 
+// Two FP16 values that are e4m3 values, as BF16: exact, NaN stays NaN.
+__device__ __forceinline__ uint32_t f16x2_to_bf16x2(uint32_t h) {
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+  return pack_bf16(f.x, f.y);
+}
+
 // Which token of the tile a lane's logits and V rows belong to: columns n = 2tq + e of
 // S's n-tile j (lane tq of each quad holds e = 0, 1) are micro-block 2j + e, row tq ^ e
 // (BF16) or tq ^ 2e (e4m3).  K's columns n, n + 1 are then read from rows whose swizzles
@@ -387,6 +400,7 @@ __device__ void consumers(const DenseArgs& a, uint8_t* smem, Walk w, const Share
   constexpr int kWarps = LY::kWarps, kConsumerThreads = LY::kConsumerThreads;
   const int G = a.G;
   const int64_t max_tiles = (int64_t)a.mpps * kTilesPerPage;
+  const uint32_t wide_at = smem_u32(smem + LY::kOffWide) + warp * 1024 + lane * 16;
 
   // K: column n = gq of n-tile j, V: this lane's tokens (j, e)
   const int ke = gq & 1, kr = tile_row<F8>(gq >> 1, ke);
@@ -518,8 +532,14 @@ __device__ void consumers(const DenseArgs& a, uint8_t* smem, Walk w, const Share
     };
     // ---- S to weights: mask, running maximum and sum (base 2; the scale is positive, so the
     // largest product is the largest logit).  BF16 V: the weights leave as a BF16 hi + lo
-    // pair (about 17 significant bits; 8 alone would show in short contexts).  e4m3 V: FP16
-    // weights (at most 2^8), 11 bits against the cache's 4.
+    // pair (about 17 significant bits; 8 alone would show in short contexts).  e4m3 V: as
+    // FP16, 11 bits against the cache's 4, while all of the tile's are normal numbers (an
+    // FP16 hi + lo pair took 7% more time on long batches).  Otherwise the tile is wide (the
+    // result): the BF16 pair, whose exponents are fp32's.  Below a key that outweighs all
+    // others and whose value is near 0, the output is made of weights that FP16 would
+    // round coarsely, or drop while l counts them.  The test and the second form cost 4%
+    // where no tile is wide (64 x 16K-131K tokens, 12/1 heads: 391 -> 409 us) and 24% more
+    // where all are (507).
     auto weigh = [&](int ti, int nv, float(&p)[2][4], uint32_t(&pa)[4], uint32_t(&pl)[4]) {
       auto seen = [&](int j, int e) { return tile_run(j, e) * kRatio + tile_row<F8>(tq, e) < nv; };
       if (nv != kTile) {
@@ -535,9 +555,10 @@ __device__ void consumers(const DenseArgs& a, uint8_t* smem, Walk w, const Share
       r1 = fmaxf(r1, __shfl_xor_sync(0xffffffffu, r1, 1));
       r0 = fmaxf(r0, __shfl_xor_sync(0xffffffffu, r0, 2)) * sc0;
       r1 = fmaxf(r1, __shfl_xor_sync(0xffffffffu, r1, 2)) * sc1;
-      const bool up0 = r0 > m0 + kLag, up1 = r1 > m1 + kLag;  // -inf + 8 = -inf: the first logit always moves it
+      // -inf + kLag = -inf: the first logit always moves it
+      const bool up0 = r0 > m0 + (kLag + LY::kBias), up1 = r1 > m1 + (kLag + LY::kBias);
       if (__any_sync(0xffffffffu, up0 || up1)) {
-        const float n0 = up0 ? r0 : m0, n1 = up1 ? r1 : m1;
+        const float n0 = up0 ? r0 - LY::kBias : m0, n1 = up1 ? r1 - LY::kBias : m1;
         const float al0 = up0 ? exp2_fast(m0 - n0) : 1.f, al1 = up1 ? exp2_fast(m1 - n1) : 1.f;
         m0 = n0;
         m1 = n1;
@@ -560,13 +581,20 @@ __device__ void consumers(const DenseArgs& a, uint8_t* smem, Walk w, const Share
         p[j][2] = exp2_fast(fmaf(p[j][2], sc1, sub1));
         p[j][3] = exp2_fast(fmaf(p[j][3], sc1, sub1));
       }
+      auto least4 = [&](int j) { return fminf(fminf(p[j][0], p[j][1]), fminf(p[j][2], p[j][3])); };
+      float least = fminf(least4(0), least4(1));  // of the lane's weights
       if (nv != kTile) {  // also where a scale has underflowed to 0
+        least = 1.f;
 #pragma unroll
         for (int j = 0; j < 2; ++j)
 #pragma unroll
           for (int e = 0; e < 2; ++e)
-            if (!seen(j, e)) p[j][e] = p[j][2 + e] = 0.f;
+            if (seen(j, e))
+              least = fminf(least, fminf(p[j][e], p[j][2 + e]));
+            else
+              p[j][e] = p[j][2 + e] = 0.f;
       }
+      const bool wide = F8 && __any_sync(0xffffffffu, least < kLeastF16);
       l0 += (p[0][0] + p[0][1]) + (p[1][0] + p[1][1]);
       l1 += (p[0][2] + p[0][3]) + (p[1][2] + p[1][3]);
       // weight of each micro-block: sums over its 4 tokens, one per quad lane (run 2j + e
@@ -591,6 +619,14 @@ __device__ void consumers(const DenseArgs& a, uint8_t* smem, Walk w, const Share
           if (tq == 0) a.bmax[at] = m1;
         }
       }
+      if (F8 && wide) {  // the pair waits in shared memory: O leaves no registers for it
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) split_bf16(p[k >> 1][2 * (k & 1)], p[k >> 1][2 * (k & 1) + 1], hi[k], lo[k]);
+        sts128(wide_at, make_uint4(hi[0], hi[1], hi[2], hi[3]));
+        sts128(wide_at + 512, make_uint4(lo[0], lo[1], lo[2], lo[3]));
+        return true;
+      }
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const float x = p[k >> 1][2 * (k & 1)], y = p[k >> 1][2 * (k & 1) + 1];
@@ -601,6 +637,7 @@ __device__ void consumers(const DenseArgs& a, uint8_t* smem, Walk w, const Share
           split_bf16(x, y, pa[k], pl[k]);
         }
       }
+      return false;
     };
     // ---- O += P V of the tile at kb
     auto add_values = [&](uint32_t kb, int nv, const uint32_t(&pa)[4], const uint32_t(&pl)[4]) {
@@ -644,6 +681,39 @@ __device__ void consumers(const DenseArgs& a, uint8_t* smem, Walk w, const Share
         }
       }
     };
+    // the same of an e4m3 tile with wide weights: V as BF16
+    auto add_values_wide = [&](uint32_t kb, int nv) {
+      const uint4 hi = lds128(wide_at), lo = lds128(wide_at + 512);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {  // 8 of a chunk's 16 dims
+        const int part = c >> 1, r0 = 2 * (c & 1);
+        uint32_t x[2][2][2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const uint32_t at = kb + (v_off[j][e] ^ (part * (128 + 16))) + r0 * 4;
+            const bool off = nv != kTile && tile_run(j, e) * kRatio + tile_row<F8>(tq, e) >= nv;
+            const uint2 v = lds64(at);
+            x[j][e][0] = off ? 0 : v.x;
+            x[j][e][1] = off ? 0 : v.y;
+          }
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const uint2 t = e4m3x4_to_f16x4(__byte_perm(x[0][0][r], x[0][1][r], k ? 0x7362 : 0x5140));
+            const uint2 u = e4m3x4_to_f16x4(__byte_perm(x[1][0][r], x[1][1][r], k ? 0x7362 : 0x5140));
+            float(&o0)[4] = o[part * 16 + 4 * (r0 + r) + 2 * k], (&o1)[4] = o[part * 16 + 4 * (r0 + r) + 2 * k + 1];
+            const uint32_t b0 = f16x2_to_bf16x2(t.x), b1 = f16x2_to_bf16x2(u.x);
+            mma_bf16_16816(o0, hi.x, hi.y, hi.z, hi.w, b0, b1);
+            mma_bf16_16816(o0, lo.x, lo.y, lo.z, lo.w, b0, b1);
+            const uint32_t b2 = f16x2_to_bf16x2(t.y), b3 = f16x2_to_bf16x2(u.y);
+            mma_bf16_16816(o1, hi.x, hi.y, hi.z, hi.w, b2, b3);
+            mma_bf16_16816(o1, lo.x, lo.y, lo.z, lo.w, b2, b3);
+          }
+      }
+    };
     for (int ti = rank; ti < n_tiles; ti += kWarps) {
       const int stage = landed(ti);
       if (stage < 0) break;
@@ -652,8 +722,11 @@ __device__ void consumers(const DenseArgs& a, uint8_t* smem, Walk w, const Share
       float s[2][4];
       uint32_t pa[4], pl[4];
       products(kb, s);
-      weigh(ti, nv, s, pa, pl);
-      add_values(kb, nv, pa, pl);
+      const bool wide = weigh(ti, nv, s, pa, pl);
+      if (F8 && wide)
+        add_values_wide(kb, nv);
+      else
+        add_values(kb, nv, pa, pl);
       held = stage;
       if (ti + kWarps < n_tiles) {  // the last stage is kept for the join
         __syncwarp();

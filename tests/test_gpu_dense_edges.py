@@ -2,14 +2,17 @@
 accept: alignment, ranges of weights and queries, tables that mix a sequence's
 own pages with others, several streams.  References and bounds: dense_ref.py,
 and the ones stated beside each test."""
+import numpy as np
 import pytest
 import torch
+
+from tests import dense_ref as D
 
 pytestmark = pytest.mark.gpu
 
 qsa = pytest.importorskip("sparse_attention_decode_03_b200")
 
-from tests.test_gpu_dense import Group, bits, i32, queries  # noqa: E402
+from tests.test_gpu_dense import Group, bits, i32, queries, within  # noqa: E402
 
 
 @pytest.fixture(autouse=True, scope="module")
@@ -42,3 +45,83 @@ def test_dense_decode_writes_outputs_that_are_8_byte_aligned(hq, hkv, fp8):
         assert (buf[:shift] == 7.0).all() and (buf[shift + n:] == 7.0).all()       # nothing beside the rows
         assert (stats[:shift // 4] == 7.0).all() and (stats[shift // 4 + nq * hq:] == 7.0).all()
     assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+
+
+# ---------------------------------------------------------------- one key far above the others
+
+
+def rewrite(grp, s, k, v):
+    """Give sequence s of a group other K and V rows."""
+    grp.k[s], grp.v[s] = k.bfloat16(), v.bfloat16()
+    grp.append(s, 0, grp.k[s], grp.v[s], grp.ki[s])
+
+
+def check_rows(grp, q, lens):
+    """A tracked step of every sequence against 64 bits.  Bounds: dense_ref's for logits and sums, and for each
+    weight half an FP16 step of its own size (an e4m3 cache's; BF16 pairs are finer), however small it is."""
+    nq, hq = q.shape[:2]
+    dec = qsa.DenseDecoder(grp.cache, hq, nq, track=True)
+    out, lse = dec.run(q.cuda(), i32(list(range(nq))), i32([n - 1 for n in lens]))
+    torch.cuda.synchronize()
+    assert int(dec.dev_status.item()) == 0
+    group = hq // grp.hkv
+    for s, n in enumerate(lens):
+        k, v = (x[:n] for x in grp.rows(s))
+        o, l, w, ob, lb, wb = D.dense(q[s].double().numpy(), k, v, 1 / 16, False)
+        for h in range(hq):
+            z = k[:, h // group] @ q[s, h].double().numpy() / 16
+            ob[h] += D.FP16 * (np.exp(z - l[h]) @ np.abs(v[:, h // group]))
+        within(out[s].double().cpu().numpy(), o, ob, f"sequence {s}: out")
+        within(lse[s].double().cpu().numpy(), l, lb, f"sequence {s}: lse")
+        nb = -(-n // 4)
+        within(dec.mass[s, :nb].double().cpu().numpy(), D.block_sums(w), D.block_sums(wb) +
+               2 * hq * D.FP32 * D.block_sums(w), "totals")
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("gap", [8, 12, 16, 18, 20, 30, 60])
+def test_dense_decode_weights_far_below_one_key_with_no_value(gap, fp8):
+    """A key `gap` nats above thousands of others, with V = 0: the output is made of the others' weights alone."""
+    lens, hq, hkv = [5000, 33000, 700, 30], 12, 1
+    grp = Group(lens, hkv, fp8, seed=gap)
+    g = torch.Generator().manual_seed(gap)
+    q = torch.empty((len(lens), hq, 256))
+    for s, n in enumerate(lens):
+        lead = torch.randn(256, generator=g)
+        q[s] = lead + 0.2 * torch.randn((hq, 256), generator=g)
+        k, v = torch.randn((n, hkv, 256), generator=g), 1.0 + 0.4 * torch.randn((n, hkv, 256), generator=g)
+        at = [0, n // 2, n - 1, 5][s]                   # the first, a middle, the last key
+        k[at, 0], v[at] = lead * (16 * gap / (lead * lead).sum()), 0.0
+        rewrite(grp, s, k, v)
+    check_rows(grp, q.bfloat16(), lens)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("spread", [2.0, 6.0, 20.0])
+def test_dense_decode_weights_of_many_sizes(spread, fp8):
+    """Logits spread over tens of nats, so that tiles with and without tiny weights follow one another."""
+    lens = [3000, 9001, 64, 17]
+    grp = Group(lens, 2, fp8, seed=int(spread))
+    for s, n in enumerate(lens):
+        rewrite(grp, s, grp.k[s].float(), grp.v[s].float().abs())
+    check_rows(grp, queries(len(lens), 16, 5, spread), lens)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("gap", [0, 40])
+def test_dense_decode_keeps_a_nan_in_its_dims(gap, fp8):
+    """A NaN among the values reaches the outputs of its dims and no others, whatever form the weights take."""
+    lens, hq = [400, 5, 16], 6
+    grp = Group(lens, 1, fp8, seed=1)
+    q = queries(len(lens), hq, 2)
+    bad = torch.zeros(256, dtype=torch.bool)
+    bad[[0, 7, 100, 255]] = True
+    for s, n in enumerate(lens):
+        k, v = grp.k[s].float(), grp.v[s].float()
+        k[0, 0] += q[s].float().mean(0) * gap
+        v[n - 1, 0, bad] = float("nan")
+        rewrite(grp, s, k, v)
+    dec = qsa.DenseDecoder(grp.cache, hq, len(lens))
+    out, lse = dec.run(q.cuda(), i32([0, 1, 2]), i32([n - 1 for n in lens]))
+    torch.cuda.synchronize()
+    assert torch.equal(out.isnan().cpu(), bad.expand(len(lens), hq, 256)) and bool(lse.isfinite().all())
