@@ -444,8 +444,10 @@ __device__ void consumers(const DenseArgs& a, uint8_t* smem, Walk w, const Share
     float sc0 = a.scale_log2, sc1 = a.scale_log2;
     if constexpr (F8) {
       float* row_scale = scales + qi * 16;
-      // FP16 operands: each row is scaled by a power of two into FP16's range (exact down
-      // to 2^-38 of its largest element) and its logit scale takes the factor back
+      // FP16 operands: each row is scaled by a power of two that puts its largest element
+      // into [2^13, 2^14), and its logit scale takes the factor back.  An element is off by
+      // at most 2^-38 of the row's largest (half of FP16's smallest step), and exact from
+      // 2^-30 of it up, where FP16's steps of 2^-24 hold BF16's 8 bits
       for (int row = lone ? 0 : warp; row < G; row += lone ? 1 : kWarps) {
         const uint4 v = lds128(qb + row * kQStride + lane * 16);
         uint32_t x[4] = {v.x, v.y, v.z, v.w};
@@ -454,7 +456,8 @@ __device__ void consumers(const DenseArgs& a, uint8_t* smem, Walk w, const Share
         for (int e = 0; e < 4; ++e) mx = max(mx, max(x[e] & 0x7fffu, (x[e] >> 16) & 0x7fffu));
         mx = __reduce_max_sync(0xffffffffu, mx);
         const int ex = (int)(mx >> 7);  // biased exponent
-        const int up = (ex == 0 || ex == 255) ? 0 : max(-100, min(100, 127 + 13 - ex));
+        // -114 for the largest floats; 126 keeps 2^-up a normal number for the smallest
+        const int up = ex == 255 ? 0 : min(126, 127 + 13 - ex);
         const float f = __uint_as_float((uint32_t)(127 + up) << 23);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {

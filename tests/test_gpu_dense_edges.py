@@ -12,7 +12,7 @@ pytestmark = pytest.mark.gpu
 
 qsa = pytest.importorskip("sparse_attention_decode_03_b200")
 
-from tests.test_gpu_dense import Group, bits, i32, queries, within  # noqa: E402
+from tests.test_gpu_dense import Group, bits, check_dense, i32, queries, within  # noqa: E402
 
 
 @pytest.fixture(autouse=True, scope="module")
@@ -125,3 +125,16 @@ def test_dense_decode_keeps_a_nan_in_its_dims(gap, fp8):
     out, lse = dec.run(q.cuda(), i32([0, 1, 2]), i32([n - 1 for n in lens]))
     torch.cuda.synchronize()
     assert torch.equal(out.isnan().cpu(), bad.expand(len(lens), hq, 256)) and bool(lse.isfinite().all())
+
+
+# ---------------------------------------------------------------- queries at the ends of BF16's range
+
+
+@pytest.mark.parametrize("fp8,gain", [(True, 2.0 ** 118), (True, 2.0 ** 122), (True, 2.0 ** -100), (True, 2.0 ** -120),
+                                      (False, 2.0 ** 118)])
+def test_dense_decode_queries_at_the_ends_of_their_range(fp8, gain):
+    """Rows of |q| near 2^120 or 2^-120 under a scale that leaves ordinary logits; small elements in one row too."""
+    grp = Group([333, 40, 7], 1, fp8, seed=4)
+    q = queries(3, 6, 8, gain)
+    q[0, :, 128:] *= 2.0 ** -20
+    check_dense(grp, q, [0, 1, 2], [332, 39, 6], scale=1 / (16 * gain))
