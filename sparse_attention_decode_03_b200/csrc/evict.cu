@@ -524,7 +524,13 @@ __global__ void __launch_bounds__(kWorkers * 32) evict_move_kernel(EvictArgs a, 
     const bool has_dep = movers && dep <= now.p1;
     bool clear = !has_dep || ld_acquire(now.done + dep);
     if (movers) {
-      if (!mbar_wait_bounded(bar, parity, kWaitLimitNs)) sound = false;
+      if (!__all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, kWaitLimitNs))) {
+        // the blocks have not arrived: their flag stays down, so nobody overwrites them, and nothing
+        // is stored; one more bounded wait, so as not to leave with copies into this buffer in flight
+        if (lane == 0) flag(a.st, QSA_DEV_TIMEOUT);
+        mbar_wait_bounded(bar, parity, kWaitLimitNs);
+        break;
+      }
       parity ^= 1u;
     }
     const bool wait = !__all_sync(0xffffffffu, clear);
@@ -540,7 +546,7 @@ __global__ void __launch_bounds__(kWorkers * 32) evict_move_kernel(EvictArgs a, 
           }
       }
       sound = __all_sync(0xffffffffu, sound);
-      if (!sound) {  // never store what may be wrong; the buffer's copies have been waited for
+      if (!sound) {  // a lower unit has not read what lies there; the buffer's copies have arrived
         if (lane == 0) flag(a.st, QSA_DEV_TIMEOUT);
         break;
       }
