@@ -2,6 +2,8 @@
 accept: alignment, ranges of weights and queries, tables that mix a sequence's
 own pages with others, several streams.  References and bounds: dense_ref.py,
 and the ones stated beside each test."""
+import random
+
 import numpy as np
 import pytest
 import torch
@@ -12,7 +14,8 @@ pytestmark = pytest.mark.gpu
 
 qsa = pytest.importorskip("sparse_attention_decode_03_b200")
 
-from tests.test_gpu_dense import Group, bits, check_dense, i32, queries, within  # noqa: E402
+from tests.test_gpu_dense import (  # noqa: E402
+    Group, bits, check_dense, i32, masses, queries, snapshot, within)
 
 
 @pytest.fixture(autouse=True, scope="module")
@@ -138,3 +141,65 @@ def test_dense_decode_queries_at_the_ends_of_their_range(fp8, gain):
     q = queries(3, 6, 8, gain)
     q[0, :, 128:] *= 2.0 ** -20
     check_dense(grp, q, [0, 1, 2], [332, 39, 6], scale=1 / (16 * gain))
+
+
+# ---------------------------------------------------------------- eviction into tables that mix own pages with others
+
+
+OWN = {"copy": lambda P, n: True, "fresh then own": lambda P, n: P >= n // 2, "own then fresh": lambda P, n: P < n // 2,
+       "alternating": lambda P, n: P % 2 == 0, "one own": lambda P, n: P == n // 3, "every third fresh": lambda P, n: P % 3 != 1}
+
+
+@pytest.mark.parametrize("alias", [False, True])
+@pytest.mark.parametrize("fp8,hkv", [(False, 1), (False, 3), (True, 2)])
+@pytest.mark.parametrize("mix", list(OWN))
+def test_evict_into_tables_that_mix_own_pages_with_others(mix, fp8, hkv, alias):
+    """Rows of dst_table that name the sequence's own page at some places and spare pages at others: every moved
+    block, the pages that nothing may write, keep, lengths and totals.  Few units (4 blocks each) and many (8)."""
+    for lens, budget, sink, recent in (([2100, 67, 1300, 900], 150, 3, 20), ([9001, 12000, 4097, 30, 8000], 900, 0, 100),
+                                       ([7000 + 300 * i for i in range(12)], 1100, 16, 64)):
+        rng = random.Random(len(lens))
+        grp = Group(lens, hkv, fp8, seed=budget, spare=sum(-(-n // 64) for n in lens))
+        c, table = grp.cache, grp.cache.block_table.cpu()
+        mass = masses(rng, (len(lens), c.max_pages_per_seq * 16))
+        before = snapshot(c, c.block_table, lens)
+        dst, at, fresh = table.clone(), 0, set()
+        for s, n in enumerate(lens):
+            pages = -(-n // 64)
+            for P in range(pages):
+                if not OWN[mix](P, pages):
+                    dst[s, P] = grp.free[at]
+                    fresh.add((s, P))
+                    at += 1
+        spare = grp.free[at:].long().cuda()                     # named by no table
+        c.kv_pages.view(torch.uint8)[spare] = 0x5a
+        mass_in = mass.cuda()
+        mass_out = mass_in if alias else torch.full_like(mass_in, -9.0)
+        n = len(lens)
+        keep, seq_len = torch.empty((n, budget), dtype=torch.int32, device="cuda"), i32(lens)
+        cnt, new_len = torch.empty_like(seq_len), seq_len if alias else torch.empty_like(seq_len)
+        ws = torch.full((qsa.evict_workspace_bytes(c, n, budget),), 0xff, dtype=torch.uint8, device="cuda")
+        st = torch.zeros(1, dtype=torch.int32, device="cuda")
+        qsa.qsa_evict(c, i32(list(range(n))), seq_len, mass_in, mass_out, budget, sink, recent, keep, cnt, new_len, ws,
+                      dst_table=dst.cuda(), dev_status=st)
+        torch.cuda.synchronize()
+        assert int(st.item()) == 0
+        assert (c.kv_pages.view(torch.uint8)[spare] == 0x5a).all()
+        moved = []
+        for s, x in enumerate(lens):
+            kept = D.keep_blocks(mass[s].tolist(), x, budget, sink, recent)
+            assert keep[s].tolist() == kept + [-1] * (budget - len(kept))
+            assert int(cnt[s]) == len(kept) and int(new_len[s]) == 4 * len(kept) + x % 4
+            moved.append(kept + ([x // 4] if x % 4 else []))
+        after = snapshot(c, dst.cuda(), [4 * len(m) for m in moved])
+        old = snapshot(c, c.block_table, lens)
+        for s, m in enumerate(moved):
+            for was, now, left in zip(before[s], after[s], old[s]):
+                assert torch.equal(was[m], now), f"sequence {s}: rows differ"
+                for b in range(was.shape[0]):                   # places that no block went to keep what they held
+                    if (s, b // 16) in fresh or b >= len(m):
+                        assert torch.equal(was[b], left[b]), f"sequence {s}: block {b} changed"
+            got = mass_out[s].cpu()
+            want = torch.zeros(-(-lens[s] // 4))
+            want[:len(m)] = mass[s, m]
+            assert torch.equal(got[:len(want)].view(torch.int32), want.view(torch.int32))
