@@ -999,7 +999,13 @@ class DenseDecoder:
     ``track=True`` it also holds `mass`, the running attention weight of every
     micro-block (``decay`` of the old total is kept at each step), and
     :meth:`evict` cuts sequences to a budget by it.  A row of `mass` belongs to
-    the sequence in its slot: zero it when the slot goes to another."""
+    the sequence in its slot: zero it when the slot goes to another.
+
+    Calls share `mass`, the outputs and the workspace: :meth:`run` and
+    :meth:`evict` may take any stream, and each waits for the object's last call
+    and, given a stream, for the caller's current one.  Launches from
+    :meth:`bind`, and calls while their stream is captured, are put on their
+    stream as they are; order those yourself."""
 
     def __init__(self, cache: PagedCache, hq: int, max_nq: int, scale: float = 1.0 / 16.0, track: bool = False,
                  decay: float = 1.0):
@@ -1012,6 +1018,24 @@ class DenseDecoder:
         self.workspace = torch.empty(dense_decode_workspace_bytes(cache, max_nq, hq, track), dtype=torch.uint8,
                                      device=dev)
         self.dev_status = torch.zeros((1,), dtype=torch.int32, device=dev)
+        self._last = None  # the stream of the last run or evict
+
+    def _enter(self, stream) -> bool:
+        """Order a call behind the last one and the caller's current stream; whether it leaves that stream."""
+        raw = torch._C._cuda_getCurrentRawStream(self.workspace.device.index)
+        leaves = stream is not None and stream.cuda_stream != raw
+        if not leaves and self._last is not None and self._last.cuda_stream == raw:
+            return False  # the usual call, on the stream of the last one
+        current = torch.cuda.current_stream(self.workspace.device)
+        s = stream if leaves else current
+        with torch.cuda.stream(s):
+            captured = torch.cuda.is_current_stream_capturing()
+        if not captured:
+            for other in (current, self._last):
+                if other is not None and other != s:
+                    s.wait_stream(other)
+            self._last = s
+        return leaves
 
     def bind(self, q, q_seq, q_pos, stream=None) -> list:
         """The pre-bound launch of a step's attention, for a StepGraph."""
@@ -1023,7 +1047,9 @@ class DenseDecoder:
 
     def run(self, q, q_seq, q_pos, stream=None):
         """out [nq][hq][256] and lse [nq][hq] of the queries (views of this object's buffers)."""
-        self.bind(q, q_seq, q_pos, stream)[0]()
+        call = self.bind(q, q_seq, q_pos, stream)[0]
+        self._enter(stream)
+        call()
         nq = int(q_seq.shape[0])
         return self.out[:nq], self.lse[:nq]
 
@@ -1038,10 +1064,9 @@ class DenseDecoder:
         count = torch.empty((n,), dtype=torch.int32, device=dev)
         new_len = torch.empty((n,), dtype=torch.int32, device=dev)
         ws = torch.empty(evict_workspace_bytes(self.cache, n, budget), dtype=torch.uint8, device=dev)
-        if stream is not None:  # allocated on the current stream, used on this one
+        if self._enter(stream):  # allocated on the current stream, used on another
             for t in (keep, count, new_len, ws):
                 t.record_stream(stream)
-            stream.wait_stream(torch.cuda.current_stream(dev))
         qsa_evict(self.cache, seq_ids, seq_len, self.mass, self.mass, budget, sink, recent, keep, count, new_len, ws,
                   dst_table, self.dev_status, stream)
         return new_len, keep, count

@@ -203,3 +203,56 @@ def test_evict_into_tables_that_mix_own_pages_with_others(mix, fp8, hkv, alias):
             want = torch.zeros(-(-lens[s] // 4))
             want[:len(m)] = mass[s, m]
             assert torch.equal(got[:len(want)].view(torch.int32), want.view(torch.int32))
+
+
+# ---------------------------------------------------------------- streams of one decoder
+
+
+def test_dense_decoder_calls_on_several_streams_follow_one_another():
+    """Inputs made late on the current stream, a step on one side stream, an eviction on another and a step on the
+    current one: as if all were on one stream."""
+    lens, hq = [900, 640], 8
+    results = []
+    for apart in (False, True):
+        grp = Group(lens, 1, seed=2)
+        dec = qsa.DenseDecoder(grp.cache, hq, 2, track=True)
+        q1, q2 = queries(2, hq, 1).cuda(), queries(2, hq, 2).cuda()
+        q, seqs, pos = torch.zeros_like(q1), i32([0, 1]), i32([n - 1 for n in lens])
+        a, b = (torch.cuda.Stream(), torch.cuda.Stream()) if apart else (None, None)
+        torch.cuda.synchronize()
+        if apart:
+            torch.cuda._sleep(40_000_000)          # about 20 ms: what follows is enqueued long before it runs
+        q.copy_(q1)
+        dec.run(q, seqs, pos, stream=a)
+        new_len, keep, count = dec.evict(seqs, pos + 1, 100, 2, 10, stream=b)
+        if apart:
+            torch.cuda.current_stream().wait_stream(b)
+        out, lse = dec.run(q2, seqs, new_len - 1)
+        torch.cuda.synchronize()
+        assert int(dec.dev_status.item()) == 0
+        results.append([x.clone() for x in (out, lse, dec.mass, new_len, keep, count)])
+    for x, y in zip(*results):
+        assert torch.equal(bits(x), bits(y))
+
+
+def test_dense_decoder_runs_inside_a_capture():
+    """run and evict captured on a side stream, after calls on another one."""
+    lens, hq = [700, 333], 4
+    grp = Group(lens, 1, seed=3)
+    dec = qsa.DenseDecoder(grp.cache, hq, 2, track=True)
+    q, seqs, pos = queries(2, hq, 1).cuda(), i32([0, 1]), i32([n - 1 for n in lens])
+    out, lse = (x.clone() for x in dec.run(q, seqs, pos))
+    mass = dec.mass.clone()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        dec.mass.zero_()
+        dec.run(q, seqs, pos)
+        totals = dec.mass.clone()
+        _, keep, count = dec.evict(seqs, pos + 1, 1000)       # nothing to cut
+    dec.out.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(bits(dec.out), bits(out)) and torch.equal(bits(dec.lse), bits(lse))
+    assert torch.equal(bits(totals), bits(mass)) and count.tolist() == [n // 4 for n in lens]
