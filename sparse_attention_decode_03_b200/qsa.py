@@ -772,6 +772,14 @@ class StepPipeline:
 # eviction.  Every call has a bind_* form that checks its arguments once.
 
 
+def _as_c(fn: str, t, x):
+    """x as the C type t; an integer that t cannot hold is refused (ctypes would cut it to t's bits)."""
+    v = t(x)
+    if isinstance(x, int) and v.value != x:
+        raise ValueError(f"{fn}: {x} is beyond the {8 * ctypes.sizeof(t)} bits of its argument")
+    return v
+
+
 class LaunchCall:
     """A bound C entry point (see :class:`BoundCall`) that takes its stream when
     it is called: the one it was bound to, or the caller's current stream.  It
@@ -782,7 +790,7 @@ class LaunchCall:
         self.name = name
         self.fn = LIB[name]  # a function object of its own: its arguments are converted here, once
         self.fn.restype = ctypes.c_int
-        self.args = tuple(x if t is None or not isinstance(x, (int, float, type(None))) else t(x)
+        self.args = tuple(_as_c(name, t, x) if isinstance(x, (int, float, type(None))) else x
                           for x, t in zip(args, getattr(LIB, name).argtypes))
         self._keep = keep
         self.device = device.index if device.index is not None else torch.cuda.current_device()
@@ -902,8 +910,10 @@ def qsa_rope(plan: RopePlan, pos, inputs, outputs=None, stream=None):
 
 
 def dense_decode_workspace_bytes(cache: PagedCache, nq: int, hq: int, with_mass: bool = False) -> int:
-    r = LIB.qsa_dense_decode_workspace_bytes(ctypes.byref(cache.struct()), int(nq), int(hq), int(with_mass))
-    _check("qsa_dense_decode_workspace_bytes", r if r < 0 else QSA_OK)
+    fn = "qsa_dense_decode_workspace_bytes"
+    r = LIB.qsa_dense_decode_workspace_bytes(ctypes.byref(cache.struct()), _as_c(fn, ctypes.c_int32, int(nq)),
+                                             _as_c(fn, ctypes.c_int32, int(hq)), int(with_mass))
+    _check(fn, r if r < 0 else QSA_OK)
     return r
 
 
@@ -955,8 +965,10 @@ def qsa_dense_decode(cache: PagedCache, q, q_seq, q_pos, scale: float, out, lse,
 
 
 def evict_workspace_bytes(cache: PagedCache, n: int, budget: int) -> int:
-    r = LIB.qsa_evict_workspace_bytes(ctypes.byref(cache.struct()), int(n), int(budget))
-    _check("qsa_evict_workspace_bytes", r if r < 0 else QSA_OK)
+    fn = "qsa_evict_workspace_bytes"
+    r = LIB.qsa_evict_workspace_bytes(ctypes.byref(cache.struct()), _as_c(fn, ctypes.c_int32, int(n)),
+                                      _as_c(fn, ctypes.c_int32, int(budget)))
+    _check(fn, r if r < 0 else QSA_OK)
     return r
 
 
