@@ -944,7 +944,7 @@ def bind_dense_decode(cache: PagedCache, q, q_seq, q_pos, scale: float, out, lse
     _status(dev_status)
     ws = _workspace_ptr(workspace, dense_decode_workspace_bytes(cache, nq, hq, ld > 0))
     _same_device(q.device, q_seq=q_seq, q_pos=q_pos, out=out, lse=lse, workspace=workspace, mass_in=mass_in,
-                 mass_out=mass_out, dev_status=dev_status, kv_pages=cache.kv_pages)
+                 mass_out=mass_out, dev_status=dev_status, kv_pages=cache.kv_pages, block_table=cache.block_table)
     st = cache.struct()
     return LaunchCall("qsa_dense_decode",
                       (ctypes.byref(st), _ptr(q), nq, hq, _ptr(q_seq), _ptr(q_pos), float(scale), _ptr(out),
@@ -986,7 +986,8 @@ def bind_evict(cache: PagedCache, seq_ids, seq_len, mass_in, mass_out, budget: i
     ws = _workspace_ptr(workspace, evict_workspace_bytes(cache, n, budget))
     _same_device(seq_ids.device, seq_len=seq_len, mass_in=mass_in, mass_out=mass_out, keep=keep,
                  keep_count=keep_count, new_len=new_len, workspace=workspace, dst_table=dst_table,
-                 dev_status=dev_status, block_table=cache.block_table)
+                 dev_status=dev_status, block_table=cache.block_table, kv_pages=cache.kv_pages,
+                 kc_pages=cache.kc_pages)
     st = cache.struct()
     return LaunchCall("qsa_evict",
                       (ctypes.byref(st), _ptr(dst_table), _ptr(seq_ids), _ptr(seq_len), n, _ptr(mass_in),

@@ -41,3 +41,23 @@ def test_workspace_sizes_of_counts_beyond_32_bits_are_refused():
                 call(big)
         with pytest.raises(qsa.QSAError):
             call(-1)
+
+
+def group(**elsewhere):
+    """A cache group of CPU tensors, those named on another device."""
+    t = dict(kv_pages=torch.empty(1), kc_pages=torch.empty(1), block_table=torch.empty(1))
+    t.update({k: torch.empty(1, device="meta") for k in elsewhere})
+    return types.SimpleNamespace(struct=lambda: STRUCT, max_pages_per_seq=4, max_seqs=2, **t)
+
+
+@pytest.mark.parametrize("name", ["kv_pages", "kc_pages", "block_table"])
+def test_buffers_of_the_group_on_another_device_are_refused(monkeypatch, name):
+    monkeypatch.setattr(Q, "_req", lambda t, *a: t)
+    i32, mass, byte = torch.zeros(2, dtype=torch.int32), torch.zeros(2, 64), torch.empty(1 << 24, dtype=torch.uint8)
+    cache = group(**{name: True})
+    with pytest.raises(ValueError, match=name):
+        qsa.bind_evict(cache, i32, i32, mass, mass, 16, 2, 4, i32, i32, i32, byte)
+    if name != "kc_pages":      # which dense decode does not read
+        q = torch.zeros(2, 4, 256)
+        with pytest.raises(ValueError, match=name):
+            qsa.bind_dense_decode(cache, q, i32, i32, 1 / 16, q, q, byte)
