@@ -30,14 +30,15 @@
 // tiles.  The copy warp resolves 32 tiles' pages at once, one batch ahead, a lane
 // each moves a tile, and it brings the Q rows of the next pairs.
 //
-// Measured on one B200 (time of the call, share of the 6.54 TB/s copy rate):
-//   BF16, 32 x 131,072 tokens, 24/2 heads     1,181 us   111%
-//   BF16, 8 x 32,768 tokens, 16/2 heads          85 us    97%
-//   e4m3, 64 x 16K-262K tokens, 12/1 heads      455 us    92%; power-capped at 1.7 GHz,
-//                                                         ALU 39%, tensor 34% of cycles
-//   BF16, 16 x 9K-16K tokens, 24/2, with totals   73 us    84%
-//   BF16, 1 x 4,096 tokens, 16/2                 10 us    of it 7 main kernel, 3 join
-//   BF16, 200 x 1-700 tokens, 3/1                15 us
+// Measured on one B200 (time of the call, share of the 6.54 TB/s copy rate; a range is
+// from a card at rest to one that has been busy):
+//   BF16, 32 x 131,072 tokens, 24/2 heads     1,181-1,246 us   105-111%
+//   BF16, 8 x 32,768 tokens, 16/2 heads          85-87 us      94-97%
+//   e4m3, 64 x 16K-262K tokens, 12/1 heads      495-525 us     80-85%; power-capped, ALU 38%,
+//                                                              tensor 32% of active cycles
+//   BF16, 16 x 9K-16K tokens, 24/2, with totals   73-75 us     82-84%
+//   BF16, 1 x 4,096 tokens, 16/2                  9.5 us       of it 7 main kernel, 3 join
+//   BF16, 200 x 1-700 tokens, 3/1                 15 us
 // What did not pay for e4m3: 6 or 7 consumers (512, 526 us then), 32-token tiles
 // (no change), one tile's products beside the last one's values (508 against 494),
 // e4m3 matrix instructions (25 to 38 cycles against 8 for FP16 ones of half the depth).
@@ -75,7 +76,7 @@ constexpr float kLag = 8.f;
 // e4m3 V takes FP16 weights, whose precision is relative from 2^-14 up only.  What is
 // subtracted lies 7 below the running maximum there, so the largest weights are between
 // 2^7 and 2^15 and a tile may hold weights down to 2^-21 of theirs; one with a smaller
-// weight takes the wide form (see weigh).
+// weight takes the wide form (see as_operand).
 constexpr float kLeastF16 = 0x1p-14f;
 
 // BF16: runs lie in shared memory as in the cache (128-byte swizzled rows), a
@@ -107,8 +108,7 @@ struct Lay {
   static constexpr int kOffTab = kOffPlan + 16 * 8;             // (len, seq) of queries q0 ..
   static constexpr int kOffBar = kOffTab + kTab * 8;            // full, empty, Q full, Q empty
   static constexpr int kOffAbort = kOffBar + 2 * (kStages + kMaxQ) * 8;
-  static constexpr int kOffWide = kOffAbort + 16;               // e4m3: each warp's wide weights, hi and lo
-  static constexpr int kSmem = kOffWide + (F8 ? kWarps * 1024 : 0);
+  static constexpr int kSmem = kOffAbort + 16;
   static constexpr int kIssue = F8 ? 8 : 3;  // copy-warp lanes that wait and issue together, a tile each
   static_assert(kSmem <= 232448, "shared memory budget");
   static constexpr int kRounds = F8 ? 2 : 1;  // the join puts O into a held stage in so many parts
@@ -400,7 +400,6 @@ __device__ void consumers(const DenseArgs& a, uint8_t* smem, Walk w, const Share
   constexpr int kWarps = LY::kWarps, kConsumerThreads = LY::kConsumerThreads;
   const int G = a.G;
   const int64_t max_tiles = (int64_t)a.mpps * kTilesPerPage;
-  const uint32_t wide_at = smem_u32(smem + LY::kOffWide) + warp * 1024 + lane * 16;
 
   // K: column n = gq of n-tile j, V: this lane's tokens (j, e)
   const int ke = gq & 1, kr = tile_row<F8>(gq >> 1, ke);
@@ -534,16 +533,9 @@ __device__ void consumers(const DenseArgs& a, uint8_t* smem, Walk w, const Share
       }
     };
     // ---- S to weights: mask, running maximum and sum (base 2; the scale is positive, so the
-    // largest product is the largest logit).  BF16 V: the weights leave as a BF16 hi + lo
-    // pair (about 17 significant bits; 8 alone would show in short contexts).  e4m3 V: as
-    // FP16, 11 bits against the cache's 4, while all of the tile's are normal numbers (an
-    // FP16 hi + lo pair took 7% more time on long batches).  Otherwise the tile is wide (the
-    // result): the BF16 pair, whose exponents are fp32's.  Below a key that outweighs all
-    // others and whose value is near 0, the output is made of weights that FP16 would
-    // round coarsely, or drop while l counts them.  The test and the second form cost 4%
-    // where no tile is wide (64 x 16K-131K tokens, 12/1 heads: 391 -> 409 us) and 24% more
-    // where all are (507).
-    auto weigh = [&](int ti, int nv, float(&p)[2][4], uint32_t(&pa)[4], uint32_t(&pl)[4]) {
+    // largest product is the largest logit).  The result: whether the tile is wide, that is,
+    // e4m3 V and a weight below FP16's normal numbers (see as_operand).
+    auto weigh = [&](int ti, int nv, float(&p)[2][4]) {
       auto seen = [&](int j, int e) { return tile_run(j, e) * kRatio + tile_row<F8>(tq, e) < nv; };
       if (nv != kTile) {
 #pragma unroll
@@ -622,25 +614,27 @@ __device__ void consumers(const DenseArgs& a, uint8_t* smem, Walk w, const Share
           if (tq == 0) a.bmax[at] = m1;
         }
       }
-      if (F8 && wide) {  // the pair waits in shared memory: O leaves no registers for it
-        uint32_t hi[4], lo[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) split_bf16(p[k >> 1][2 * (k & 1)], p[k >> 1][2 * (k & 1) + 1], hi[k], lo[k]);
-        sts128(wide_at, make_uint4(hi[0], hi[1], hi[2], hi[3]));
-        sts128(wide_at + 512, make_uint4(lo[0], lo[1], lo[2], lo[3]));
-        return true;
-      }
+      return wide;
+    };
+    // ---- weights to the operand of P V.  BF16 V: a BF16 hi + lo pair (about 17 significant
+    // bits; 8 alone would show in short contexts).  e4m3 V: FP16, 11 bits against the cache's
+    // 4, while all of the tile's weights are normal numbers (an FP16 hi + lo pair took 7%
+    // more time on long batches).  A wide tile takes the BF16 pair, whose exponents are
+    // fp32's, and V widened to BF16: below a key that outweighs all others and whose value
+    // is near 0, the output is made of weights that FP16 would round coarsely, or drop while
+    // l counts them.  The test and the second form cost 4% where no tile is wide (64 x
+    // 16K-131K tokens, 12/1 heads: 391 -> 409 us) and 24% more where all are (507).
+    auto as_operand = [&](const float(&p)[2][4], bool wide, uint32_t(&pa)[4], uint32_t(&pl)[4]) {
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const float x = p[k >> 1][2 * (k & 1)], y = p[k >> 1][2 * (k & 1) + 1];
-        if constexpr (F8) {
+        if (F8 && !wide) {
           const __half2 h = __floats2half2_rn(x, y);
           pa[k] = *reinterpret_cast<const uint32_t*>(&h);
         } else {
           split_bf16(x, y, pa[k], pl[k]);
         }
       }
-      return false;
     };
     // ---- O += P V of the tile at kb
     auto add_values = [&](uint32_t kb, int nv, const uint32_t(&pa)[4], const uint32_t(&pl)[4]) {
@@ -685,8 +679,7 @@ __device__ void consumers(const DenseArgs& a, uint8_t* smem, Walk w, const Share
       }
     };
     // the same of an e4m3 tile with wide weights: V as BF16
-    auto add_values_wide = [&](uint32_t kb, int nv) {
-      const uint4 hi = lds128(wide_at), lo = lds128(wide_at + 512);
+    auto add_values_wide = [&](uint32_t kb, int nv, const uint32_t(&pa)[4], const uint32_t(&pl)[4]) {
 #pragma unroll
       for (int c = 0; c < 4; ++c) {  // 8 of a chunk's 16 dims
         const int part = c >> 1, r0 = 2 * (c & 1);
@@ -709,11 +702,11 @@ __device__ void consumers(const DenseArgs& a, uint8_t* smem, Walk w, const Share
             const uint2 u = e4m3x4_to_f16x4(__byte_perm(x[1][0][r], x[1][1][r], k ? 0x7362 : 0x5140));
             float(&o0)[4] = o[part * 16 + 4 * (r0 + r) + 2 * k], (&o1)[4] = o[part * 16 + 4 * (r0 + r) + 2 * k + 1];
             const uint32_t b0 = f16x2_to_bf16x2(t.x), b1 = f16x2_to_bf16x2(u.x);
-            mma_bf16_16816(o0, hi.x, hi.y, hi.z, hi.w, b0, b1);
-            mma_bf16_16816(o0, lo.x, lo.y, lo.z, lo.w, b0, b1);
+            mma_bf16_16816(o0, pa[0], pa[1], pa[2], pa[3], b0, b1);
+            mma_bf16_16816(o0, pl[0], pl[1], pl[2], pl[3], b0, b1);
             const uint32_t b2 = f16x2_to_bf16x2(t.y), b3 = f16x2_to_bf16x2(u.y);
-            mma_bf16_16816(o1, hi.x, hi.y, hi.z, hi.w, b2, b3);
-            mma_bf16_16816(o1, lo.x, lo.y, lo.z, lo.w, b2, b3);
+            mma_bf16_16816(o1, pa[0], pa[1], pa[2], pa[3], b2, b3);
+            mma_bf16_16816(o1, pl[0], pl[1], pl[2], pl[3], b2, b3);
           }
       }
     };
@@ -725,11 +718,13 @@ __device__ void consumers(const DenseArgs& a, uint8_t* smem, Walk w, const Share
       float s[2][4];
       uint32_t pa[4], pl[4];
       products(kb, s);
-      const bool wide = weigh(ti, nv, s, pa, pl);
-      if (F8 && wide)
-        add_values_wide(kb, nv);
-      else
+      if (weigh(ti, nv, s)) {
+        as_operand(s, true, pa, pl);
+        add_values_wide(kb, nv, pa, pl);
+      } else {
+        as_operand(s, false, pa, pl);
         add_values(kb, nv, pa, pl);
+      }
       held = stage;
       if (ti + kWarps < n_tiles) {  // the last stage is kept for the join
         __syncwarp();
@@ -818,7 +813,8 @@ __device__ void consumers(const DenseArgs& a, uint8_t* smem, Walk w, const Share
       const float sub = M[hr] == -INFINITY ? 0.f : M[hr];
 #pragma unroll
       for (int v = 0; v < kWarps; ++v) L[hr] += e[v].y * exp2_fast(e[v].x - sub);
-      // L = 0: no token; a NaN stays one
+      // L = 0: no token; a NaN stays one.  The quotient is within 2 ulp: one of the fp32
+      // roundings of a row's factor, next to the BF16 rounding of out
       fac[hr] = L[hr] > 0.f ? __fdividef(exp2_fast((hr ? m1 : m0) - sub), L[hr]) : L[hr];
     }
     // O: every warp puts its own into the stage it holds, and a thread adds up float4s of
