@@ -28,7 +28,8 @@
  *
  * Conventions for every call
  *  - Pointers are DEVICE pointers owned and allocated by the caller, except
- *    the `cache` descriptor itself (host memory, read during the call only).
+ *    the `cache` descriptor itself and qsa_rope's `plan` and `tensors` (host
+ *    memory, read during the call only) and qsa_decode_plan's results.
  *    The library allocates nothing and never synchronises the host.
  *  - `stream` is a cudaStream_t (NULL = the legacy default stream); calls only
  *    enqueue work on it.
@@ -51,7 +52,8 @@
  *    skipped (masked); kernels never trap.  The caller clears and reads it.
  *  - All outputs are deterministic: no floating-point atomics.
  *  - Tensors are dense row-major with the shapes given; no strides (except
- *    qsa_combine_strided, which takes them explicitly).
+ *    qsa_combine_strided and qsa_rope, which take them explicitly, and the row
+ *    lengths scores_ld and mass_ld).
  */
 #ifndef QSA_H
 #define QSA_H
@@ -125,12 +127,12 @@ typedef enum {
  *               di sekitarnya tentang Qwen4Exp"), which halves the bytes the
  *               sparse attention gathers.  The side cache stays BF16.
  * All buffers are caller-owned device memory; the library writes kv/kc pages
- * and kc_partial only in qsa_append_kv.
+ * only in qsa_append_kv and qsa_evict, and kc_partial only in qsa_append_kv.
  * A group may leave out one part: kv_pages NULL (a selector-only group, e.g.
  * the replicated side cache of a DCP rank) or kc_pages and kc_partial NULL (a
  * main-K/V-only group, e.g. a DCP rank's K/V shard).  qsa_append_kv then
- * writes only the part that is there; qsa_index_scores needs kc_pages and
- * qsa_sparse_decode needs kv_pages.
+ * writes and qsa_evict moves only the part that is there; qsa_index_scores
+ * needs kc_pages, qsa_sparse_decode and qsa_dense_decode need kv_pages.
  */
 #define QSA_KV_BF16 0
 #define QSA_KV_FP8_E4M3 1
@@ -477,19 +479,27 @@ QSA_API int qsa_rope(const qsa_rope_plan_t* plan, const qsa_rope_tensor_t* tenso
  *   mass_in, mass_out fp32 [max_seqs][mass_ld] (both or neither), mass_ld >=
  *   max_pages_per_seq * 16
  *   workspace  256-byte aligned, at least qsa_dense_decode_workspace_bytes (its
- *              contents need no preparation): at most 8.5 MB, and with totals
- *              nq * hq * max_pages_per_seq * 80 bytes more; calls that share
- *              one must not overlap on the GPU, captured graphs included
+ *              contents need no preparation): at most 8.5 MB and 8 bytes a
+ *              (query, KV head) pair, and with totals nq * hq *
+ *              max_pages_per_seq * 80 bytes more, whatever the lengths; calls
+ *              that share one must not overlap on the GPU, captured graphs
+ *              included
  * A query with q_seq < 0 (padding) or q_pos == -1 (no tokens) gets out = 0 and
  * lse = -inf; so does, flagged, one whose sequence or position is out of range.
  * The 64 tokens of a page-table miss are left out and flagged; a query left
  * with no token gets out = 0 and lse = -inf.  Rows behind q_pos are never read
  * into a result, whatever they hold.  Several queries of one sequence are
- * allowed.  Splits depend on the lengths and the SM count alone: the same call
- * gives the same bits.
+ * allowed; each reads the K/V for itself, and with totals the blocks of the
+ * longest add up all of theirs, so a prompt chunk of hundreds is slow.  Splits
+ * depend on the lengths and the SM count alone: the same call gives the same
+ * bits.
  * Requirements: hq % Hkv == 0, hq / Hkv <= 16, scale > 0, nq * Hkv *
- * (max_pages_per_seq * 4 + 8) < 2^31; BF16 or FP8 K/V (for
- * FP8 each q row is scaled by a power of two into FP16's range).
+ * (max_pages_per_seq * 4 + 8) < 2^31; BF16 or FP8 K/V.  Logits, maxima, sums and
+ * totals are fp32.  BF16: the softmax weights enter the product with V as a
+ * BF16 hi + lo pair.  FP8: q rows are scaled by a power of two into FP16's range
+ * (each element off by at most 2^-38 of its row's largest), and the weights
+ * enter as FP16, 11 bits each; 16 tokens one of whose weights is below 2^-21 of
+ * the running maximum's take the BF16 pair.
  */
 QSA_API int64_t qsa_dense_decode_workspace_bytes(const qsa_cache_t* cache, int32_t nq, int32_t hq, int32_t with_mass);
 QSA_API int qsa_dense_decode(const qsa_cache_t* cache, const void* q, int32_t nq, int32_t hq, const int32_t* q_seq,

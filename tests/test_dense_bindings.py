@@ -61,3 +61,12 @@ def test_buffers_of_the_group_on_another_device_are_refused(monkeypatch, name):
         q = torch.zeros(2, 4, 256)
         with pytest.raises(ValueError, match=name):
             qsa.bind_dense_decode(cache, q, i32, i32, 1 / 16, q, q, byte)
+
+
+@pytest.mark.parametrize("nq,hq,hkv", [(1, 16, 1), (1, 128, 8), (9800, 16, 1), (20000, 128, 8), (300000, 4, 4)])
+def test_workspace_stays_within_the_stated_bound(nq, hq, hkv):
+    """8.5 MB and 8 bytes a (query, KV head) pair; with totals 80 bytes a query, head and page of the table more."""
+    st = Q.qsa_cache_t(0x1000, 0x1000, 0x1000, 0x1000, 10, 2, 4, hkv, 0)
+    cache = types.SimpleNamespace(struct=lambda: st)
+    need, totals = (qsa.dense_decode_workspace_bytes(cache, nq, hq, m) for m in (False, True))
+    assert need <= 8_500_000 + 8 * nq * hkv and totals - need <= 80 * nq * hq * 4 + 512
