@@ -30,11 +30,15 @@
 // lower ones first, and read before they wait, so the lowest unit at work
 // never waits and every wait ends.
 //
-// Measured on one B200 (time of the call, share of the 6.54 TB/s copy rate):
-//   8 x 33K-50K tokens to 8,192 blocks, 2 heads      192 us   88%; in place 2% more
+// Measured on one B200 (time of the call, share of the 6.54 TB/s copy rate; BF16 into
+// other pages, each pass among others; then the same with a cold L2, into other pages and
+// in place):
+//   8 x 33K-50K tokens to 8,192 blocks, 2 heads      192 us   88%; cold 197, in place 199
 //   48 x 4.3K-4.9K tokens to 1,024 blocks, 1 head     81 us   81%; 10 us of it selection;
-//                                                             in place 7% more
-//   1 x 4,163 tokens to 1,024 blocks, 2 heads         12 us   of it 6 selection, 5 moves
+//                                                             cold 84, in place 92
+//   1 x 4,163 tokens to 1,024 blocks, 2 heads         12 us   of it 6 selection, 5 moves;
+//                                                             cold 18, in place 20
+// e4m3, into other pages: 110, 52 and 11 us (floors 87, 35 and 1.4).
 #include "qsa_common.cuh"
 
 namespace {
