@@ -1033,12 +1033,13 @@ class DenseDecoder:
         self.dev_status = torch.zeros((1,), dtype=torch.int32, device=dev)
         self._last = None  # the stream of the last run or evict
 
-    def _enter(self, stream) -> bool:
-        """Order a call behind the last one and the caller's current stream; whether it leaves that stream."""
+    def _enter(self, stream, *tensors):
+        """Order a call behind the last one and the caller's current stream; `tensors`, allocated on that
+        stream, stay theirs until a call on another one has used them."""
         raw = torch._C._cuda_getCurrentRawStream(self.workspace.device.index)
         leaves = stream is not None and stream.cuda_stream != raw
         if not leaves and self._last is not None and self._last.cuda_stream == raw:
-            return False  # the usual call, on the stream of the last one
+            return  # the usual call, on the stream of the last one
         current = torch.cuda.current_stream(self.workspace.device)
         s = stream if leaves else current
         with torch.cuda.stream(s):
@@ -1048,7 +1049,10 @@ class DenseDecoder:
                 if other is not None and other != s:
                     s.wait_stream(other)
             self._last = s
-        return leaves
+        if leaves:
+            for t in tensors:
+                if t is not None:
+                    t.record_stream(s)
 
     def bind(self, q, q_seq, q_pos, stream=None) -> list:
         """The pre-bound launch of a step's attention, for a StepGraph."""
@@ -1061,7 +1065,7 @@ class DenseDecoder:
     def run(self, q, q_seq, q_pos, stream=None):
         """out [nq][hq][256] and lse [nq][hq] of the queries (views of this object's buffers)."""
         call = self.bind(q, q_seq, q_pos, stream)[0]
-        self._enter(stream)
+        self._enter(stream, q, q_seq, q_pos)
         call()
         nq = int(q_seq.shape[0])
         return self.out[:nq], self.lse[:nq]
@@ -1077,9 +1081,7 @@ class DenseDecoder:
         count = torch.empty((n,), dtype=torch.int32, device=dev)
         new_len = torch.empty((n,), dtype=torch.int32, device=dev)
         ws = torch.empty(evict_workspace_bytes(self.cache, n, budget), dtype=torch.uint8, device=dev)
-        if self._enter(stream):  # allocated on the current stream, used on another
-            for t in (keep, count, new_len, ws):
-                t.record_stream(stream)
+        self._enter(stream, seq_ids, seq_len, dst_table, keep, count, new_len, ws)
         qsa_evict(self.cache, seq_ids, seq_len, self.mass, self.mass, budget, sink, recent, keep, count, new_len, ws,
                   dst_table, self.dev_status, stream)
         return new_len, keep, count

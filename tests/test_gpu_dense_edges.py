@@ -256,3 +256,28 @@ def test_dense_decoder_runs_inside_a_capture():
     torch.cuda.synchronize()
     assert torch.equal(bits(dec.out), bits(out)) and torch.equal(bits(dec.lse), bits(lse))
     assert torch.equal(bits(totals), bits(mass)) and count.tolist() == [n // 4 for n in lens]
+
+
+def test_dense_decoder_keeps_a_side_streams_inputs():
+    """Inputs that the caller lets go of right after a call on a side stream are not handed out again before it ran."""
+    lens, hq = [900, 640], 8
+    results = []
+    for apart in (False, True):
+        grp = Group(lens, 1, seed=2)
+        dec = qsa.DenseDecoder(grp.cache, hq, 2, track=True)
+        q, side = queries(2, hq, 1).cuda(), torch.cuda.Stream() if apart else None
+        pos, n = i32([n - 1 for n in lens]), i32(lens)
+        torch.cuda.synchronize()
+        if apart:
+            with torch.cuda.stream(side):
+                torch.cuda._sleep(40_000_000)
+        out, lse = dec.run(q.clone(), i32([0, 1]), pos.clone(), stream=side)
+        # what takes the memory that came free: padding ids, which read nothing
+        taken = [torch.full((2,), -1, dtype=torch.int32, device="cuda") for _ in range(8)] + [torch.zeros_like(q) for _ in range(4)]
+        new_len, keep, count = dec.evict(i32([0, 1]), n.clone(), 100, 2, 10, stream=side)
+        taken += [torch.full((2,), -1, dtype=torch.int32, device="cuda") for _ in range(8)]
+        torch.cuda.synchronize()
+        assert int(dec.dev_status.item()) == 0
+        results.append([x.clone() for x in (out, lse, dec.mass, new_len, keep, count)])
+    for x, y in zip(*results):
+        assert torch.equal(bits(x), bits(y))
