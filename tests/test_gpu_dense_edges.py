@@ -281,3 +281,57 @@ def test_dense_decoder_keeps_a_side_streams_inputs():
         results.append([x.clone() for x in (out, lse, dec.mass, new_len, keep, count)])
     for x, y in zip(*results):
         assert torch.equal(bits(x), bits(y))
+
+
+# ---------------------------------------------------------------- queries that are not numbers; calls at once
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_dense_decode_keeps_a_bad_query_to_its_head(value, fp8):
+    """A NaN or an infinity in one head's query makes that head's row NaN (infinite logits of both signs) and no other."""
+    lens, hq, bad = [16, 700, 5000], 12, 5
+    grp = Group(lens, 1, fp8, seed=8)
+    q = queries(3, hq, 4)
+    q[:, bad, 17] = value
+    dec = qsa.DenseDecoder(grp.cache, hq, 3)
+    out, lse = dec.run(q.cuda(), i32([0, 1, 2]), i32([n - 1 for n in lens]))
+    torch.cuda.synchronize()
+    good = [h for h in range(hq) if h != bad]
+    assert bool(out[:, bad].isnan().all()) and bool(lse[:, bad].isnan().all())
+    for s, n in enumerate(lens):
+        k, v = grp.rows(s)
+        o, l, _, ob, lb, _ = D.dense(q[s, good].double().numpy(), k, v, 1 / 16, fp8)
+        within(out[s, good].double().cpu().numpy(), o, ob, f"sequence {s}: out")
+        within(lse[s, good].double().cpu().numpy(), l, lb, f"sequence {s}: lse")
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_evictions_and_steps_at_once(fp8):
+    """Two evictions in place of different sequences and a step of a third, on three streams with workspaces of their
+    own, again and again: the same bytes as one after the other."""
+    lens, budget, hq = [9000, 7001, 8003, 5000, 6002], 700, 6
+    results = []
+    for apart in (False, True):
+        grp = Group(lens, 1, fp8, seed=6)
+        c = grp.cache
+        mass = masses(random.Random(1), (len(lens), c.max_pages_per_seq * 16)).cuda()
+        q, decs = queries(1, hq, 3).cuda(), qsa.DenseDecoder(c, hq, 1)
+        args = []
+        for ids in ([0, 1], [2, 3]):
+            n, ws = len(ids), torch.empty(qsa.evict_workspace_bytes(c, 2, budget), dtype=torch.uint8, device="cuda")
+            args.append((i32(ids), i32([lens[s] for s in ids]), mass, mass, budget, 3, 40,
+                         torch.empty((n, budget), dtype=torch.int32, device="cuda"), *(torch.empty_like(i32(ids)) for _ in range(2)),
+                         ws))
+        step_args = (q, i32([4]), i32([lens[4] - 1]))
+        torch.cuda.synchronize()
+        s = [torch.cuda.Stream() for _ in range(3)] if apart else [None] * 3
+        out, lse = decs.run(*step_args, stream=s[2])
+        for call, st in zip(args, s):
+            qsa.qsa_evict(c, *call, stream=st)
+        for _ in range(20):
+            decs.run(*step_args, stream=s[2])
+        torch.cuda.synchronize()
+        results.append([bits(x) for x in (c.kv_pages.view(torch.uint8), c.kc_pages, mass, out, lse, args[0][7], args[1][7])])
+    for x, y in zip(*results):
+        assert torch.equal(x, y)
