@@ -1007,6 +1007,11 @@ def qsa_evict(cache: PagedCache, seq_ids, seq_len, mass_in, mass_out, budget: in
                workspace, dst_table, dev_status, stream)()
 
 
+def _capturing(stream) -> bool:
+    with torch.cuda.stream(stream):
+        return torch.cuda.is_current_stream_capturing()
+
+
 class DenseDecoder:
     """Outputs and workspace of qsa_dense_decode for up to `max_nq` queries.  With
     ``track=True`` it also holds `mass`, the running attention weight of every
@@ -1017,8 +1022,9 @@ class DenseDecoder:
     Calls share `mass`, the outputs and the workspace: :meth:`run` and
     :meth:`evict` may take any stream, and each waits for the object's last call
     and, given a stream, for the caller's current one.  Launches from
-    :meth:`bind`, and calls while their stream is captured, are put on their
-    stream as they are; order those yourself."""
+    :meth:`bind`, and calls that are captured, are put on their stream as they
+    are (one given a stream inside a capture branches off it); order those
+    yourself."""
 
     def __init__(self, cache: PagedCache, hq: int, max_nq: int, scale: float = 1.0 / 16.0, track: bool = False,
                  decay: float = 1.0):
@@ -1042,9 +1048,10 @@ class DenseDecoder:
             return  # the usual call, on the stream of the last one
         current = torch.cuda.current_stream(self.workspace.device)
         s = stream if leaves else current
-        with torch.cuda.stream(s):
-            captured = torch.cuda.is_current_stream_capturing()
-        if not captured:
+        if _capturing(current):
+            if leaves:
+                s.wait_stream(current)  # a branch of the capture, which the caller joins
+        elif not _capturing(s):
             for other in (current, self._last):
                 if other is not None and other != s:
                     s.wait_stream(other)

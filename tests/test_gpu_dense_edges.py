@@ -258,6 +258,31 @@ def test_dense_decoder_runs_inside_a_capture():
     assert torch.equal(bits(totals), bits(mass)) and count.tolist() == [n // 4 for n in lens]
 
 
+def test_dense_decoder_branches_off_a_capture():
+    """A step on a stream of its own inside a capture, after calls outside it: a branch that the caller joins."""
+    lens, hq = [700, 333], 4
+    grp = Group(lens, 1, seed=3)
+    dec = qsa.DenseDecoder(grp.cache, hq, 2)
+    q, seqs, pos = queries(2, hq, 1).cuda(), i32([0, 1]), i32([n - 1 for n in lens])
+    side, other = torch.cuda.Stream(), torch.cuda.Stream()
+    out, lse = (x.clone() for x in dec.run(q, seqs, pos))
+    dec.run(q, seqs, pos, stream=other)
+    torch.cuda.synchronize()
+    graph, twice = torch.cuda.CUDAGraph(), torch.empty_like(q)
+    with torch.cuda.graph(graph):
+        twice.copy_(q)
+        dec.run(twice, seqs, pos, stream=side)
+        torch.cuda.current_stream().wait_stream(side)
+        copy = dec.out.clone()
+    dec.out.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(bits(copy), bits(out)) and torch.equal(bits(dec.lse), bits(lse))
+    dec.run(q, seqs, pos)
+    torch.cuda.synchronize()
+    assert torch.equal(bits(dec.out), bits(out))
+
+
 def test_dense_decoder_keeps_a_side_streams_inputs():
     """Inputs that the caller lets go of right after a call on a side stream are not handed out again before it ran."""
     lens, hq = [900, 640], 8
